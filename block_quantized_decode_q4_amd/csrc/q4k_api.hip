@@ -645,6 +645,95 @@ int f16_gemm_checks(const void* w16, const void* x16, const float* y, int64_t m,
     return Q4K_OK;
 }
 
+// ------------------------------------------- around a layer's projections
+constexpr int64_t kMaxRows = ((int64_t)1 << 22) - 1; // rows and positions of a call: one
+                                                     // workgroup of 1024 each fits a launch
+
+// A launch has fewer than 2^32 threads (the runtime's limit).
+inline bool fits_launch(int64_t blocks, int64_t threads)
+{
+    return blocks >= 1 && blocks <= kInt32Max && blocks * threads < ((int64_t)1 << 32);
+}
+
+inline bool known_type(int t)
+{
+    return t == Q4K_F32 || t == Q4K_F16 || t == Q4K_BF16;
+}
+
+inline bool in_range(int64_t v, int64_t lo, int64_t hi)
+{
+    return v >= lo && v <= hi;
+}
+
+// The shape rules of the grouping (ids of n_experts groups, topk per token)
+int check_group_shape(int64_t slots, int64_t groups, int64_t topk)
+{
+    if (!in_range(groups, 1, q4k::kMaxGroups) || !in_range(topk, 1, q4k::kMaxTopk) ||
+        topk > groups || !in_range(slots, 1, kMaxRows)) {
+        return Q4K_ERR_SHAPE;
+    }
+    return Q4K_OK;
+}
+
+// Grouped rows: pointers, counts and the index arrays' alignment (NULL, an
+// optional array that is not given, is aligned)
+int check_group_rows(const int32_t* offsets, const int32_t* x_rows, const int32_t* y_rows,
+                     int64_t n, int64_t groups, int64_t rows, int64_t x_div, int64_t x_count,
+                     int64_t y_count, q4k::GroupRows* out)
+{
+    if (!offsets) {
+        return Q4K_ERR_NULL;
+    }
+    if (n < 1 || n > kInt32Max || !in_range(groups, 1, kMaxRows) || !in_range(rows, 1, kMaxRows) ||
+        !in_range(x_div, 1, kMaxRows) || !in_range(x_count, 1, kMaxRows) ||
+        !in_range(y_count, 1, kMaxRows)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(offsets) || !aligned16(x_rows) || !aligned16(y_rows)) {
+        return Q4K_ERR_ALIGN;
+    }
+    out->offsets = offsets;
+    out->x_rows = x_rows;
+    out->y_rows = y_rows;
+    out->groups = (int)groups;
+    out->rows = (int)rows;
+    out->x_div = (int)x_div;
+    out->x_count = (int)x_count;
+    out->y_count = (int)y_count;
+    return Q4K_OK;
+}
+
+int gemv_grouped_checked(const void* w, const float* x, const int8_t* q, const float* d, float* y,
+                         q4k::GroupRows& g, int64_t n, int64_t k, void* ws, size_t ws_bytes,
+                         void* stream)
+{
+    const int rc = check_nk(n, k);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    if (!fits_launch(q4k::grouped_grid(g.rows, g.groups, n), 512)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(w) || !aligned16(x) || !aligned16(q) || !aligned16(d) || !aligned16(y) ||
+        !aligned16(ws)) {
+        return Q4K_ERR_ALIGN;
+    }
+    if (ws_bytes < q4k::grouped_ws_bytes(k, g.x_count)) {
+        return Q4K_ERR_SIZE;
+    }
+    q4k::GroupedArgs a;
+    a.w = w;
+    a.x = x;
+    a.q = q;
+    a.d = d;
+    a.y = y;
+    a.ws = ws;
+    a.g = g;
+    a.n = (int)n;
+    a.k = (int)k;
+    return hip_status(q4k::launch_grouped(a, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -1035,13 +1124,291 @@ int q4k_f16_gemm_f32x_noalloc(const void* w16, const float* x, float* y, int64_t
     return hip_status(q4k::launch_f16_gemm(w16, xh, y, (int)m, (int)n, (int)k, s));
 }
 
+int q4k_rmsnorm(const void* x, int x_type, int64_t x_stride, const float* residual,
+                const float* weight, float* sum_out, float* y, void* y16, int8_t* q, float* d,
+                int64_t k, int64_t m, float eps, void* stream)
+{
+    if (!x || !weight || (!sum_out && !y && !y16 && !q) || (q == nullptr) != (d == nullptr)) {
+        return Q4K_ERR_NULL;
+    }
+    const int64_t stride = x_stride == 0 ? k : x_stride;
+    if (!in_range(m, 1, kMaxRows) || k < 1 || k > kInt32Max || stride < k ||
+        stride > ((int64_t)1 << 40) || (q && k % 32 != 0) || !(eps >= 0.f) ||
+        !__builtin_isfinite(eps) || !fits_launch(m, k > 8192 ? 1024 : (k / 8 + 64) / 64 * 64)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!known_type(x_type)) {
+        return Q4K_ERR_UNSUPPORTED;
+    }
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(residual) ||
+        !aligned16(sum_out) || !aligned16(y) || !aligned16(y16) ||
+        !aligned16(q) || !aligned16(d)) {
+        return Q4K_ERR_ALIGN;
+    }
+    q4k::NormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.sum = sum_out;
+    a.y = y;
+    a.y16 = y16;
+    a.q = q;
+    a.d = d;
+    a.x_stride = stride;
+    a.x_type = x_type;
+    a.k = (int)k;
+    a.m = (int)m;
+    a.eps = eps;
+    return hip_status(q4k::launch_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t q4k_moe_group_ws(int64_t slots, int64_t groups, int64_t topk)
+{
+    if (check_group_shape(slots, groups, topk) != Q4K_OK) {
+        return 0;
+    }
+    return q4k::group_ws_bytes(slots, groups, topk);
+}
+
+int q4k_moe_route(const float* logits, int64_t logits_stride, int32_t* ids, float* weights,
+                  int32_t* offsets, int32_t* order, int64_t n_experts, int64_t topk, int renorm,
+                  int64_t m, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!logits || !ids || !weights || (offsets == nullptr) != (order == nullptr)) {
+        return Q4K_ERR_NULL;
+    }
+    if (!in_range(m, 1, kMaxRows) || !in_range(topk, 1, q4k::kMaxTopk)) {
+        return Q4K_ERR_SHAPE;
+    }
+    const int rc = check_group_shape(m * topk, n_experts, topk);
+    const int64_t stride = logits_stride == 0 ? n_experts : logits_stride;
+    if (rc != Q4K_OK || stride < n_experts || stride > ((int64_t)1 << 40)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) ||
+        !aligned16(offsets) || !aligned16(order) || !aligned16(ws)) {
+        return Q4K_ERR_ALIGN;
+    }
+    if (offsets) {
+        const size_t need = q4k::group_ws_bytes(m * topk, n_experts, topk);
+        if (need && !ws) {
+            return Q4K_ERR_NULL;
+        }
+        if (need > ws_bytes) {
+            return Q4K_ERR_SIZE;
+        }
+    }
+    q4k::RouteArgs a = {};
+    a.logits = logits;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.order = order;
+    a.counts = static_cast<int*>(ws);
+    a.stride = stride;
+    a.m = (int)m;
+    a.groups = (int)n_experts;
+    a.topk = (int)topk;
+    a.renorm = renorm != 0;
+    a.slots = (int)(m * topk);
+    return hip_status(q4k::launch_route(a, static_cast<hipStream_t>(stream)));
+}
+
+int q4k_moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, int64_t count,
+                  int64_t groups, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!ids || !offsets || !order) {
+        return Q4K_ERR_NULL;
+    }
+    const int rc = check_group_shape(count, groups, 1);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    if (!aligned16(ids) || !aligned16(offsets) || !aligned16(order) || !aligned16(ws)) {
+        return Q4K_ERR_ALIGN;
+    }
+    const size_t need = q4k::group_ws_bytes(count, groups, 1);
+    if (need && !ws) {
+        return Q4K_ERR_NULL;
+    }
+    if (need > ws_bytes) {
+        return Q4K_ERR_SIZE;
+    }
+    q4k::RouteArgs a = {};
+    a.ids = const_cast<int32_t*>(ids);               // read only without logits
+    a.offsets = offsets;
+    a.order = order;
+    a.counts = static_cast<int*>(ws);
+    a.m = (int)count;
+    a.groups = (int)groups;
+    a.topk = 1;
+    a.slots = (int)count;
+    return hip_status(q4k::launch_route(a, static_cast<hipStream_t>(stream)));
+}
+
+int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
+                    const float* residual, float* out, int64_t n, int64_t topk, int64_t m,
+                    void* stream)
+{
+    if (!y || !weights || !out) {
+        return Q4K_ERR_NULL;
+    }
+    if (n < 1 || n > kInt32Max / 2 || !in_range(topk, 1, q4k::kMaxTopk) ||
+        !in_range(m, 1, kMaxRows) ||
+        !fits_launch(m * (n % 4 == 0 ? (n + 1023) / 1024 : (n + 255) / 256), 256)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(y) || !aligned16(weights) || !aligned16(out) || !aligned16(ids) ||
+        !aligned16(residual)) {
+        return Q4K_ERR_ALIGN;
+    }
+    q4k::CombineArgs a = {};
+    a.y = y;
+    a.weights = weights;
+    a.ids = ids;
+    a.residual = residual;
+    a.out = out;
+    a.n = (int)n;
+    a.topk = (int)topk;
+    a.m = (int)m;
+    return hip_status(q4k::launch_combine(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t q4k_gemv_grouped_ws(int64_t k, int64_t x_count)
+{
+    if (check_nk(1, k) != Q4K_OK || !in_range(x_count, 1, kMaxRows)) {
+        return 0;
+    }
+    return q4k::grouped_ws_bytes(k, x_count);
+}
+
+int q4k_gemv_grouped(const void* w, const float* x, float* y, const int32_t* offsets,
+                     const int32_t* x_rows, const int32_t* y_rows, int64_t n, int64_t k,
+                     int64_t groups, int64_t rows, int64_t x_div, int64_t x_count,
+                     int64_t y_count, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!w || !x || !y || !ws) {
+        return Q4K_ERR_NULL;
+    }
+    q4k::GroupRows g;
+    const int rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count,
+                                    y_count, &g);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    return gemv_grouped_checked(w, x, nullptr, nullptr, y, g, n, k, ws, ws_bytes, stream);
+}
+
+int q4k_gemv_grouped_q8(const void* w, const int8_t* q, const float* d, float* y,
+                        const int32_t* offsets, const int32_t* x_rows, const int32_t* y_rows,
+                        int64_t n, int64_t k, int64_t groups, int64_t rows, int64_t x_div,
+                        int64_t x_count, int64_t y_count, void* ws, size_t ws_bytes,
+                        void* stream)
+{
+    if (!w || !q || !d || !y || !ws) {
+        return Q4K_ERR_NULL;
+    }
+    q4k::GroupRows g;
+    const int rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count,
+                                    y_count, &g);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    return gemv_grouped_checked(w, nullptr, q, d, y, g, n, k, ws, ws_bytes, stream);
+}
+
+int q4k_f16_gemm_grouped(const void* w16, const void* x16, float* y, const int32_t* offsets,
+                         const int32_t* x_rows, const int32_t* y_rows, int64_t n, int64_t k,
+                         int64_t groups, int64_t rows, int64_t x_div, int64_t x_count,
+                         int64_t y_count, void* stream)
+{
+    if (!w16 || !x16 || !y) {
+        return Q4K_ERR_NULL;
+    }
+    q4k::GroupRows g;
+    const int rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count,
+                                    y_count, &g);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    if (k < 1 || k > kInt32Max) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (k % 64 != 0) {
+        return Q4K_ERR_UNSUPPORTED;      // the k step of the tile
+    }
+    if (!fits_launch(q4k::f16_grouped_grid(rows, groups, n), 256)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(w16) || !aligned16(x16) || !aligned16(y)) {
+        return Q4K_ERR_ALIGN;
+    }
+    return hip_status(q4k::launch_f16_gemm_grouped(w16, x16, y, g, (int)n, (int)k,
+                                                   static_cast<hipStream_t>(stream)));
+}
+
+size_t q4k_lora_ws(int64_t rows, int64_t r)
+{
+    if (!in_range(rows, 1, kMaxRows) || !in_range(r, 1, 1024)) {
+        return 0;
+    }
+    return q4k::lora_ws_bytes(rows, r);
+}
+
+int q4k_lora(const void* x, int x_type, const void* a, const void* b, const float* base,
+             float* y, const int32_t* ranks, const float* scales, const int32_t* offsets,
+             const int32_t* order, int64_t n, int64_t k, int64_t r, int64_t adapters,
+             int64_t rows, void* ws, size_t ws_bytes, void* stream)
+{
+    if (!x || !a || !b || !y || !offsets || !ws) {
+        return Q4K_ERR_NULL;
+    }
+    if (!in_range(n, 1, kMaxRows) || k < 1 || k > kInt32Max || !in_range(r, 1, 1024) ||
+        !in_range(adapters, 1, kMaxRows) || !in_range(rows, 1, kMaxRows)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!known_type(x_type) || k % 8 != 0) {
+        return Q4K_ERR_UNSUPPORTED;      // 16-byte pieces of a row
+    }
+    if (!aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(base) ||
+        !aligned16(y) || !aligned16(ranks) || !aligned16(scales) ||
+        !aligned16(offsets) || !aligned16(order) || !aligned16(ws)) {
+        return Q4K_ERR_ALIGN;
+    }
+    if (!q4k::lora_fits(rows, adapters, n, r)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (ws_bytes < q4k::lora_ws_bytes(rows, r)) {
+        return Q4K_ERR_SIZE;
+    }
+    q4k::LoraArgs l;
+    l.x = x;
+    l.a = a;
+    l.b = b;
+    l.base = base;
+    l.y = y;
+    l.ranks = ranks;
+    l.scales = scales;
+    l.offsets = offsets;
+    l.order = order;
+    l.v = static_cast<float*>(ws);
+    l.x_type = x_type;
+    l.n = (int)n;
+    l.k = (int)k;
+    l.r = (int)r;
+    l.adapters = (int)adapters;
+    l.rows = (int)rows;
+    return hip_status(q4k::launch_lora(l, static_cast<hipStream_t>(stream)));
+}
+
 const char* q4k_status_string(int rc)
 {
     switch (rc) {
     case Q4K_OK: return "ok";
     case Q4K_ERR_NULL: return "a required pointer is NULL";
     case Q4K_ERR_SHAPE: return "bad shape: need 1 <= n, 256 <= k, k % 256 == 0, 1 <= m, n and k below 2^31";
-    case Q4K_ERR_SIZE: return "byte count does not match n rows of the format (144 or 210 bytes per 256 weights)";
+    case Q4K_ERR_SIZE: return "byte count does not match n rows of the format (144 or 210 bytes per "
+                             "256 weights), or the workspace is too small";
     case Q4K_ERR_ALIGN: return "a pointer, or a Q6_K row stride, is not 16-byte aligned";
     case Q4K_ERR_UNSUPPORTED:
         return "unsupported: m > 32, or launch options that do not fit the shape, m or the "

@@ -28,6 +28,7 @@
 #include <type_traits>
 #include <mutex>
 
+#include "q4k_groups.h"
 #include "q4k_kernels.h"
 
 namespace q4k {
@@ -57,15 +58,15 @@ f16_cvt_kernel(const float* __restrict__ x, _Float16* __restrict__ out, int64_t 
     }
 }
 
-// y[b * n + r] = sum_c w16[r * k + c] x16[b * k + c] (f32 accumulation).
-// Tiles of BM x rows by BN mirror rows (64 or 128 each); four waves in a
-// 2 x 2 layout, each with (BM / 32) x (BN / 32) MFMA blocks of 16 x 16.
-// Grid: kGXcd * ceil(NT / kGXcd) * MT workgroups (MT, NT: tiles of x rows
-// and of mirror rows); k % 64 == 0.
-template <int BM, int BN>
-__global__ void __launch_bounds__(256, 2)
-f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
-                float* __restrict__ y, int m, int n, int k, int MT, int NT)
+// One tile of y: BM x rows by the BN mirror rows from row_w0 on (64 or 128
+// each) over all of k; four waves in a 2 x 2 layout, each with (BM / 32) x
+// (BN / 32) MFMA blocks of 16 x 16.  xrow(i) is where tile row i's x begins
+// (i < BM, readable for every i), put(i, r, v) takes y of tile row i and
+// mirror row r < n.
+template <int BM, int BN, typename XRow, typename Put>
+__device__ __forceinline__ void
+f16_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n, int k,
+         unsigned char* smem)
 {
     static_assert((BM == 64 || BM == 128) && (BN == 64 || BN == 128), "tile");
     constexpr int LA = BM / 32;              // 16-byte loads of the x tile per thread and step
@@ -74,22 +75,9 @@ f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x
     constexpr int FB = BN / 32;
     constexpr int kXs = BM * kGRow;          // LDS bytes of one x tile
     constexpr int kStage = (BM + BN) * kGRow;
-    extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = tid >> 6;
-    // XCD-aware tile order: workgroup b runs on XCD b % 8; within an XCD
-    // the x tiles of one mirror tile follow each other
-    const int bid = blockIdx.x;
-    const int xcd = bid % kGXcd;
-    const int local = bid / kGXcd;
-    const int tm = local % MT;
-    const int tn = (local / MT) * kGXcd + xcd;
-    if (tn >= NT) {
-        return;
-    }
-    const int row_x0 = tm * BM;
-    const int row_w0 = tn * BN;
 
     // load role: 16 bytes of a tile row per thread and load (tile row
     // idx / 8, 16-byte chunk idx % 8 of its 128 bytes)
@@ -99,7 +87,7 @@ f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         const int idx = tid + 256 * i;
-        xsrc[i] = x16 + (int64_t)min(row_x0 + (idx >> 3), m - 1) * k + (idx & 7) * 8;
+        xsrc[i] = xrow(idx >> 3) + (idx & 7) * 8;
         xoff[i] = (idx >> 3) * kGRow + (idx & 7) * 16;
     }
 #pragma unroll
@@ -200,24 +188,97 @@ f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x
             step(kb + 1, std::integral_constant<int, 0>());
         }
     }
-    // D[4 g + r][j] of block (a, b): x row (BM / 2) wm + 16 a + 4 g + r,
+    // D[4 g + r][j] of block (a, b): tile row (BM / 2) wm + 16 a + 4 g + r,
     // mirror row (BN / 2) wn + 16 b + j
 #pragma unroll
     for (int a = 0; a < FA; ++a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int xr = row_x0 + (BM / 2) * wm + 16 * a + 4 * g + r;
-            if (xr < m) {
+            put((BM / 2) * wm + 16 * a + 4 * g + r, [&](auto out) __attribute__((always_inline)) {
 #pragma unroll
                 for (int b = 0; b < FB; ++b) {
                     const int wr = row_w0 + (BN / 2) * wn + 16 * b + j;
                     if (wr < n) {
-                        y[(int64_t)xr * n + wr] = acc[a][b][r];
+                        out(wr, acc[a][b][r]);
                     }
                 }
-            }
+            });
         }
     }
+}
+
+// y[b * n + r] = sum_c w16[r * k + c] x16[b * k + c] (f32 accumulation).
+// Grid: kGXcd * ceil(NT / kGXcd) * MT workgroups (MT, NT: tiles of x rows
+// and of mirror rows); k % 64 == 0.
+template <int BM, int BN>
+__global__ void __launch_bounds__(256, 2)
+f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
+                float* __restrict__ y, int m, int n, int k, int MT, int NT)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    // XCD-aware tile order: workgroup b runs on XCD b % 8; within an XCD
+    // the x tiles of one mirror tile follow each other
+    const int bid = blockIdx.x;
+    const int xcd = bid % kGXcd;
+    const int local = bid / kGXcd;
+    const int tm = local % MT;
+    const int tn = (local / MT) * kGXcd + xcd;
+    if (tn >= NT) {
+        return;
+    }
+    const int row_x0 = tm * BM;
+    f16_tile<BM, BN>(
+        w16, [&](int i) { return x16 + (int64_t)min(row_x0 + i, m - 1) * k; },
+        [&](int i, auto each) {
+            if (row_x0 + i < m) {
+                float* const out = y + (int64_t)(row_x0 + i) * n;
+                each([&](int r, float v) { out[r] = v; });
+            }
+        },
+        tn * BN, n, k, smem);
+}
+
+// The same product for rows grouped by matrix: tile tm holds up to BM
+// positions of one group (MT: the most tiles there can be), its mirror is the
+// group's.  Positions that are left out read x row 0 and are not written.
+template <int BM, int BN>
+__global__ void __launch_bounds__(256, 2)
+f16_gemm_grouped_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
+                        float* __restrict__ y, GroupRows rows, int n, int k, int MT, int NT)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int bid = blockIdx.x;
+    const int xcd = bid % kGXcd;
+    const int local = bid / kGXcd;
+    const int tn = (local / MT) * kGXcd + xcd;
+    if (tn >= NT) {
+        return;
+    }
+    const GroupTile t = find_tile<BM>(rows.offsets, rows.groups, rows.rows, local % MT);
+    if (t.count == 0) {
+        return;
+    }
+    auto x_row = [&](int i) -> int {            // -1: left out
+        if (i >= t.count) {
+            return -1;
+        }
+        const int p = t.begin + i;
+        const int r = rows.x_rows ? rows.x_rows[p] : p;
+        return r < 0 || r / rows.x_div >= rows.x_count ? -1 : r / rows.x_div;
+    };
+    f16_tile<BM, BN>(
+        w16 + (int64_t)t.group * n * k,
+        [&](int i) { return x16 + (int64_t)max(x_row(i), 0) * k; },
+        [&](int i, auto each) {
+            if (x_row(i) >= 0) {
+                const int r = rows.y_rows ? rows.y_rows[t.begin + i] : t.begin + i;
+                if (r >= 0 && r < rows.y_count) {
+                    float* const out = y + (int64_t)r * n;
+                    each([&](int c, float v) { out[c] = v; });
+                }
+            }
+        },
+        tn * BN, n, k, smem);
 }
 
 hipError_t launch_f16_cvt(const float* x, void* out, int64_t count, hipStream_t stream)
@@ -284,6 +345,51 @@ hipError_t launch_f16_gemm(const void* w16, const void* x16, float* y, int m, in
         return launch_f16_gemm_t<64, 128>(w16, x16, y, m, n, k, stream);
     }
     return launch_f16_gemm_t<64, 64>(w16, x16, y, m, n, k, stream);
+}
+
+// The grouped product's tile: 128 positions where the groups hold about that
+// many, else 64 (a tile never spans groups); 128 mirror rows while that gives
+// a tile for every CU.
+void f16_grouped_tile(int64_t rows, int64_t groups, int64_t n, int* bm, int* bn)
+{
+    *bm = rows >= 96 * groups ? 128 : 64;
+    *bn = most_tiles(rows, groups, *bm) * ((n + 127) / 128) >= 256 ? 128 : 64;
+    *bm = *bn == 64 ? 64 : *bm;
+}
+
+int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n)
+{
+    int bm, bn;
+    f16_grouped_tile(rows, groups, n, &bm, &bn);
+    const int64_t NT = (n + bn - 1) / bn;
+    return kGXcd * ((NT + kGXcd - 1) / kGXcd) * most_tiles(rows, groups, bm);
+}
+
+template <int BM, int BN>
+static hipError_t launch_f16_grouped_t(const void* w16, const void* x16, float* y,
+                                       const GroupRows& g, int n, int k, hipStream_t stream)
+{
+    const int MT = (int)most_tiles(g.rows, g.groups, BM);
+    const int NT = (n + BN - 1) / BN;
+    const int64_t grid = (int64_t)kGXcd * ((NT + kGXcd - 1) / kGXcd) * MT;
+    hipLaunchKernelGGL((f16_gemm_grouped_kernel<BM, BN>), dim3((unsigned)grid), dim3(256),
+                       f16_gemm_lds_bytes(BM, BN), stream, static_cast<const _Float16*>(w16),
+                       static_cast<const _Float16*>(x16), y, g, n, k, MT, NT);
+    return hipGetLastError();
+}
+
+hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
+                                   int n, int k, hipStream_t stream)
+{
+    int bm, bn;
+    f16_grouped_tile(g.rows, g.groups, n, &bm, &bn);
+    if (bm == 128) {
+        return launch_f16_grouped_t<128, 128>(w16, x16, y, g, n, k, stream);
+    }
+    if (bn == 128) {
+        return launch_f16_grouped_t<64, 128>(w16, x16, y, g, n, k, stream);
+    }
+    return launch_f16_grouped_t<64, 64>(w16, x16, y, g, n, k, stream);
 }
 
 // ------------------------------------------------- allocation-free variant

@@ -98,4 +98,107 @@ hipError_t f16_scratch(void** out);
 size_t f16_gemm_lds_bytes(int bm, int bn);
 int64_t f16_gemm_grid(int64_t m, int64_t n);
 
+// The types of the activations that q4k_rmsnorm and q4k_lora take (enum
+// q4k_type of include/q4k.h).
+constexpr int kTypeF32 = 0;
+constexpr int kTypeF16 = 1;
+constexpr int kTypeBF16 = 2;
+
+// The norm (q4k_norm.hip): m rows of k elements; any output may be null.
+struct NormArgs {
+    const void* x;
+    const float* residual;
+    const float* weight;
+    float* sum;
+    float* y;
+    void* y16;
+    int8_t* q;
+    float* d;
+    int64_t x_stride;
+    int x_type, k, m;
+    float eps;
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// Routing and grouping (q4k_moe.hip).  logits null: the ids are given.
+constexpr int kFewSlots = 512;         // slots that one workgroup groups in one launch
+constexpr int kMaxGroups = 1024;       // experts (ids) that routing and grouping take
+constexpr int kMaxTopk = 32;
+struct RouteArgs {
+    const float* logits;
+    int* ids;
+    float* weights;
+    int* offsets;                      // null: no grouping
+    int* order;
+    int* counts;                       // chunks x groups (workspace)
+    int64_t stride;                    // floats from one token's logits to the next
+    int64_t chunk;                     // slots per chunk (set by the launch)
+    int chunks;
+    int m, groups, topk, renorm;
+    int slots;                         // m * topk
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk);
+
+struct CombineArgs {
+    const float* y;
+    const float* weights;
+    const int* ids;                    // null: every slot counts
+    const float* residual;             // may be null
+    float* out;
+    int n, topk, m;
+    int parts;                         // workgroups per token (set by the launch)
+};
+hipError_t launch_combine(CombineArgs a, hipStream_t stream);
+
+// Rows grouped by a matrix: position i (offsets[g] <= i < offsets[g + 1])
+// takes x row (x_rows ? x_rows[i] : i) / x_div and writes y row
+// (y_rows ? y_rows[i] : i); a position whose row is outside 0 .. x_count - 1
+// or 0 .. y_count - 1 is left out.
+struct GroupRows {
+    const int* offsets;
+    const int* x_rows;
+    const int* y_rows;
+    int groups, rows;
+    int x_div, x_count, y_count;
+};
+
+// Q4_K matrices (q4k_grouped.hip): x f32, or (x null) Q8 codes and scales.
+struct GroupedArgs {
+    const void* w;
+    const float* x;
+    const int8_t* q;
+    const float* d;
+    float* y;
+    void* ws;
+    GroupRows g;
+    int n, k;
+};
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
+size_t grouped_ws_bytes(int64_t k, int64_t x_count);
+int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n);
+
+// The fp16 mirror (q4k_f16.hip).
+hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
+                                   int n, int k, hipStream_t stream);
+int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n);
+
+// Low-rank adapters (q4k_lora.hip).
+struct LoraArgs {
+    const void* x;
+    const void* a;                     // adapters x r x k halves
+    const void* b;                     // adapters x n x r halves
+    const float* base;                 // null: y is overwritten with the product alone
+    float* y;
+    const int* ranks;                  // null: r
+    const float* scales;               // null: 1
+    const int* offsets;
+    const int* order;                  // null: position i is row i
+    float* v;                          // rows x r (workspace)
+    int x_type, n, k, r, adapters, rows;
+};
+hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
+size_t lora_ws_bytes(int64_t rows, int64_t r);
+bool lora_fits(int64_t rows, int64_t adapters, int64_t n, int64_t r);    // the launch limits
+
 }  // namespace q4k

@@ -23,6 +23,10 @@ Q4K_ERR_ALIGN = 4
 Q4K_ERR_UNSUPPORTED = 5
 Q4K_ERR_HIP = 1000
 
+Q4K_F32 = 0
+Q4K_F16 = 1
+Q4K_BF16 = 2
+
 # every symbol include/q4k.h declares
 EXPORTED = (
     "q4k_row_bytes",
@@ -48,6 +52,17 @@ EXPORTED = (
     "q4k_f16_gemm",
     "q4k_f16_gemm_f32x",
     "q4k_f16_gemm_f32x_noalloc",
+    "q4k_rmsnorm",
+    "q4k_moe_group_ws",
+    "q4k_moe_route",
+    "q4k_moe_group",
+    "q4k_moe_combine",
+    "q4k_gemv_grouped_ws",
+    "q4k_gemv_grouped",
+    "q4k_gemv_grouped_q8",
+    "q4k_f16_gemm_grouped",
+    "q4k_lora_ws",
+    "q4k_lora",
 )
 
 
@@ -175,6 +190,26 @@ def load_library():
         lib.q4k_plan.argtypes = [i64, i64, i64, ctypes.POINTER(q4k_launch), ctypes.c_int,
                                  ctypes.c_size_t, ctypes.POINTER(q4k_plan_info)]
         lib.q4k_plan.restype = ctypes.c_int
+        ci = ctypes.c_int
+        sz = ctypes.c_size_t
+        grouped = [vp, vp, vp, i64, i64, i64, i64, i64, i64, i64]   # offsets .. y_count
+        for name, args, res in (
+                ("q4k_rmsnorm", [vp, ci, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64,
+                                 ctypes.c_float, vp], ci),
+                ("q4k_moe_group_ws", [i64, i64, i64], sz),
+                ("q4k_moe_route", [vp, i64, vp, vp, vp, vp, i64, i64, ci, i64, vp, sz, vp], ci),
+                ("q4k_moe_group", [vp, vp, vp, i64, i64, vp, sz, vp], ci),
+                ("q4k_moe_combine", [vp, vp, vp, vp, vp, i64, i64, i64, vp], ci),
+                ("q4k_gemv_grouped_ws", [i64, i64], sz),
+                ("q4k_gemv_grouped", [vp, vp, vp] + grouped + [vp, sz, vp], ci),
+                ("q4k_gemv_grouped_q8", [vp, vp, vp, vp] + grouped + [vp, sz, vp], ci),
+                ("q4k_f16_gemm_grouped", [vp, vp, vp] + grouped + [vp], ci),
+                ("q4k_lora_ws", [i64, i64], sz),
+                ("q4k_lora", [vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp,
+                              sz, vp], ci)):
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = res
         _lib = lib
         return lib
 
@@ -362,6 +397,223 @@ def q4k_f16_gemm_f32x_noalloc(w16, x, y, m: int, n: int, k: int, stream=None) ->
     _check(load_library().q4k_f16_gemm_f32x_noalloc(_addr(w16), _addr(x), _addr(y), int(m),
                                                     int(n), int(k), _stream(stream)),
            "q4k_f16_gemm_f32x_noalloc")
+
+
+# ---------------------------------------- around a layer's projections
+# These run where their tensors live: ``stream=None`` is torch's current
+# stream of the first tensor's device, made current for the call when it is
+# not, and a tensor on another device is refused.
+class _Call:
+    """Addresses, stream and device of one call."""
+
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def at(self, a, kind=None, count=None):
+        """Address of a (None passes through); a tensor is checked to be dense,
+        on the call's device, of the element type `kind` and to hold at least
+        `count` elements."""
+        if a is None or isinstance(a, int):
+            return a
+        if not hasattr(a, "data_ptr"):
+            return _addr(a)
+        if not a.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        device = a.device
+        if device.type != "cuda":
+            raise ValueError("expected a tensor on the GPU, got one on %s" % device)
+        if self.device is None:
+            self.device = device
+        elif device != self.device:
+            raise ValueError("tensors on %s and %s in one call" % (self.device, device))
+        if kind is not None and str(a.dtype) not in kind:
+            raise TypeError("expected %s, got %s" % (" or ".join(kind), a.dtype))
+        if count is not None and a.numel() < count:
+            raise ValueError("a tensor of %d elements where %d are needed" % (a.numel(), count))
+        return a.data_ptr()
+
+    def run(self, fn, where, stream, *args):
+        import torch
+        if self.device is None:
+            rc = fn(*args, _stream(stream))
+        else:
+            index = self.device.index
+            s = torch.cuda.current_stream(index).cuda_stream if stream is None else _stream(stream)
+            if index == torch.cuda.current_device():
+                rc = fn(*args, s)
+            else:
+                with torch.cuda.device(index):
+                    rc = fn(*args, s)
+        if rc != Q4K_OK:
+            raise Q4KError(rc, where)
+
+
+_F32 = ("torch.float32",)
+_F16 = ("torch.float16",)
+_I8 = ("torch.int8",)
+_I32 = ("torch.int32",)
+_U8 = ("torch.uint8", "torch.int8")
+_TYPE_OF = {"torch.float32": Q4K_F32, "torch.float16": Q4K_F16, "torch.bfloat16": Q4K_BF16}
+
+
+def _act_type(x, x_type):
+    """The q4k_type of x: given, or its tensor's."""
+    if x_type is not None:
+        return int(x_type)
+    if hasattr(x, "data_ptr"):
+        t = _TYPE_OF.get(str(x.dtype))
+        if t is None:
+            raise TypeError("expected f32, f16 or bf16 activations, got %s" % x.dtype)
+        return t
+    return Q4K_F32
+
+
+def _ws_bytes(ws, ws_bytes):
+    if ws_bytes is not None:
+        return int(ws_bytes)
+    if ws is None:
+        return 0
+    return ws.numel() * ws.element_size() if hasattr(ws, "numel") else 0
+
+
+def q4k_rmsnorm(x, weight, k: int, m: int = 1, *, eps: float = 1e-5, residual=None, sum_out=None,
+                y=None, y16=None, q=None, d=None, x_stride: int = 0, x_type=None,
+                stream=None) -> None:
+    """h = x + residual, y = h * weight / sqrt(mean h^2 + eps) for m rows of
+    k: h to sum_out, y to any of y (f32), y16 (f16) and q, d (Q8 codes and
+    scales); asynchronous on stream."""
+    c = _Call()
+    mk = m * k
+    if hasattr(x, "data_ptr") and x_stride:
+        # a view with strided rows: its elements need not be dense
+        need = (m - 1) * x_stride + k
+        if x.untyped_storage().nbytes() // x.element_size() - x.storage_offset() < need:
+            raise ValueError("x does not hold %d rows at stride %d" % (m, x_stride))
+        if x.device.type != "cuda":
+            raise ValueError("expected a tensor on the GPU, got one on %s" % x.device)
+        c.device = x.device
+        xa = x.data_ptr()
+    else:
+        xa = c.at(x, None, mk)
+    c.run(load_library().q4k_rmsnorm, "q4k_rmsnorm", stream, xa, _act_type(x, x_type),
+          int(x_stride), c.at(residual, _F32, mk), c.at(weight, _F32, k), c.at(sum_out, _F32, mk),
+          c.at(y, _F32, mk), c.at(y16, _F16, mk), c.at(q, _I8, mk), c.at(d, _F32, mk // 32), int(k),
+          int(m), float(eps))
+
+
+def q4k_moe_group_ws(slots: int, groups: int, topk: int = 1) -> int:
+    """Bytes of workspace of q4k_moe_group and q4k_moe_route."""
+    return int(load_library().q4k_moe_group_ws(int(slots), int(groups), int(topk)))
+
+
+def q4k_moe_route(logits, ids, weights, n_experts: int, topk: int, m: int = 1, *,
+                  renorm: bool = True, offsets=None, order=None, ws=None, ws_bytes=None,
+                  logits_stride: int = 0, stream=None) -> None:
+    """The topk experts of m tokens (ids, softmax weights) and, with offsets
+    and order, their slots grouped by expert; asynchronous on stream."""
+    c = _Call()
+    slots = m * topk
+    span = (m - 1) * (logits_stride or n_experts) + n_experts
+    c.run(load_library().q4k_moe_route, "q4k_moe_route", stream, c.at(logits, _F32, span),
+          int(logits_stride), c.at(ids, _I32, slots), c.at(weights, _F32, slots),
+          c.at(offsets, _I32, n_experts + 1), c.at(order, _I32, slots), int(n_experts), int(topk),
+          1 if renorm else 0, int(m), c.at(ws), _ws_bytes(ws, ws_bytes))
+
+
+def q4k_moe_group(ids, offsets, order, count: int, groups: int, *, ws=None, ws_bytes=None,
+                  stream=None) -> None:
+    """Slots grouped by id (order), and where each group begins (offsets);
+    asynchronous on stream."""
+    c = _Call()
+    c.run(load_library().q4k_moe_group, "q4k_moe_group", stream, c.at(ids, _I32, count),
+          c.at(offsets, _I32, groups + 1), c.at(order, _I32, count), int(count), int(groups),
+          c.at(ws), _ws_bytes(ws, ws_bytes))
+
+
+def q4k_moe_combine(y, weights, ids, out, n: int, topk: int, m: int = 1, *, residual=None,
+                    stream=None) -> None:
+    """out[t] = residual[t] + sum_j weights[t][j] y[t * topk + j] over the
+    choices with an id (ids None: all); asynchronous on stream."""
+    c = _Call()
+    c.run(load_library().q4k_moe_combine, "q4k_moe_combine", stream, c.at(y, _F32, m * topk * n),
+          c.at(weights, _F32, m * topk), c.at(ids, _I32, m * topk), c.at(residual, _F32, m * n),
+          c.at(out, _F32, m * n), int(n), int(topk), int(m))
+
+
+def _grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count):
+    return (c.at(offsets, _I32, groups + 1), c.at(x_rows, _I32, rows), c.at(y_rows, _I32, rows),
+            int(n), int(k), int(groups), int(rows), int(x_div), int(x_count), int(y_count))
+
+
+def q4k_gemv_grouped_ws(k: int, x_count: int) -> int:
+    """Bytes of workspace of q4k_gemv_grouped and q4k_gemv_grouped_q8."""
+    return int(load_library().q4k_gemv_grouped_ws(int(k), int(x_count)))
+
+
+def q4k_gemv_grouped(w, x, y, offsets, n: int, k: int, groups: int, rows: int, *, x_rows=None,
+                     x_div: int = 1, x_count=None, y_rows=None, y_count=None, ws=None,
+                     ws_bytes=None, stream=None) -> None:
+    """Position p of group g: y[y_rows[p]] = W_g x[x_rows[p] // x_div], W_g
+    in Q4_K, x f32 (counts default to rows); asynchronous on stream."""
+    c = _Call()
+    x_count = rows if x_count is None else x_count
+    y_count = rows if y_count is None else y_count
+    c.run(load_library().q4k_gemv_grouped, "q4k_gemv_grouped", stream,
+          c.at(w, _U8, groups * n * (k // 256) * 144), c.at(x, _F32, x_count * k),
+          c.at(y, _F32, y_count * n),
+          *_grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count),
+          c.at(ws), _ws_bytes(ws, ws_bytes))
+
+
+def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: int, *,
+                        x_rows=None, x_div: int = 1, x_count=None, y_rows=None, y_count=None,
+                        ws=None, ws_bytes=None, stream=None) -> None:
+    """q4k_gemv_grouped with x in Q8: codes q (int8) and scales d (f32, one
+    per 32); asynchronous on stream."""
+    c = _Call()
+    x_count = rows if x_count is None else x_count
+    y_count = rows if y_count is None else y_count
+    c.run(load_library().q4k_gemv_grouped_q8, "q4k_gemv_grouped_q8", stream,
+          c.at(w, _U8, groups * n * (k // 256) * 144), c.at(q, _I8, x_count * k),
+          c.at(d, _F32, x_count * (k // 32)), c.at(y, _F32, y_count * n),
+          *_grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count),
+          c.at(ws), _ws_bytes(ws, ws_bytes))
+
+
+def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows: int, *,
+                         x_rows=None, x_div: int = 1, x_count=None, y_rows=None, y_count=None,
+                         stream=None) -> None:
+    """q4k_gemv_grouped on fp16 mirrors (groups * n x k halves) and fp16 x, on
+    the matrix cores; asynchronous on stream."""
+    c = _Call()
+    x_count = rows if x_count is None else x_count
+    y_count = rows if y_count is None else y_count
+    c.run(load_library().q4k_f16_gemm_grouped, "q4k_f16_gemm_grouped", stream,
+          c.at(w16, None, groups * n * k), c.at(x16, None, x_count * k),
+          c.at(y, _F32, y_count * n),
+          *_grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count))
+
+
+def q4k_lora_ws(rows: int, r: int) -> int:
+    """Bytes of workspace of q4k_lora."""
+    return int(load_library().q4k_lora_ws(int(rows), int(r)))
+
+
+def q4k_lora(x, a, b, y, offsets, order, n: int, k: int, r: int, adapters: int, rows: int, *,
+             base=None, ranks=None, scales=None, ws=None, ws_bytes=None, x_type=None,
+             stream=None) -> None:
+    """y[row] = base[row] + scales[a] B_a (A_a x[row]) for the rows of each
+    adapter a (a: adapters x r x k, b: adapters x n x r, both f16; offsets and
+    order as q4k_moe_group gives them); asynchronous on stream."""
+    c = _Call()
+    c.run(load_library().q4k_lora, "q4k_lora", stream, c.at(x, None, rows * k),
+          _act_type(x, x_type), c.at(a, _F16, adapters * r * k), c.at(b, _F16, adapters * n * r),
+          c.at(base, _F32, rows * n), c.at(y, _F32, rows * n), c.at(ranks, _I32, adapters),
+          c.at(scales, _F32, adapters), c.at(offsets, _I32, adapters + 1),
+          c.at(order, _I32, rows), int(n), int(k), int(r), int(adapters), int(rows), c.at(ws),
+          _ws_bytes(ws, ws_bytes))
 
 
 def q4k_read_calibrate_blocks() -> int:

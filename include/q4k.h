@@ -65,7 +65,8 @@ enum q4k_status {
     Q4K_OK = 0,
     Q4K_ERR_NULL = 1,        /* a required pointer is NULL                       */
     Q4K_ERR_SHAPE = 2,       /* n < 1, k < 256, k % 256 != 0, m < 1, or too big  */
-    Q4K_ERR_SIZE = 3,        /* byte count does not match n rows of the format   */
+    Q4K_ERR_SIZE = 3,        /* byte count does not match n rows of the format,
+                                or a workspace is too small                     */
     Q4K_ERR_ALIGN = 4,       /* a pointer (or a Q6_K row stride) is not 16-byte
                                 aligned                                         */
     Q4K_ERR_UNSUPPORTED = 5, /* m > 32; 9-32 vectors where the one-pass
@@ -381,6 +382,174 @@ int q4k_f16_gemm_f32x(const void* w16, const float* x, void* xh, float* y, int64
  * and must be serialised by the caller.  Asynchronous on `stream`. */
 int q4k_f16_gemm_f32x_noalloc(const void* w16, const float* x, float* y, int64_t m, int64_t n,
                               int64_t k, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Around the projections of a decoder layer: the norm that makes their
+ * activations, the routing of tokens to experts, the experts' products and
+ * their weighted sum, and low-rank adapters beside a shared projection.
+ *  - Every tensor is row-major and dense unless a stride is given; device
+ *    pointers are 16-byte aligned (an optional one may be NULL).
+ *  - A workspace is the caller's, `ws_bytes` long; the *_ws function of the
+ *    call gives the bytes it needs (Q4K_ERR_SIZE when there are fewer).  Calls
+ *    that may run at the same time need workspaces of their own, captured
+ *    graphs included.  Its contents mean nothing between calls.
+ *  - Rows and positions number fewer than 2^22 (Q4K_ERR_SHAPE beyond), and a
+ *    launch fewer than 2^32 threads.
+ * ------------------------------------------------------------------- */
+
+/* Types of activations. */
+enum q4k_type {
+    Q4K_F32 = 0,
+    Q4K_F16 = 1,
+    Q4K_BF16 = 2
+};
+
+/* The root-mean-square norm with the residual's addition:
+ *   h = x + residual  (f32, rounded once; h = x when residual is NULL)
+ *   y = h * weight / sqrt(sum h^2 / k + eps)  per row of k elements
+ *  x        : device, m rows of k elements of x_type, x_stride elements from
+ *             row to row (0 = k; at least k otherwise)
+ *  residual : device, m x k f32, or NULL
+ *  weight   : device, k f32
+ *  sum_out  : device, m x k f32, gets h; NULL = not kept.  May be residual
+ *             itself (the residual stream updated in place), or x when x is
+ *             f32 and dense; no other output may overlap an input
+ *  y, y16   : device, m x k f32 / binary16 (nearest even of the f32 y); NULL
+ *             = not wanted
+ *  q, d     : device, m x k int8 codes and m x (k/32) f32 scales, exactly
+ *             what q4k_quantize_q8 writes for the f32 y; both or neither,
+ *             k % 32 == 0
+ * At least one output.  m, k >= 1, eps >= 0 and finite (Q4K_ERR_SHAPE).  Sums
+ * and products in f64, y rounded once to f32 (within 2^-23 |y| of the exact
+ * value).  A row with an infinity gives NaN there and 0 elsewhere, a row with
+ * a NaN gives NaN; a row of zeros with eps = 0 gives NaN.  Asynchronous on
+ * `stream`; allocates nothing. */
+int q4k_rmsnorm(const void* x, int x_type, int64_t x_stride, const float* residual,
+                const float* weight, float* sum_out, float* y, void* y16, int8_t* q, float* d,
+                int64_t k, int64_t m, float eps, void* stream);
+
+/* Bytes of workspace of q4k_moe_group for `slots` ids of `groups` groups and
+ * (slots = m * topk) of q4k_moe_route; 0 for few slots (ws may be NULL
+ * then) and for arguments that the calls refuse. */
+size_t q4k_moe_group_ws(int64_t slots, int64_t groups, int64_t topk);
+
+/* The experts of m tokens.
+ *  logits  : device, m rows of n_experts f32, logits_stride floats apart (0 =
+ *            n_experts)
+ *  ids     : device, m x topk int32: the topk largest logits' experts, the
+ *            largest first, equal logits in the order of the experts
+ *  weights : device, m x topk f32: exp(l - max) / sum exp(l - max), the sum over
+ *            the chosen experts (renorm nonzero) or over all of them.  Where
+ *            the largest logits are +infinite, they count 1 and others 0
+ *  A NaN or -infinity masks an expert: it is never chosen and not in the
+ *  sum.  Choices that are not there get id -1 and weight 0.
+ *  offsets : device, n_experts + 1 int32, or NULL
+ *  order   : device, m * topk int32, NULL with offsets: the grouping of the
+ *            slots by id, as q4k_moe_group gives it
+ * 1 <= topk <= min(n_experts, 32), n_experts <= 1024, m >= 1.  Workspace:
+ * q4k_moe_group_ws(m * topk, n_experts, topk), none without offsets.
+ * The same input gives the same bits.  Asynchronous; allocates nothing. */
+int q4k_moe_route(const float* logits, int64_t logits_stride, int32_t* ids, float* weights,
+                  int32_t* offsets, int32_t* order, int64_t n_experts, int64_t topk, int renorm,
+                  int64_t m, void* ws, size_t ws_bytes, void* stream);
+
+/* Slots 0 .. count - 1 grouped by their ids: order[offsets[g] ..
+ * offsets[g + 1] - 1] are the slots with id g in slot order; offsets[groups]
+ * of them are in a group.  Ids outside 0 .. groups - 1 are in none, and the
+ * rest of order is -1.
+ *  ids : device, count int32;  offsets : device, groups + 1 int32;
+ *  order : device, count int32.  1 <= groups <= 1024, count >= 1.
+ * Workspace: q4k_moe_group_ws(count, groups, 1).  Asynchronous. */
+int q4k_moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, int64_t count,
+                  int64_t groups, void* ws, size_t ws_bytes, void* stream);
+
+/* out[t][c] = residual[t][c] + sum_j weights[t][j] * y[t*topk + j][c] over the
+ * choices j with ids[t][j] >= 0 (f32, in the order of j, the residual last).
+ *  y : device, m*topk x n f32;  weights : device, m x topk f32
+ *  ids : device, m x topk int32, or NULL (every choice counts); rows of y
+ *        whose id is negative are not read
+ *  residual : device, m x n f32, or NULL;  out : device, m x n f32, may be
+ *        residual
+ * n, m >= 1, 1 <= topk <= 32.  Asynchronous. */
+int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
+                    const float* residual, float* out, int64_t n, int64_t topk, int64_t m,
+                    void* stream);
+
+/* Grouped rows.  Of `rows` positions, group g (of `groups`) holds positions
+ * offsets[g] .. offsets[g + 1] - 1 (device, groups + 1 int32, not decreasing;
+ * cut to 0 .. rows).  Position p multiplies x row
+ *   (x_rows ? x_rows[p] : p) / x_div      of x_count rows
+ * and writes y row
+ *   (y_rows ? y_rows[p] : p)              of y_count rows
+ * (device int32 arrays of `rows` entries).  A position in no group, or with a
+ * row that is negative or at or beyond the count, is left out: nothing is
+ * read or written for it.  Rows of y that no position names stay as they
+ * are.  Two positions must not name the same y row.  The order of
+ * q4k_moe_route serves as x_rows with x_div = topk (x by token: the up
+ * projections) or as y_rows (y by slot: the down projection). */
+
+/* Bytes of workspace of q4k_gemv_grouped and q4k_gemv_grouped_q8 (0 for
+ * arguments that they refuse). */
+size_t q4k_gemv_grouped_ws(int64_t k, int64_t x_count);
+
+/* y[row] = W_g x[row] over grouped rows, W_g n x k in Q4_K (the rows of
+ * q4k_gemv; group g's begin at row g*n of w): the experts' products of a decode
+ * batch.
+ *  w : device, groups*n Q4_K rows;  x : device, x_count x k f32
+ *  y : device, y_count x n f32
+ * 1 <= n, k as for q4k_gemv.  x is carried to 2^-22 of its value or 2^-50 of
+ * its row's largest, the weights' two terms (d sc q and dmin m, times x) are
+ * added up apart in f32: with T = sum (|d sc q| + |dmin m|) |x| and U the same
+ * sum with the row's largest |x| for every x, y is within
+ * (280 + k/128) 2^-23 T + 2^-48 U of the exact value (the bound of f32 sums of
+ * 256 terms; in practice a few 2^-23 of the row's scale).  A row of x with an
+ * infinity or NaN gives NaN or an infinity in all of its y row; other rows
+ * are unaffected.  Asynchronous;
+ * allocates nothing. */
+int q4k_gemv_grouped(const void* w, const float* x, float* y, const int32_t* offsets,
+                     const int32_t* x_rows, const int32_t* y_rows, int64_t n, int64_t k,
+                     int64_t groups, int64_t rows, int64_t x_div, int64_t x_count,
+                     int64_t y_count, void* ws, size_t ws_bytes, void* stream);
+
+/* The same with x in Q8: codes q (device, x_count x k int8) and scales d
+ * (device, x_count x k/32 f32), x = d * q rounded to f32. */
+int q4k_gemv_grouped_q8(const void* w, const int8_t* q, const float* d, float* y,
+                        const int32_t* offsets, const int32_t* x_rows, const int32_t* y_rows,
+                        int64_t n, int64_t k, int64_t groups, int64_t rows, int64_t x_div,
+                        int64_t x_count, int64_t y_count, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* The same on fp16 mirrors, for prompts: w16 device, groups*n x k halves; x16
+ * device, x_count x k halves; k % 64 == 0 (Q4K_ERR_UNSUPPORTED otherwise).
+ * Accuracy as q4k_f16_gemm.  No workspace. */
+int q4k_f16_gemm_grouped(const void* w16, const void* x16, float* y, const int32_t* offsets,
+                         const int32_t* x_rows, const int32_t* y_rows, int64_t n, int64_t k,
+                         int64_t groups, int64_t rows, int64_t x_div, int64_t x_count,
+                         int64_t y_count, void* stream);
+
+/* Bytes of workspace of q4k_lora (0 for arguments that it refuses). */
+size_t q4k_lora_ws(int64_t rows, int64_t r);
+
+/* Low-rank adapters beside a shared projection: y[row] = base[row] +
+ * scales[a] * B_a (A_a x[row]) for the rows of each adapter a.
+ *  x       : device, rows x k elements of x_type
+ *  a       : device, adapters x r x k binary16;  b : device, adapters x n x r
+ *            binary16
+ *  base    : device, rows x n f32 (the shared projection's y), may be y; NULL = 0
+ *  y       : device, rows x n f32; rows of no adapter stay as they are
+ *  ranks   : device, `adapters` int32, the adapters' own ranks (cut to 0 .. r;
+ *            rows of a and columns of b at or beyond it are not read), NULL = r
+ *  scales  : device, `adapters` f32, NULL = 1
+ *  offsets, order : the rows grouped by adapter, as q4k_moe_group gives them
+ *            (order NULL: position p is row p)
+ * n, r, adapters, rows >= 1; r <= 1024; k >= 8, k % 8 == 0
+ * (Q4K_ERR_UNSUPPORTED otherwise).  No operand is rounded, sums are f32, A x
+ * is kept in f32: y is within (k + r + 2) 2^-23 * (|base| + |scale| sum_r |B|
+ * sum_k |A| |x|) of the exact value.  Asynchronous; allocates nothing. */
+int q4k_lora(const void* x, int x_type, const void* a, const void* b, const float* base,
+             float* y, const int32_t* ranks, const float* scales, const int32_t* offsets,
+             const int32_t* order, int64_t n, int64_t k, int64_t r, int64_t adapters,
+             int64_t rows, void* ws, size_t ws_bytes, void* stream);
 
 /* Read `bytes` (a multiple of 16) of device memory at `buf` (16-byte
  * aligned) with coalesced 16-byte loads and write a checksum per workgroup

@@ -1,0 +1,157 @@
+"""GPU parity of q4k_rmsnorm against the norm in f64 (numpy).
+
+h = x + residual is one f32 addition: bit-exact.  y is formed in f64 from f64
+sums and rounded once to f32, so it is within half a step (2^-24 |y|) of the
+exact value, but for f64 rounding: 2^-23 |y| leaves a factor of two (plus the
+smallest subnormal).  y16 rounds that f32 once more: 2^-11 |y| + 2^-23 |y| and
+half the subnormal step 2^-25.  The codes and scales are integer work on the
+f32 y that the same call writes: bit-exact against the oracle's rule.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from block_quantized_decode_q4_amd import q4k  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    q4k.load_library()
+    yield
+
+
+def _ref(h, w, eps):
+    h = h.astype(np.float64)
+    ms = (h * h).sum(1, keepdims=True) / h.shape[1]
+    with np.errstate(all="ignore"):
+        return h * w.astype(np.float64) / np.sqrt(ms + np.float64(np.float32(eps)))
+
+
+def _check(y, ref):
+    ok = np.abs(y.astype(np.float64) - ref) <= 2.0 ** -23 * np.abs(ref) + 2.0 ** -149
+    assert ok.all(), np.argwhere(~ok)[:3]
+
+
+def _run(m, k, kind, residual, q8, seed, stride=0, scale=1.0, eps=1e-5):
+    g = torch.Generator().manual_seed(seed)
+    wide = stride or k
+    xt = (torch.randn((m, wide), generator=g) * scale).to(TYPES[kind])
+    res = torch.randn((m, k), generator=g) * scale if residual else None
+    w = torch.randn(k, generator=g)
+    x_d = xt.cuda()
+    x_d = x_d[:, :k] if stride else x_d
+    w_d = w.cuda()
+    r_d = res.cuda() if residual else None
+    h_d = torch.full((m, k), float("nan"), device="cuda")
+    y_d = torch.full((m, k), float("nan"), device="cuda")
+    y16_d = torch.full((m, k), float("nan"), dtype=torch.float16, device="cuda")
+    q_d = torch.full((m, k), 99, dtype=torch.int8, device="cuda") if q8 else None
+    d_d = torch.full((m, k // 32), 7.0, device="cuda") if q8 else None
+    print("rmsnorm m=%d k=%d %s residual=%s q8=%s stride=%d" % (m, k, kind, residual, q8, stride),
+          flush=True)
+    q4k.q4k_rmsnorm(x_d, w_d, k, m, eps=eps, residual=r_d, sum_out=h_d, y=y_d, y16=y16_d, q=q_d,
+                    d=d_d, x_stride=stride)
+    torch.cuda.synchronize()
+    h = xt[:, :k].float().numpy()
+    h = h + res.numpy() if residual else h
+    return h, w.numpy(), h_d, y_d, y16_d, q_d, d_d
+
+
+@pytest.mark.parametrize("m,k,kind,residual,stride", [
+    (1, 1, "f32", False, 0), (1, 1, "bf16", True, 0), (3, 7, "f16", True, 0),
+    (5, 250, "f32", True, 0), (2, 251, "bf16", False, 300), (4, 256, "f16", True, 264),
+    (1, 4096, "f32", True, 0), (7, 4096, "f16", False, 4099), (2, 8192, "bf16", True, 0),
+    (1, 14336, "f32", True, 0), (2, 33000, "f32", True, 0), (1, 70008, "f16", True, 0),
+    (1, 70011, "bf16", False, 0), (1030, 64, "f16", True, 0), (1025, 2056, "f32", True, 2064),
+    (1100, 4128, "bf16", True, 0),
+])
+def test_rmsnorm(oracle_mod, m, k, kind, residual, stride):
+    q8 = k % 32 == 0
+    h, w, h_d, y_d, y16_d, q_d, d_d = _run(m, k, kind, residual, q8, m + k, stride)
+    assert np.array_equal(h_d.cpu().numpy().view(np.uint32), h.view(np.uint32))
+    ref = _ref(h, w, 1e-5)
+    y = y_d.cpu().numpy()
+    _check(y, ref)
+    err16 = np.abs(y16_d.cpu().numpy().astype(np.float64) - ref)
+    assert (err16 <= (2.0 ** -11 + 2.0 ** -23) * np.abs(ref) + 2.0 ** -25).all()
+    if q8:
+        q_ref, d_ref = oracle_mod.quantize_q8(y)
+        assert np.array_equal(q_d.cpu().numpy(), q_ref)
+        assert np.array_equal(d_d.cpu().numpy().view(np.uint32), d_ref.view(np.uint32))
+
+
+@pytest.mark.parametrize("scale,eps", [(1e25, 0.0), (1e-30, 0.0), (1e-42, 1e-5), (3e37, 1e-5)])
+def test_rmsnorm_ranges(scale, eps):
+    """Squares beyond the f32 range, and subnormal rows."""
+    h, w, h_d, y_d, _, _, _ = _run(2, 512, "f32", False, True, 5, scale=scale, eps=eps)
+    ref = _ref(h, w, eps)
+    _check(y_d.cpu().numpy(), ref)
+
+
+def test_rmsnorm_in_place_and_single_outputs():
+    """The residual stream updated in place gives the same bits as kept apart,
+    and each output alone those of all together; also past what registers
+    hold."""
+    for m, k in ((3, 2048), (2, 40960)):
+        h, w, h_d, y_d, y16_d, q_d, d_d = _run(m, k, "f16", True, True, 11)
+        g = torch.Generator().manual_seed(11)
+        x = torch.randn((m, k), generator=g).half().cuda()
+        res = torch.randn((m, k), generator=g).cuda()
+        wd = torch.from_numpy(w).cuda()
+        y2 = torch.empty_like(y_d)
+        stream = res.clone()
+        q4k.q4k_rmsnorm(x, wd, k, m, residual=stream, sum_out=stream, y=y2)
+        assert torch.equal(stream, h_d) and torch.equal(y2, y_d)
+        y3 = torch.empty_like(y16_d)
+        q4k.q4k_rmsnorm(x, wd, k, m, residual=res, y16=y3)
+        assert torch.equal(y3, y16_d)
+        q2, d2 = torch.empty_like(q_d), torch.empty_like(d_d)
+        q4k.q4k_rmsnorm(x, wd, k, m, residual=res, q=q2, d=d2)
+        assert torch.equal(q2, q_d) and torch.equal(d2, d_d)
+        h2 = torch.empty_like(h_d)
+        q4k.q4k_rmsnorm(x, wd, k, m, residual=res, sum_out=h2)
+        assert torch.equal(h2, h_d)
+
+
+def test_rmsnorm_non_finite_rows():
+    """An infinity: NaN there, 0 elsewhere; a NaN: the row; zeros with eps 0:
+    NaN.  Other rows are untouched by it."""
+    x = torch.ones((5, 64))
+    x[1, 3] = float("inf")
+    x[2, 5] = float("nan")
+    x[3] = 0.0
+    w = torch.full((64,), 2.0)
+    y = torch.empty((5, 64), device="cuda")
+    q = torch.empty((5, 64), dtype=torch.int8, device="cuda")
+    d = torch.empty((5, 2), device="cuda")
+    q4k.q4k_rmsnorm(x.cuda(), w.cuda(), 64, 5, eps=0.0, y=y, q=q, d=d)
+    y = y.cpu()
+    assert (y[0] == 2.0).all() and (y[4] == 2.0).all()
+    assert torch.isnan(y[1, 3]) and (torch.cat((y[1, :3], y[1, 4:])) == 0).all()
+    assert torch.isnan(y[2]).all() and torch.isnan(y[3]).all()
+    q, d = q.cpu(), d.cpu()
+    assert torch.isnan(d[1, 0]) and d[1, 1] == 0 and (q[1] == 0).all() and (q[2] == 0).all()
+    assert (q[0] == 127).all()
+
+
+def test_rmsnorm_refuses_short_tensors():
+    x = torch.zeros((2, 256), device="cuda")
+    w = torch.zeros(256, device="cuda")
+    with pytest.raises(ValueError):
+        q4k.q4k_rmsnorm(x, w, 256, 3, y=torch.empty((3, 256), device="cuda"))
+    with pytest.raises(ValueError):
+        q4k.q4k_rmsnorm(x, w, 256, 2, y=torch.empty((1, 256), device="cuda"))
+    with pytest.raises(ValueError):
+        q4k.q4k_rmsnorm(x[:, :128], w, 128, 3, x_stride=256,
+                        y=torch.empty((3, 128), device="cuda"))
+    with pytest.raises(TypeError):
+        q4k.q4k_rmsnorm(x, w, 256, 2, y16=torch.empty((2, 256), device="cuda"))
+    with pytest.raises(TypeError):
+        q4k.q4k_rmsnorm(x.double(), w, 256, 2, y=torch.empty((2, 256), device="cuda"))
