@@ -14,7 +14,7 @@
 // operand is rounded, the sums are f32.  A row or column of an adapter at or
 // beyond its rank is never read, whatever it holds.
 //
-// Down: the eight waves of a workgroup share k, 64 ranks at a time (x is read
+// Down: the sixteen waves of a workgroup share k, 64 ranks at a time (x is read
 // once for r <= 64), and add up their parts in LDS in wave order.  Up: bound
 // by reading the base and writing y; B's rows are the matrix operand's rows,
 // so a lane holds four consecutive columns of one y row (16-byte accesses).
@@ -31,12 +31,12 @@ namespace {
 
 typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
-typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTile = 16;              // rows per tile
 constexpr int kRanks = 4;              // rank tiles of 16 per down workgroup
-constexpr int kDownWaves = 8;
+constexpr int kDownWaves = 16;
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter)
 {
@@ -50,21 +50,98 @@ __device__ __forceinline__ int row_of(const LoraArgs& a, int p)
     return r >= 0 && r < a.rows ? r : -1;
 }
 
-// Four x elements as f32
+// Eight consecutive x elements, as the matrix operands take them
 template <int TYPE>
-__device__ __forceinline__ f4_t load_x4(const void* base, int64_t at)
+struct X8 {
+    f4_t lo, hi;                               // f32 (bfloat16 widened)
+};
+template <>
+struct X8<kTypeF16> {
+    h8_t v;
+};
+
+template <int TYPE>
+__device__ __forceinline__ X8<TYPE> load_x8(const void* base, int64_t at)
 {
-    if constexpr (TYPE == kTypeF32) {
-        return *reinterpret_cast<const f4_t*>(static_cast<const float*>(base) + at);
-    } else {                                   // bfloat16
-        const u16x4_t v =
-            *reinterpret_cast<const u16x4_t*>(static_cast<const uint16_t*>(base) + at);
-        f4_t r;
+    X8<TYPE> r;
+    if constexpr (TYPE == kTypeF16) {
+        r.v = *reinterpret_cast<const h8_t*>(static_cast<const _Float16*>(base) + at);
+    } else if constexpr (TYPE == kTypeF32) {
+        const float* p = static_cast<const float*>(base) + at;
+        r.lo = *reinterpret_cast<const f4_t*>(p);
+        r.hi = *reinterpret_cast<const f4_t*>(p + 4);
+    } else {
+        const u16x8_t v =
+            *reinterpret_cast<const u16x8_t*>(static_cast<const uint16_t*>(base) + at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            r[i] = __builtin_bit_cast(float, (uint32_t)v[i] << 16);
+            r.lo[i] = __builtin_bit_cast(float, (uint32_t)v[i] << 16);
+            r.hi[i] = __builtin_bit_cast(float, (uint32_t)v[i + 4] << 16);
         }
-        return r;
+    }
+    return r;
+}
+
+// One wave's part of v for the tile: k steps of 32 from wave * 32 on, every
+// kDownWaves-th, U of them in flight.  acc[i]: rank tile i.
+template <int TYPE, int NT, int U>
+__device__ __forceinline__ void down_part(const LoraArgs& a, int64_t xat, bool there, int group,
+                                          int rank0, int rank, f4_t* acc)
+{
+    const int lane = threadIdx.x & 63;
+    const int j = lane & 15;
+    const int g = lane >> 4;
+    // rank tile i: this lane's row of A, read only below the rank
+    const _Float16* arow[NT];
+    bool has[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int rr = rank0 + 16 * i + j;
+        has[i] = rr < rank;
+        arow[i] = static_cast<const _Float16*>(a.a) +
+                  ((int64_t)group * a.r + (has[i] ? rr : 0)) * a.k;
+        acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int k0 = (threadIdx.x >> 6) * 32; k0 < a.k; k0 += 32 * kDownWaves * U) {
+        X8<TYPE> x[U];
+        h8_t w[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = k0 + u * 32 * kDownWaves + 8 * g;
+            const bool in = at < a.k;          // k % 8 == 0: all eight or none
+            x[u] = X8<TYPE>{};
+            if (there && in) {
+                x[u] = load_x8<TYPE>(a.x, xat + at);
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                w[u][i] = h8_t{0, 0, 0, 0, 0, 0, 0, 0};
+                if (has[i] && in) {
+                    w[u][i] = *reinterpret_cast<const h8_t*>(arow[i] + at);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if constexpr (TYPE == kTypeF16) {
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[u].v, w[u][i], acc[i], 0, 0,
+                                                                    0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            x[u].lo[c], (float)w[u][i][c], acc[i], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            x[u].hi[c], (float)w[u][i][c + 4], acc[i], 0, 0, 0);
+                    }
+                }
+            }
+        }
     }
 }
 
@@ -90,68 +167,27 @@ lora_down_kernel(LoraArgs a)
     const int row = j < t.count ? row_of(a, t.begin + j) : -1;
     const bool there = row >= 0;
     const int64_t xat = (int64_t)(there ? row : 0) * a.k;
-    // rank tile i: this lane's row of A, read only below the rank
-    const _Float16* arow[kRanks];
-    bool has[kRanks];
-#pragma unroll
-    for (int i = 0; i < kRanks; ++i) {
-        const int rr = rank0 + 16 * i + j;
-        has[i] = rr < rank;
-        arow[i] = static_cast<const _Float16*>(a.a) +
-                  ((int64_t)t.group * a.r + (has[i] ? rr : 0)) * a.k;
-    }
     f4_t acc[kRanks];
-#pragma unroll
-    for (int i = 0; i < kRanks; ++i) {
-        acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
-    }
-    if constexpr (TYPE == kTypeF16) {
-        const _Float16* x = static_cast<const _Float16*>(a.x) + xat;
-        for (int kb = wave * 32; kb < a.k; kb += 32 * kDownWaves) {
-            const int at = kb + 8 * g;
-            const bool in = at < a.k;          // k % 8 == 0: all eight or none
-            h8_t xv = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (there && in) {
-                xv = *reinterpret_cast<const h8_t*>(x + at);
-            }
-#pragma unroll
-            for (int i = 0; i < kRanks; ++i) {
-                h8_t av = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (has[i] && in) {
-                    av = *reinterpret_cast<const h8_t*>(arow[i] + at);
-                }
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv, av, acc[i], 0, 0, 0);
-            }
-        }
+    // as many rank tiles as the adapter has; steps in flight by the registers
+    // that leaves
+    const int left = rank - rank0;
+    if (left <= 16) {
+        down_part<TYPE, 1, TYPE == kTypeF16 ? 8 : 4>(a, xat, there, t.group, rank0, rank, acc);
+    } else if (left <= 32) {
+        down_part<TYPE, 2, 4>(a, xat, there, t.group, rank0, rank, acc);
     } else {
-        for (int kb = wave * 16; kb < a.k; kb += 16 * kDownWaves) {
-            const int at = kb + 4 * g;
-            const bool in = at < a.k;
-            f4_t xv = {0.f, 0.f, 0.f, 0.f};
-            if (there && in) {
-                xv = load_x4<TYPE>(a.x, xat + at);
-            }
-#pragma unroll
-            for (int i = 0; i < kRanks; ++i) {
-                h4_t av = {0, 0, 0, 0};
-                if (has[i] && in) {
-                    av = *reinterpret_cast<const h4_t*>(arow[i] + at);
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[c], (float)av[c], acc[i], 0,
-                                                                  0, 0);
-                }
-            }
-        }
+        down_part<TYPE, 4, TYPE == kTypeF16 ? 4 : 2>(a, xat, there, t.group, rank0, rank, acc);
     }
+    const int tiles = left <= 16 ? 1 : left <= 32 ? 2 : 4;
 #pragma unroll
     for (int i = 0; i < kRanks; ++i) {
-        part[wave][i][lane] = acc[i];
+        if (i < tiles) {
+            part[wave][i][lane] = acc[i];
+        }
     }
     __syncthreads();
     const int i = wave;
-    if (i >= kRanks || rank0 + 16 * i >= rank) {
+    if (i >= kRanks || 16 * i >= left) {
         return;
     }
     f4_t sum = part[0][i][lane];
@@ -172,69 +208,90 @@ lora_down_kernel(LoraArgs a)
     }
 }
 
-// y of the tile's positions, columns from blockIdx.y * 64 * each on: wave w
-// takes 16-column tiles w, w + 4, ...  VB: rows of B are multiples of four
-// halves; VY: rows of y and base multiples of four floats.
+// y of the tile's positions, 64 columns per wave from blockIdx.y * 256 on.
+// VB: rows of B are multiples of four halves; VY: rows of y and base
+// multiples of four floats.  The base is the accumulators' start.
 template <bool VB, bool VY>
 __global__ void __launch_bounds__(256)
-lora_up_kernel(LoraArgs a, int each)
+lora_up_kernel(LoraArgs a)
 {
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
     const int j = lane & 15;
     const int g = lane >> 4;
+    const int col0 = (int)blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
     const GroupTile t = find_tile<kTile>(a.offsets, a.adapters, a.rows, blockIdx.x);
-    if (t.count == 0) {
+    if (t.count == 0 || col0 >= a.n) {
         return;
     }
     const int rank = rank_of(a, t.group);
     const int row = j < t.count ? row_of(a, t.begin + j) : -1;
     const int pitch = (a.r + 15) / 16 * 16;
     const float* v = a.v + (int64_t)(t.begin + min(j, t.count - 1)) * pitch + 4 * g;
-    for (int e = 0; e < each; ++e) {
-        const int col0 = ((int)blockIdx.y * each + e) * 64 + wave * 16;
-        if (col0 >= a.n) {
-            return;
-        }
-        // B row of this lane (as a matrix row), then four columns of y
-        const int col = min(col0 + j, a.n - 1);
-        const _Float16* b = static_cast<const _Float16*>(a.b) +
-                            ((int64_t)t.group * a.n + col) * a.r + 4 * g;
-        f4_t acc = {0.f, 0.f, 0.f, 0.f};
-        for (int k0 = 0; k0 < rank; k0 += 16) {
-            const int left = rank - k0 - 4 * g;        // ranks of this lane's four
-            const f4_t vv = *reinterpret_cast<const f4_t*>(v + k0);
-            h4_t bv = {0, 0, 0, 0};
-            if (VB && left >= 4) {
-                bv = *reinterpret_cast<const h4_t*>(b + k0);
-            } else {
+    // D[4 g + c][j]: column col0 + 16 i + 4 g + c of position j
+    f4_t acc[4];
+    const _Float16* b[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    bv[c] = c < left ? b[k0 + c] : (_Float16)0;
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32((float)bv[c], vv[c], acc, 0, 0, 0);
-            }
-        }
-        // D[4 g + c][j]: column col0 + 4 g + c of position j
-        if (row >= 0) {
-            const int at = col0 + 4 * g;
-            const int64_t o = (int64_t)row * a.n + at;
+    for (int i = 0; i < 4; ++i) {
+        const int at = col0 + 16 * i + 4 * g;
+        const int64_t o = (int64_t)row * a.n + at;
+        acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
+        if (a.base != nullptr && row >= 0) {
             if constexpr (VY) {
                 if (at < a.n) {                        // n % 4 == 0: all four or none
-                    if (a.base != nullptr) {
-                        acc += *reinterpret_cast<const f4_t*>(a.base + o);
-                    }
-                    *reinterpret_cast<f4_t*>(a.y + o) = acc;
+                    acc[i] = *reinterpret_cast<const f4_t*>(a.base + o);
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (at + c < a.n) {
-                        a.y[o + c] = acc[c] + (a.base != nullptr ? a.base[o + c] : 0.f);
-                    }
+                    acc[i][c] = at + c < a.n ? a.base[o + c] : 0.f;
+                }
+            }
+        }
+        // B row of this lane, as a matrix row
+        const int col = min(col0 + 16 * i + j, a.n - 1);
+        b[i] = static_cast<const _Float16*>(a.b) + ((int64_t)t.group * a.n + col) * a.r + 4 * g;
+    }
+    for (int k0 = 0; k0 < rank; k0 += 16) {
+        const int left = rank - k0 - 4 * g;            // ranks of this lane's four
+        const f4_t vv = *reinterpret_cast<const f4_t*>(v + k0);
+        h4_t bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bv[i] = h4_t{0, 0, 0, 0};
+            if (VB && left >= 4) {
+                bv[i] = *reinterpret_cast<const h4_t*>(b[i] + k0);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    bv[i][c] = c < left ? b[i][k0 + c] : (_Float16)0;
+                }
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)bv[i][c], vv[c], acc[i], 0, 0,
+                                                              0);
+            }
+        }
+    }
+    if (row < 0) {
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = col0 + 16 * i + 4 * g;
+        const int64_t o = (int64_t)row * a.n + at;
+        if constexpr (VY) {
+            if (at < a.n) {
+                *reinterpret_cast<f4_t*>(a.y + o) = acc[i];
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (at + c < a.n) {
+                    a.y[o + c] = acc[i][c];
                 }
             }
         }
@@ -253,7 +310,7 @@ bool lora_fits(int64_t rows, int64_t adapters, int64_t n, int64_t r)
 {
     const int64_t tiles = most_tiles(rows, adapters, kTile);
     const int64_t down = (r + 16 * kRanks - 1) / (16 * kRanks);
-    const int64_t up = (n + 63) / 64;
+    const int64_t up = (n + 255) / 256;
     const int64_t most = (int64_t)1 << 32;
     return tiles * down * 64 * kDownWaves < most && up <= 65535 && tiles * up * 256 < most;
 }
@@ -274,20 +331,17 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream)
     if (e != hipSuccess) {
         return e;
     }
-    // several column tiles per wave once there are enough workgroups without
-    const int64_t parts = (a.n + 63) / 64;
-    const int each = (int64_t)tiles * parts >= 8192 ? 4 : 1;
-    const dim3 up(tiles, (unsigned)((parts + each - 1) / each));
+    const dim3 up(tiles, (unsigned)((a.n + 255) / 256));
     const bool vb = a.r % 4 == 0;
     const bool vy = a.n % 4 == 0;
     if (vb && vy) {
-        hipLaunchKernelGGL((lora_up_kernel<true, true>), up, dim3(256), 0, stream, a, each);
+        hipLaunchKernelGGL((lora_up_kernel<true, true>), up, dim3(256), 0, stream, a);
     } else if (vb) {
-        hipLaunchKernelGGL((lora_up_kernel<true, false>), up, dim3(256), 0, stream, a, each);
+        hipLaunchKernelGGL((lora_up_kernel<true, false>), up, dim3(256), 0, stream, a);
     } else if (vy) {
-        hipLaunchKernelGGL((lora_up_kernel<false, true>), up, dim3(256), 0, stream, a, each);
+        hipLaunchKernelGGL((lora_up_kernel<false, true>), up, dim3(256), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((lora_up_kernel<false, false>), up, dim3(256), 0, stream, a, each);
+        hipLaunchKernelGGL((lora_up_kernel<false, false>), up, dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }
