@@ -36,14 +36,27 @@ namespace {
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWaves = kPlaceThreads / 64;
 
-// Wave maximum of f32 values that are not NaN.
+// One step of a wave reduction: v of the lane that DPP control CTRL names (its
+// own where there is none).
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v)
+{
+    const int i = __builtin_bit_cast(int, v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+}
+
+// Wave maximum of f32 values that are not NaN: within rows of 16 lanes (row
+// shifts by 1, 2, 4, 8), then across them (broadcasts of lanes 15 and 31), so
+// lane 63 has it.
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        v = fmaxf(v, __shfl_xor(v, off, 64));
-    }
-    return v;
+    v = fmaxf(v, dpp_f<0x111>(v));
+    v = fmaxf(v, dpp_f<0x112>(v));
+    v = fmaxf(v, dpp_f<0x114>(v));
+    v = fmaxf(v, dpp_f<0x118>(v));
+    v = fmaxf(v, dpp_f<0x142>(v));
+    v = fmaxf(v, dpp_f<0x143>(v));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 __device__ __forceinline__ float wave_sum_f(float v)

@@ -133,6 +133,8 @@ _lib = None
 def load_library():
     """Load libq4k.so (raises OSError/RuntimeError when it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -400,82 +402,86 @@ def q4k_f16_gemm_f32x_noalloc(w16, x, y, m: int, n: int, k: int, stream=None) ->
 
 
 # ---------------------------------------- around a layer's projections
-# These run where their tensors live: ``stream=None`` is torch's current
-# stream of the first tensor's device, made current for the call when it is
-# not, and a tensor on another device is refused.
-class _Call:
-    """Addresses, stream and device of one call."""
+# These run where their tensors live: the device of the first tensor, made
+# current for the call when it is not, on that device's current stream unless
+# one is given.  A tensor on another device, of another type than the call
+# takes, not dense or too short is refused before the call.
+_torch = None
 
-    __slots__ = ("device",)
 
-    def __init__(self):
-        self.device = None
-
-    def at(self, a, kind=None, count=None):
-        """Address of a (None passes through); a tensor is checked to be dense,
-        on the call's device, of the element type `kind` and to hold at least
-        `count` elements."""
-        if a is None or isinstance(a, int):
-            return a
-        if not hasattr(a, "data_ptr"):
-            return _addr(a)
-        if not a.is_contiguous():
-            raise ValueError("tensor must be contiguous")
-        device = a.device
-        if device.type != "cuda":
-            raise ValueError("expected a tensor on the GPU, got one on %s" % device)
-        if self.device is None:
-            self.device = device
-        elif device != self.device:
-            raise ValueError("tensors on %s and %s in one call" % (self.device, device))
-        if kind is not None and str(a.dtype) not in kind:
-            raise TypeError("expected %s, got %s" % (" or ".join(kind), a.dtype))
-        if count is not None and a.numel() < count:
-            raise ValueError("a tensor of %d elements where %d are needed" % (a.numel(), count))
-        return a.data_ptr()
-
-    def run(self, fn, where, stream, *args):
+def _device(*args):
+    """Index of the device of the first tensor among args (None: no tensor)."""
+    global _torch
+    if _torch is None:
         import torch
-        if self.device is None:
-            rc = fn(*args, _stream(stream))
+        _torch = torch
+    for a in args:
+        if hasattr(a, "get_device"):
+            index = a.get_device()
+            if index < 0:
+                raise ValueError("expected a tensor on the GPU, got one on %s" % a.device)
+            return index
+    return None
+
+
+def _at(a, dtype, count, dev):
+    """Address of a (None and integer addresses as they are); a tensor is
+    dense, on device dev, of type dtype (None: any) and holds at least count
+    elements."""
+    if a is None or type(a) is int:
+        return a
+    if not hasattr(a, "get_device"):
+        return _addr(a)
+    if a.get_device() != dev:
+        raise ValueError("tensors on more than one device: %s and cuda:%s" % (a.device, dev))
+    if a.dtype is not dtype and dtype is not None:
+        raise TypeError("expected %s, got %s" % (dtype, a.dtype))
+    if not a.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    if a.numel() < count:
+        raise ValueError("a tensor of %d elements where %d are needed" % (a.numel(), count))
+    return a.data_ptr()
+
+
+def _run(fn, where, dev, stream, *args):
+    """fn(*args, stream) with device dev current; raises for its status."""
+    if dev is None:
+        rc = fn(*args, _stream(stream))
+    else:
+        cuda = _torch.cuda
+        if stream is None:
+            stream = cuda.current_stream(dev).cuda_stream
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if dev == cuda.current_device():
+            rc = fn(*args, stream)
         else:
-            index = self.device.index
-            s = torch.cuda.current_stream(index).cuda_stream if stream is None else _stream(stream)
-            if index == torch.cuda.current_device():
-                rc = fn(*args, s)
-            else:
-                with torch.cuda.device(index):
-                    rc = fn(*args, s)
-        if rc != Q4K_OK:
-            raise Q4KError(rc, where)
-
-
-_F32 = ("torch.float32",)
-_F16 = ("torch.float16",)
-_I8 = ("torch.int8",)
-_I32 = ("torch.int32",)
-_U8 = ("torch.uint8", "torch.int8")
-_TYPE_OF = {"torch.float32": Q4K_F32, "torch.float16": Q4K_F16, "torch.bfloat16": Q4K_BF16}
+            with cuda.device(dev):
+                rc = fn(*args, stream)
+    if rc != Q4K_OK:
+        raise Q4KError(rc, where)
 
 
 def _act_type(x, x_type):
     """The q4k_type of x: given, or its tensor's."""
     if x_type is not None:
         return int(x_type)
-    if hasattr(x, "data_ptr"):
-        t = _TYPE_OF.get(str(x.dtype))
-        if t is None:
-            raise TypeError("expected f32, f16 or bf16 activations, got %s" % x.dtype)
-        return t
-    return Q4K_F32
+    if not hasattr(x, "get_device"):
+        return Q4K_F32
+    dtype = x.dtype
+    if dtype is _torch.float32:
+        return Q4K_F32
+    if dtype is _torch.float16:
+        return Q4K_F16
+    if dtype is _torch.bfloat16:
+        return Q4K_BF16
+    raise TypeError("expected f32, f16 or bf16 activations, got %s" % dtype)
 
 
 def _ws_bytes(ws, ws_bytes):
     if ws_bytes is not None:
         return int(ws_bytes)
-    if ws is None:
-        return 0
-    return ws.numel() * ws.element_size() if hasattr(ws, "numel") else 0
+    return ws.numel() * ws.element_size() if hasattr(ws, "element_size") else 0
 
 
 def q4k_rmsnorm(x, weight, k: int, m: int = 1, *, eps: float = 1e-5, residual=None, sum_out=None,
@@ -483,24 +489,23 @@ def q4k_rmsnorm(x, weight, k: int, m: int = 1, *, eps: float = 1e-5, residual=No
                 stream=None) -> None:
     """h = x + residual, y = h * weight / sqrt(mean h^2 + eps) for m rows of
     k: h to sum_out, y to any of y (f32), y16 (f16) and q, d (Q8 codes and
-    scales); asynchronous on stream."""
-    c = _Call()
+    scales); x f32, f16 or bf16, its rows x_stride elements apart (0: k);
+    asynchronous on stream."""
+    dev = _device(x, weight)
     mk = m * k
-    if hasattr(x, "data_ptr") and x_stride:
-        # a view with strided rows: its elements need not be dense
-        need = (m - 1) * x_stride + k
-        if x.untyped_storage().nbytes() // x.element_size() - x.storage_offset() < need:
+    if x_stride and hasattr(x, "get_device"):
+        # a view with strided rows: dense within each row only
+        have = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+        if have < (m - 1) * x_stride + k:
             raise ValueError("x does not hold %d rows at stride %d" % (m, x_stride))
-        if x.device.type != "cuda":
-            raise ValueError("expected a tensor on the GPU, got one on %s" % x.device)
-        c.device = x.device
         xa = x.data_ptr()
     else:
-        xa = c.at(x, None, mk)
-    c.run(load_library().q4k_rmsnorm, "q4k_rmsnorm", stream, xa, _act_type(x, x_type),
-          int(x_stride), c.at(residual, _F32, mk), c.at(weight, _F32, k), c.at(sum_out, _F32, mk),
-          c.at(y, _F32, mk), c.at(y16, _F16, mk), c.at(q, _I8, mk), c.at(d, _F32, mk // 32), int(k),
-          int(m), float(eps))
+        xa = _at(x, None, mk, dev)
+    f32, i8, f16 = _torch.float32, _torch.int8, _torch.float16
+    _run(load_library().q4k_rmsnorm, "q4k_rmsnorm", dev, stream, xa, _act_type(x, x_type),
+         int(x_stride), _at(residual, f32, mk, dev), _at(weight, f32, k, dev), _at(sum_out, f32, mk, dev),
+         _at(y, f32, mk, dev), _at(y16, f16, mk, dev), _at(q, i8, mk, dev),
+         _at(d, f32, mk // 32, dev), int(k), int(m), float(eps))
 
 
 def q4k_moe_group_ws(slots: int, groups: int, topk: int = 1) -> int:
@@ -513,38 +518,39 @@ def q4k_moe_route(logits, ids, weights, n_experts: int, topk: int, m: int = 1, *
                   logits_stride: int = 0, stream=None) -> None:
     """The topk experts of m tokens (ids, softmax weights) and, with offsets
     and order, their slots grouped by expert; asynchronous on stream."""
-    c = _Call()
+    dev = _device(logits, ids)
+    f32, i32 = _torch.float32, _torch.int32
     slots = m * topk
     span = (m - 1) * (logits_stride or n_experts) + n_experts
-    c.run(load_library().q4k_moe_route, "q4k_moe_route", stream, c.at(logits, _F32, span),
-          int(logits_stride), c.at(ids, _I32, slots), c.at(weights, _F32, slots),
-          c.at(offsets, _I32, n_experts + 1), c.at(order, _I32, slots), int(n_experts), int(topk),
-          1 if renorm else 0, int(m), c.at(ws), _ws_bytes(ws, ws_bytes))
+    _run(load_library().q4k_moe_route, "q4k_moe_route", dev, stream, _at(logits, f32, span, dev),
+         int(logits_stride), _at(ids, i32, slots, dev), _at(weights, f32, slots, dev),
+         _at(offsets, i32, n_experts + 1, dev), _at(order, i32, slots, dev), int(n_experts),
+         int(topk), 1 if renorm else 0, int(m), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_moe_group(ids, offsets, order, count: int, groups: int, *, ws=None, ws_bytes=None,
                   stream=None) -> None:
     """Slots grouped by id (order), and where each group begins (offsets);
     asynchronous on stream."""
-    c = _Call()
-    c.run(load_library().q4k_moe_group, "q4k_moe_group", stream, c.at(ids, _I32, count),
-          c.at(offsets, _I32, groups + 1), c.at(order, _I32, count), int(count), int(groups),
-          c.at(ws), _ws_bytes(ws, ws_bytes))
+    dev = _device(ids, offsets)
+    i32 = _torch.int32
+    _run(load_library().q4k_moe_group, "q4k_moe_group", dev, stream, _at(ids, i32, count, dev),
+         _at(offsets, i32, groups + 1, dev), _at(order, i32, count, dev), int(count),
+         int(groups),
+         _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_moe_combine(y, weights, ids, out, n: int, topk: int, m: int = 1, *, residual=None,
                     stream=None) -> None:
     """out[t] = residual[t] + sum_j weights[t][j] y[t * topk + j] over the
     choices with an id (ids None: all); asynchronous on stream."""
-    c = _Call()
-    c.run(load_library().q4k_moe_combine, "q4k_moe_combine", stream, c.at(y, _F32, m * topk * n),
-          c.at(weights, _F32, m * topk), c.at(ids, _I32, m * topk), c.at(residual, _F32, m * n),
-          c.at(out, _F32, m * n), int(n), int(topk), int(m))
-
-
-def _grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count):
-    return (c.at(offsets, _I32, groups + 1), c.at(x_rows, _I32, rows), c.at(y_rows, _I32, rows),
-            int(n), int(k), int(groups), int(rows), int(x_div), int(x_count), int(y_count))
+    dev = _device(y, out)
+    f32 = _torch.float32
+    mt = m * topk
+    _run(load_library().q4k_moe_combine, "q4k_moe_combine", dev, stream, _at(y, f32, mt * n, dev),
+         _at(weights, f32, mt, dev), _at(ids, _torch.int32, mt, dev),
+         _at(residual, f32, m * n, dev), _at(out, f32, m * n, dev), int(n), int(topk),
+         int(m))
 
 
 def q4k_gemv_grouped_ws(k: int, x_count: int) -> int:
@@ -557,14 +563,15 @@ def q4k_gemv_grouped(w, x, y, offsets, n: int, k: int, groups: int, rows: int, *
                      ws_bytes=None, stream=None) -> None:
     """Position p of group g: y[y_rows[p]] = W_g x[x_rows[p] // x_div], W_g
     in Q4_K, x f32 (counts default to rows); asynchronous on stream."""
-    c = _Call()
+    dev = _device(w, x)
+    f32, i32 = _torch.float32, _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
-    c.run(load_library().q4k_gemv_grouped, "q4k_gemv_grouped", stream,
-          c.at(w, _U8, groups * n * (k // 256) * 144), c.at(x, _F32, x_count * k),
-          c.at(y, _F32, y_count * n),
-          *_grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count),
-          c.at(ws), _ws_bytes(ws, ws_bytes))
+    _run(load_library().q4k_gemv_grouped, "q4k_gemv_grouped", dev, stream,
+         _at(w, _torch.uint8, groups * n * (k // 256) * 144, dev), _at(x, f32, x_count * k, dev),
+         _at(y, f32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
+         _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
+         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: int, *,
@@ -572,28 +579,35 @@ def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: 
                         ws=None, ws_bytes=None, stream=None) -> None:
     """q4k_gemv_grouped with x in Q8: codes q (int8) and scales d (f32, one
     per 32); asynchronous on stream."""
-    c = _Call()
+    dev = _device(w, q)
+    f32, i32 = _torch.float32, _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
-    c.run(load_library().q4k_gemv_grouped_q8, "q4k_gemv_grouped_q8", stream,
-          c.at(w, _U8, groups * n * (k // 256) * 144), c.at(q, _I8, x_count * k),
-          c.at(d, _F32, x_count * (k // 32)), c.at(y, _F32, y_count * n),
-          *_grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count),
-          c.at(ws), _ws_bytes(ws, ws_bytes))
+    _run(load_library().q4k_gemv_grouped_q8, "q4k_gemv_grouped_q8", dev, stream,
+         _at(w, _torch.uint8, groups * n * (k // 256) * 144, dev),
+         _at(q, _torch.int8, x_count * k, dev), _at(d, f32, x_count * (k // 32), dev),
+         _at(y, f32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
+         _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
+         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows: int, *,
                          x_rows=None, x_div: int = 1, x_count=None, y_rows=None, y_count=None,
                          stream=None) -> None:
-    """q4k_gemv_grouped on fp16 mirrors (groups * n x k halves) and fp16 x, on
-    the matrix cores; asynchronous on stream."""
-    c = _Call()
+    """q4k_gemv_grouped on fp16 mirrors (groups * n x k halves, as f16 or
+    int16 tensors) and fp16 x, on the matrix cores; asynchronous on stream."""
+    dev = _device(w16, x16)
+    i32 = _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
-    c.run(load_library().q4k_f16_gemm_grouped, "q4k_f16_gemm_grouped", stream,
-          c.at(w16, None, groups * n * k), c.at(x16, None, x_count * k),
-          c.at(y, _F32, y_count * n),
-          *_grouped_args(c, offsets, x_rows, y_rows, n, k, groups, rows, x_div, x_count, y_count))
+    for t in (w16, x16):
+        if hasattr(t, "element_size") and t.element_size() != 2:
+            raise TypeError("expected 16-bit elements, got %s" % t.dtype)
+    _run(load_library().q4k_f16_gemm_grouped, "q4k_f16_gemm_grouped", dev, stream,
+         _at(w16, None, groups * n * k, dev), _at(x16, None, x_count * k, dev),
+         _at(y, _torch.float32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
+         _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
+         int(rows), int(x_div), int(x_count), int(y_count))
 
 
 def q4k_lora_ws(rows: int, r: int) -> int:
@@ -605,15 +619,17 @@ def q4k_lora(x, a, b, y, offsets, order, n: int, k: int, r: int, adapters: int, 
              base=None, ranks=None, scales=None, ws=None, ws_bytes=None, x_type=None,
              stream=None) -> None:
     """y[row] = base[row] + scales[a] B_a (A_a x[row]) for the rows of each
-    adapter a (a: adapters x r x k, b: adapters x n x r, both f16; offsets and
-    order as q4k_moe_group gives them); asynchronous on stream."""
-    c = _Call()
-    c.run(load_library().q4k_lora, "q4k_lora", stream, c.at(x, None, rows * k),
-          _act_type(x, x_type), c.at(a, _F16, adapters * r * k), c.at(b, _F16, adapters * n * r),
-          c.at(base, _F32, rows * n), c.at(y, _F32, rows * n), c.at(ranks, _I32, adapters),
-          c.at(scales, _F32, adapters), c.at(offsets, _I32, adapters + 1),
-          c.at(order, _I32, rows), int(n), int(k), int(r), int(adapters), int(rows), c.at(ws),
-          _ws_bytes(ws, ws_bytes))
+    adapter a (a: adapters x r x k, b: adapters x n x r, both f16; x f32, f16
+    or bf16; offsets and order as q4k_moe_group gives them); asynchronous on
+    stream."""
+    dev = _device(x, a)
+    f32, i32, f16 = _torch.float32, _torch.int32, _torch.float16
+    _run(load_library().q4k_lora, "q4k_lora", dev, stream, _at(x, None, rows * k, dev),
+         _act_type(x, x_type), _at(a, f16, adapters * r * k, dev), _at(b, f16, adapters * n * r, dev),
+         _at(base, f32, rows * n, dev), _at(y, f32, rows * n, dev), _at(ranks, i32, adapters, dev),
+         _at(scales, f32, adapters, dev), _at(offsets, i32, adapters + 1, dev),
+         _at(order, i32, rows, dev), int(n), int(k), int(r), int(adapters), int(rows), _at(ws, None, 0, dev),
+         _ws_bytes(ws, ws_bytes))
 
 
 def q4k_read_calibrate_blocks() -> int:
