@@ -23,17 +23,22 @@ __device__ __forceinline__ int wave_scan_add(int v, int lane)
     return v;
 }
 
-// Tile t when every group's positions are cut into tiles of ROWS.  Group g
-// holds positions offsets[g] .. offsets[g + 1] - 1, cut to 0 .. rows - 1
-// whatever the offsets say (a range that ends before it begins is empty).
-// Every wave of the workgroup finds the same tile by itself: 64 groups at a
-// time, a scan of their tile counts and one ballot.
+// The group that holds tile t when every group's positions are cut into tiles
+// of ROWS: its positions begin .. end - 1, its first tile and its tiles (0: no
+// such tile).  Group g holds positions offsets[g] .. offsets[g + 1] - 1, cut to
+// 0 .. rows - 1 whatever the offsets say (a range that ends before it begins
+// is empty).  Every wave of the workgroup finds the same by itself: 64 groups
+// at a time, a scan of their tile counts and one ballot.
+struct GroupSpan {
+    int group, begin, end, first, tiles;
+};
+
 template <int ROWS>
-__device__ __forceinline__ GroupTile find_tile(const int* offsets, int groups, int rows, int t)
+__device__ __forceinline__ GroupSpan find_span(const int* offsets, int groups, int rows, int t)
 {
     const int lane = threadIdx.x & 63;
     int before = 0;                        // tiles of the groups already passed
-    GroupTile r = {0, 0, 0};
+    GroupSpan r = {0, 0, 0, 0, 0};
     for (int base = 0; base < groups; base += 64) {
         const int g = base + lane;
         int lo = 0, hi = 0;
@@ -46,16 +51,70 @@ __device__ __forceinline__ GroupTile find_tile(const int* offsets, int groups, i
         const uint64_t past = __ballot(t < before + upto);
         if (past != 0) {
             const int l = __builtin_ctzll(past);
-            const int first = __builtin_amdgcn_readlane(before + upto - tiles, l);
-            const int glo = __builtin_amdgcn_readlane(lo, l);
-            const int ghi = __builtin_amdgcn_readlane(hi, l);
             r.group = base + l;
-            r.begin = glo + (t - first) * ROWS;
-            r.count = min(ROWS, ghi - r.begin);
+            r.begin = __builtin_amdgcn_readlane(lo, l);
+            r.end = __builtin_amdgcn_readlane(hi, l);
+            r.tiles = __builtin_amdgcn_readlane(tiles, l);
+            r.first = __builtin_amdgcn_readlane(before + upto, l) - r.tiles;
             return r;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
     }
+    return r;
+}
+
+// Tile t itself; count = 0: it does not exist.
+template <int ROWS>
+__device__ __forceinline__ GroupTile find_tile(const int* offsets, int groups, int rows, int t)
+{
+    const GroupSpan s = find_span<ROWS>(offsets, groups, rows, t);
+    GroupTile r = {0, 0, 0};
+    if (s.tiles > 0) {
+        r.group = s.group;
+        r.begin = s.begin + (t - s.first) * ROWS;
+        r.count = min(ROWS, s.end - r.begin);
+    }
+    return r;
+}
+
+// One workgroup's share of (tiles) x (column blocks).  Workgroup b runs on XCD
+// b % 8, so XCD x takes the x-th eighth of the list that runs over the groups,
+// their column blocks and, innermost, the group's tiles: every XCD gets as
+// many, the tiles that share a column block's weights meet in one L2, and so
+// do a group's rows.  tile.count = 0: nothing to do.
+struct GroupWork {
+    GroupTile tile;
+    int block;
+};
+
+template <int ROWS>
+__device__ __forceinline__ GroupWork find_work(const int* offsets, int groups, int rows, int blocks,
+                                               int b)
+{
+    const int lane = threadIdx.x & 63;
+    int total = 0;
+    for (int g = lane; g < groups; g += 64) {
+        const int lo = min(max(offsets[g], 0), rows);
+        const int hi = min(max(offsets[g + 1], 0), rows);
+        total += hi > lo ? (hi - lo - 1) / ROWS + 1 : 0;
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        total += __shfl_xor(total, off, 64);
+    }
+    total = __builtin_amdgcn_readfirstlane(total) * blocks;
+    const int share = (total + 7) / 8;
+    const int at = (b & 7) * share + (b >> 3);
+    GroupWork r = {{0, 0, 0}, 0};
+    if ((b >> 3) >= share || at >= total) {
+        return r;
+    }
+    const GroupSpan s = find_span<ROWS>(offsets, groups, rows, at / blocks);
+    const int in = at - s.first * blocks;              // within the group
+    r.block = in / s.tiles;
+    r.tile.group = s.group;
+    r.tile.begin = s.begin + in % s.tiles * ROWS;
+    r.tile.count = min(ROWS, s.end - r.tile.begin);
     return r;
 }
 
