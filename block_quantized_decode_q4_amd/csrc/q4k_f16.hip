@@ -3,7 +3,8 @@
 // q4k_q6k.hip) times fp16 activations on the matrix cores, f32 accumulation
 // (memra-engine 0.83.1, src/f16_ffi.rs: `memra_f16_cvt`, the f32 -> fp16
 // activation convert; `memra_f16_pp_gemm` / `try_f16_gemm`,
-// y[m, n] = x[m, k] @ (fp16 W)^T, f32 accumulate, for prefill batches).
+// y[m, n] = x[m, k] @ (fp16 W)^T, f32 accumulate, for prefill batches), and the
+// same product for rows grouped by matrix (the experts of a prompt).
 //
 // GEMM: a 256-thread workgroup computes a 128 x 128 tile of y (128 vectors x
 // 128 weight rows; 64 x 128 or 64 x 64 when that gives too few tiles to
@@ -58,15 +59,15 @@ f16_cvt_kernel(const float* __restrict__ x, _Float16* __restrict__ out, int64_t 
     }
 }
 
-// One tile of y: BM x rows by the BN mirror rows from row_w0 on (64 or 128
-// each) over all of k; four waves in a 2 x 2 layout, each with (BM / 32) x
-// (BN / 32) MFMA blocks of 16 x 16.  xrow(i) is where tile row i's x begins
-// (i < BM, readable for every i), put(i, r, v) takes y of tile row i and
-// mirror row r < n.
-template <int BM, int BN, typename XRow, typename Put>
-__device__ __forceinline__ void
-f16_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n, int k,
-         unsigned char* smem)
+// y[b * n + r] = sum_c w16[r * k + c] x16[b * k + c] (f32 accumulation).
+// Tiles of BM x rows by BN mirror rows (64 or 128 each); four waves in a
+// 2 x 2 layout, each with (BM / 32) x (BN / 32) MFMA blocks of 16 x 16.
+// Grid: kGXcd * ceil(NT / kGXcd) * MT workgroups (MT, NT: tiles of x rows
+// and of mirror rows); k % 64 == 0.
+template <int BM, int BN>
+__global__ void __launch_bounds__(256, 2)
+f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
+                float* __restrict__ y, int m, int n, int k, int MT, int NT)
 {
     static_assert((BM == 64 || BM == 128) && (BN == 64 || BN == 128), "tile");
     constexpr int LA = BM / 32;              // 16-byte loads of the x tile per thread and step
@@ -75,9 +76,22 @@ f16_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n
     constexpr int FB = BN / 32;
     constexpr int kXs = BM * kGRow;          // LDS bytes of one x tile
     constexpr int kStage = (BM + BN) * kGRow;
+    extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = tid >> 6;
+    // XCD-aware tile order: workgroup b runs on XCD b % 8; within an XCD
+    // the x tiles of one mirror tile follow each other
+    const int bid = blockIdx.x;
+    const int xcd = bid % kGXcd;
+    const int local = bid / kGXcd;
+    const int tm = local % MT;
+    const int tn = (local / MT) * kGXcd + xcd;
+    if (tn >= NT) {
+        return;
+    }
+    const int row_x0 = tm * BM;
+    const int row_w0 = tn * BN;
 
     // load role: 16 bytes of a tile row per thread and load (tile row
     // idx / 8, 16-byte chunk idx % 8 of its 128 bytes)
@@ -87,7 +101,7 @@ f16_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         const int idx = tid + 256 * i;
-        xsrc[i] = xrow(idx >> 3) + (idx & 7) * 8;
+        xsrc[i] = x16 + (int64_t)min(row_x0 + (idx >> 3), m - 1) * k + (idx & 7) * 8;
         xoff[i] = (idx >> 3) * kGRow + (idx & 7) * 16;
     }
 #pragma unroll
@@ -188,73 +202,185 @@ f16_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n
             step(kb + 1, std::integral_constant<int, 0>());
         }
     }
-    // D[4 g + r][j] of block (a, b): tile row (BM / 2) wm + 16 a + 4 g + r,
+    // D[4 g + r][j] of block (a, b): x row (BM / 2) wm + 16 a + 4 g + r,
     // mirror row (BN / 2) wn + 16 b + j
 #pragma unroll
     for (int a = 0; a < FA; ++a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            put((BM / 2) * wm + 16 * a + 4 * g + r, [&](auto out) __attribute__((always_inline)) {
+            const int xr = row_x0 + (BM / 2) * wm + 16 * a + 4 * g + r;
+            if (xr < m) {
 #pragma unroll
                 for (int b = 0; b < FB; ++b) {
                     const int wr = row_w0 + (BN / 2) * wn + 16 * b + j;
                     if (wr < n) {
-                        out(wr, acc[a][b][r]);
+                        y[(int64_t)xr * n + wr] = acc[a][b][r];
                     }
                 }
-            });
+            }
         }
     }
 }
 
-// y[b * n + r] = sum_c w16[r * k + c] x16[b * k + c] (f32 accumulation).
-// Grid: kGXcd * ceil(NT / kGXcd) * MT workgroups (MT, NT: tiles of x rows
-// and of mirror rows); k % 64 == 0.
-template <int BM, int BN>
-__global__ void __launch_bounds__(256, 2)
-f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
-                float* __restrict__ y, int m, int n, int k, int MT, int NT)
+// The grouped products' tile: BM x BN by WM x WN waves, each with a
+// (BM / WM) x (BN / WN) part.  A larger side takes less from the L2 and the LDS
+// per product, which is what bounds the 128 x 128 tile above (4096 rows in
+// eight groups, n 14336, k 4096: 757 us with it, 619 us with 128 x 256 on
+// eight waves, 780 TFLOP/s; 256 x 256 617 us, but 20-70 % slower where the
+// groups are shorter).  LDS rows of 64 halves without padding, the 16-byte piece c of row r at place
+// c ^ (r % 8): neither the stores of eight threads' 128 bytes nor the reads of
+// a 16 x 32 operand collide.  One register set: a step has twice the products
+// to hide a load behind.
+template <int BM, int BN, int WM, int WN, typename XRow, typename Put>
+__device__ __forceinline__ void
+f16_wide_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n, int k,
+              unsigned char* smem)
 {
-    extern __shared__ __align__(16) unsigned char smem[];
-    // XCD-aware tile order: workgroup b runs on XCD b % 8; within an XCD
-    // the x tiles of one mirror tile follow each other
-    const int bid = blockIdx.x;
-    const int xcd = bid % kGXcd;
-    const int local = bid / kGXcd;
-    const int tm = local % MT;
-    const int tn = (local / MT) * kGXcd + xcd;
-    if (tn >= NT) {
-        return;
+    constexpr int kThreads = 64 * WM * WN;
+    constexpr int kRows = kThreads / 8;      // tile rows per load of all threads
+    constexpr int LA = BM / kRows;           // 16-byte loads of the x tile per thread and step
+    constexpr int LB = BN / kRows;
+    constexpr int FA = BM / WM / 16;         // 16-row MFMA blocks per wave
+    constexpr int FB = BN / WN / 16;
+    constexpr int kXs = BM * kGK * 2;        // LDS bytes of one x tile
+    constexpr int kStage = (BM + BN) * kGK * 2;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int wm = wave % WM;
+    const int wn = wave / WM;
+    const int g = lane >> 4;
+    const int j = lane & 15;
+    // load role: 16 bytes of a tile row per thread and load
+    const _Float16* xsrc[LA];
+    const _Float16* wsrc[LB];
+    const int lrow = tid >> 3;
+    const int loff = lrow * 128 + (((tid & 7) ^ (lrow & 7)) << 4);       // kRows % 8 == 0
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        xsrc[i] = xrow(lrow + kRows * i) + (tid & 7) * 8;
     }
-    const int row_x0 = tm * BM;
-    f16_tile<BM, BN>(
-        w16, [&](int i) { return x16 + (int64_t)min(row_x0 + i, m - 1) * k; },
-        [&](int i, auto each) {
-            if (row_x0 + i < m) {
-                float* const out = y + (int64_t)(row_x0 + i) * n;
-                each([&](int r, float v) { out[r] = v; });
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+        wsrc[i] = w16 + (int64_t)min(row_w0 + lrow + kRows * i, n - 1) * k + (tid & 7) * 8;
+    }
+    v4u_t xa[LA], wa[LB];
+    auto load = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            xa[i] = *reinterpret_cast<const v4u_t*>(xsrc[i] + kb * kGK);
+        }
+#pragma unroll
+        for (int i = 0; i < LB; ++i) {
+            wa[i] = *reinterpret_cast<const v4u_t*>(wsrc[i] + kb * kGK);
+        }
+    };
+    auto stage = [&](int st) __attribute__((always_inline)) {
+        unsigned char* base = smem + st * kStage + loff;
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            *reinterpret_cast<v4u_t*>(base + i * (kRows * 128)) = xa[i];
+        }
+#pragma unroll
+        for (int i = 0; i < LB; ++i) {
+            *reinterpret_cast<v4u_t*>(base + kXs + i * (kRows * 128)) = wa[i];
+        }
+    };
+    f32x4_t acc[FA][FB];
+#pragma unroll
+    for (int a = 0; a < FA; ++a) {
+#pragma unroll
+        for (int b = 0; b < FB; ++b) {
+            acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+    const int KB = k / kGK;
+    load(0);
+    stage(0);
+    load(min(1, KB - 1));
+    __syncthreads();
+    for (int kb = 0; kb < KB; ++kb) {
+        const unsigned char* xs = smem + (kb & 1) * kStage + (BM / WM) * wm * 128 + j * 128;
+        const unsigned char* ws = smem + (kb & 1) * kStage + kXs + (BN / WN) * wn * 128 + j * 128;
+#pragma unroll
+        for (int s = 0; s < kGK / 32; ++s) {
+            const int c = ((4 * s + g) ^ (j & 7)) << 4;
+            half8_t av[FA], bv[FB];
+#pragma unroll
+            for (int a = 0; a < FA; ++a) {
+                av[a] = *reinterpret_cast<const half8_t*>(xs + a * 2048 + c);
             }
-        },
-        tn * BN, n, k, smem);
+#pragma unroll
+            for (int b = 0; b < FB; ++b) {
+                bv[b] = *reinterpret_cast<const half8_t*>(ws + b * 2048 + c);
+            }
+#pragma unroll
+            for (int a = 0; a < FA; ++a) {
+#pragma unroll
+                for (int b = 0; b < FB; ++b) {
+                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av[a], bv[b], acc[a][b],
+                                                                       0, 0, 0);
+                }
+            }
+        }
+        stage((kb + 1) & 1);
+        load(min(kb + 2, KB - 1));
+        // the order of a step's instructions (masks: 0x8 matrix, 0x100 LDS
+        // read, 0x200 LDS write, 0x20 load): operand reads run ahead of the
+        // products that take them, then a store or a load after each product
+        // (128 x 256: 639 -> 619 us on the shape below)
+        constexpr int kReads = 2 * (FA + FB);
+        constexpr int kAhead = FB + 3;
+        constexpr int kMfma = 2 * FA * FB;
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int i = 0; i < kReads - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < LA + LB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < LA + LB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, kMfma, 0);
+        __syncthreads();
+    }
+    // D[4 g + r][j] of block (a, b)
+#pragma unroll
+    for (int a = 0; a < FA; ++a) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            put((BM / WM) * wm + 16 * a + 4 * g + r,
+                [&](auto out) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int b = 0; b < FB; ++b) {
+                        const int wr = row_w0 + (BN / WN) * wn + 16 * b + j;
+                        if (wr < n) {
+                            out(wr, acc[a][b][r]);
+                        }
+                    }
+                });
+        }
+    }
 }
 
-// The same product for rows grouped by matrix: tile tm holds up to BM
-// positions of one group (MT: the most tiles there can be), its mirror is the
-// group's.  Positions that are left out read x row 0 and are not written.
-template <int BM, int BN>
-__global__ void __launch_bounds__(256, 2)
+// The same product for rows grouped by matrix: a tile holds up to BM positions
+// of one group, its mirror is the group's; NT column blocks of BN.  Positions
+// that are left out read x row 0 and are not written.
+template <int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, WM * WN / 4)
 f16_gemm_grouped_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
-                        float* __restrict__ y, GroupRows rows, int n, int k, int MT, int NT)
+                        float* __restrict__ y, GroupRows rows, int n, int k, int NT)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    const int bid = blockIdx.x;
-    const int xcd = bid % kGXcd;
-    const int local = bid / kGXcd;
-    const int tn = (local / MT) * kGXcd + xcd;
-    if (tn >= NT) {
-        return;
-    }
-    const GroupTile t = find_tile<BM>(rows.offsets, rows.groups, rows.rows, local % MT);
+    const GroupWork work = find_work<BM>(rows.offsets, rows.groups, rows.rows, NT, blockIdx.x);
+    const GroupTile t = work.tile;
     if (t.count == 0) {
         return;
     }
@@ -266,19 +392,18 @@ f16_gemm_grouped_kernel(const _Float16* __restrict__ w16, const _Float16* __rest
         const int r = rows.x_rows ? rows.x_rows[p] : p;
         return r < 0 || r / rows.x_div >= rows.x_count ? -1 : r / rows.x_div;
     };
-    f16_tile<BM, BN>(
-        w16 + (int64_t)t.group * n * k,
-        [&](int i) { return x16 + (int64_t)max(x_row(i), 0) * k; },
-        [&](int i, auto each) {
-            if (x_row(i) >= 0) {
-                const int r = rows.y_rows ? rows.y_rows[t.begin + i] : t.begin + i;
-                if (r >= 0 && r < rows.y_count) {
-                    float* const out = y + (int64_t)r * n;
-                    each([&](int c, float v) { out[c] = v; });
-                }
+    const auto xrow = [&](int i) { return x16 + (int64_t)max(x_row(i), 0) * k; };
+    const auto put = [&](int i, auto each) {
+        if (x_row(i) >= 0) {
+            const int r = rows.y_rows ? rows.y_rows[t.begin + i] : t.begin + i;
+            if (r >= 0 && r < rows.y_count) {
+                float* const out = y + (int64_t)r * n;
+                each([&](int c, float v) { out[c] = v; });
             }
-        },
-        tn * BN, n, k, smem);
+        }
+    };
+    const _Float16* const w = w16 + (int64_t)t.group * n * k;
+    f16_wide_tile<BM, BN, WM, WN>(w, xrow, put, work.block * BN, n, k, smem);
 }
 
 hipError_t launch_f16_cvt(const float* x, void* out, int64_t count, hipStream_t stream)
@@ -347,49 +472,49 @@ hipError_t launch_f16_gemm(const void* w16, const void* x16, float* y, int m, in
     return launch_f16_gemm_t<64, 64>(w16, x16, y, m, n, k, stream);
 }
 
-// The grouped product's tile: 128 positions where the groups hold about that
-// many, else 64 (a tile never spans groups); 128 mirror rows while that gives
-// a tile for every CU.
-void f16_grouped_tile(int64_t rows, int64_t groups, int64_t n, int* bm, int* bn)
+// The tile: 128 x 256 where the groups hold about a tile's positions and there
+// are at least half as many tiles as CUs, else 64 x 128, where a product is
+// mostly the mirror's bytes or the tiles are few.  Both sides measured: 128 x
+// 256 against 64 x 128 at 256 positions a group and 176 tiles 71 / 88 us, at
+// 128 positions and 900 tiles 139 / 138 us; at 64 positions and 176 tiles
+// 84 / 75 us, at 256 positions and 46 tiles 23 / 14 us.
+static bool f16_grouped_wide(int64_t rows, int64_t groups, int64_t n)
 {
-    *bm = rows >= 96 * groups ? 128 : 64;
-    *bn = most_tiles(rows, groups, *bm) * ((n + 127) / 128) >= 256 ? 128 : 64;
-    *bm = *bn == 64 ? 64 : *bm;
+    return rows >= 96 * groups && most_tiles(rows, groups, 128) * ((n + 255) / 256) >= 128;
+}
+
+template <int BM, int BN>
+static int64_t f16_grouped_tiles(int64_t rows, int64_t groups, int64_t n)
+{
+    return (most_tiles(rows, groups, BM) * ((n + BN - 1) / BN) + 7) / 8 * 8;
 }
 
 int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n)
 {
-    int bm, bn;
-    f16_grouped_tile(rows, groups, n, &bm, &bn);
-    const int64_t NT = (n + bn - 1) / bn;
-    return kGXcd * ((NT + kGXcd - 1) / kGXcd) * most_tiles(rows, groups, bm);
+    return f16_grouped_wide(rows, groups, n) ? f16_grouped_tiles<128, 256>(rows, groups, n)
+                                             : f16_grouped_tiles<64, 128>(rows, groups, n);
 }
 
-template <int BM, int BN>
+template <int BM, int BN, int WM, int WN>
 static hipError_t launch_f16_grouped_t(const void* w16, const void* x16, float* y,
                                        const GroupRows& g, int n, int k, hipStream_t stream)
 {
-    const int MT = (int)most_tiles(g.rows, g.groups, BM);
     const int NT = (n + BN - 1) / BN;
-    const int64_t grid = (int64_t)kGXcd * ((NT + kGXcd - 1) / kGXcd) * MT;
-    hipLaunchKernelGGL((f16_gemm_grouped_kernel<BM, BN>), dim3((unsigned)grid), dim3(256),
-                       f16_gemm_lds_bytes(BM, BN), stream, static_cast<const _Float16*>(w16),
-                       static_cast<const _Float16*>(x16), y, g, n, k, MT, NT);
+    const int64_t grid = f16_grouped_tiles<BM, BN>(g.rows, g.groups, n);
+    hipLaunchKernelGGL((f16_gemm_grouped_kernel<BM, BN, WM, WN>), dim3((unsigned)grid),
+                       dim3(64 * WM * WN), 2 * (BM + BN) * kGK * 2, stream,
+                       static_cast<const _Float16*>(w16), static_cast<const _Float16*>(x16), y, g,
+                       n, k, NT);
     return hipGetLastError();
 }
 
 hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
                                    int n, int k, hipStream_t stream)
 {
-    int bm, bn;
-    f16_grouped_tile(g.rows, g.groups, n, &bm, &bn);
-    if (bm == 128) {
-        return launch_f16_grouped_t<128, 128>(w16, x16, y, g, n, k, stream);
+    if (f16_grouped_wide(g.rows, g.groups, n)) {
+        return launch_f16_grouped_t<128, 256, 2, 4>(w16, x16, y, g, n, k, stream);
     }
-    if (bn == 128) {
-        return launch_f16_grouped_t<64, 128>(w16, x16, y, g, n, k, stream);
-    }
-    return launch_f16_grouped_t<64, 64>(w16, x16, y, g, n, k, stream);
+    return launch_f16_grouped_t<64, 128, 2, 4>(w16, x16, y, g, n, k, stream);
 }
 
 // ------------------------------------------------- allocation-free variant

@@ -154,6 +154,30 @@ def test_grouped_sizes(kind, sizes, n, k):
     _check(kind, W, x, off, np.arange(rows), np.arange(rows), y0, got, n, k)
 
 
+def test_grouped_f16_wide_tiles():
+    """Shapes that take the 128 x 256 tile (groups of about a tile or more and
+    enough of them), ragged in rows and columns; sampled columns."""
+    rng = np.random.default_rng(14)
+    for sizes, n, k in (([300, 0, 5, 190], 8229, 128), ([129, 128, 127], 12300, 192)):
+        groups, rows = len(sizes), sum(sizes)
+        w = torch.randn((groups, n, k), generator=torch.Generator("cuda").manual_seed(n),
+                        device="cuda").mul_(0.05).half()
+        x = rng.standard_normal((rows, k)).astype(np.float16)
+        off = _offsets(sizes)
+        print("grouped f16 wide sizes=%s n=%d k=%d" % (sizes, n, k), flush=True)
+        y = torch.full((rows, n), float("nan"), device="cuda")
+        perm = torch.from_numpy(rng.permutation(rows).astype(np.int32)).cuda()
+        q4k.q4k_f16_gemm_grouped(w, torch.from_numpy(x).cuda(), y, _i32(off), n, k, groups, rows,
+                                 y_rows=perm)
+        got = y.cpu().numpy()[perm.cpu().numpy()]
+        wf = w.cpu().numpy().astype(np.float64)
+        for g in range(groups):
+            part = slice(off[g], off[g + 1])
+            ref = x[part].astype(np.float64) @ wf[g].T
+            tol = k * 2.0 ** -23 * (np.abs(x[part].astype(np.float64)) @ np.abs(wf[g]).T)
+            assert (np.abs(got[part] - ref) <= tol).all()
+
+
 @pytest.mark.parametrize("kind", ["f32", "q8", "f16"])
 def test_grouped_rows_gathered_scattered_and_left_out(kind):
     """Offsets that leave positions before and behind the groups, x by token,
