@@ -5,19 +5,29 @@
 //
 // Two launches, because every output needs all of A x: lora_down_kernel
 // writes v = scale A x (f32, rows x r rounded up to 16) to the caller's
-// workspace, lora_up_kernel adds B v to the base.  Both take tiles of 16 rows
-// of one adapter (q4k_groups.h), so an adapter is read once per 16 of its
-// rows.
+// workspace, lora_up_kernel adds B v to the base.  A workgroup takes a tile of
+// rows of one adapter (q4k_groups.h).
 //
 // x in binary16 goes through v_mfma_f32_16x16x32_f16; f32 (and bfloat16)
-// x through v_mfma_f32_16x16x4_f32 with A widened to f32, as does B v: no
-// operand is rounded, the sums are f32.  A row or column of an adapter at or
-// beyond its rank is never read, whatever it holds.
+// x through v_mfma_f32_16x16x4_f32 with A widened to f32; no operand is
+// rounded.  For B v each row's v, scaled by the power of two that brings its
+// largest into [2^14, 2^15), is two binary16 numbers: hi and the rest, lo, which
+// leaves at most 2^-22 of the value or 2^-39 of the row's largest, and both go
+// through the f16 matrix cores into one f32 sum (an eighth of the f32
+// instruction's time, and no widened B in registers).  What an adapter holds at or beyond its rank does not matter.
 //
-// Down: the sixteen waves of a workgroup share k, 64 ranks at a time (x is read
-// once for r <= 64), and add up their parts in LDS in wave order.  Up: bound
-// by reading the base and writing y; B's rows are the matrix operand's rows,
-// so a lane holds four consecutive columns of one y row (16-byte accesses).
+// Down: 16 rows times up to 64 ranks; the waves of `parts` workgroups share k
+// (few rows: more parts, to fill the chip), a workgroup adds its waves up in
+// LDS, and the up kernel adds the parts, always in the same order.  Up: 32
+// rows times 256 columns (64 rows read B half as often and leave too few
+// workgroups to hide the loads: slower).
+//
+// Everything passes through LDS: the matrix operands' lane order (a row's
+// lanes 16 apart) would take 64 clocks of the vector cache per load where
+// neighbouring lanes on neighbouring bytes take about 20, and that bound both
+// kernels.  2048 rows at rank 64, n = k = 4096, x binary16 (84 MB): down
+// 20 -> 10 us, up 27 -> 21 us; 24 rows of 16 adapters at rank 16: down
+// 11.5 -> 5.7 us, up 6 us, both the latency of a handful of dependent loads.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -31,12 +41,14 @@ namespace {
 
 typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
-typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kTile = 16;              // rows per tile
+constexpr int kTile = 16;              // rows per down tile
 constexpr int kRanks = 4;              // rank tiles of 16 per down workgroup
-constexpr int kDownWaves = 16;
+constexpr int kDownWaves = 8;
+constexpr int kUpTile = 32;            // rows per up tile
+constexpr int kUpCols = 256;           // columns per up workgroup
 
 __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter)
 {
@@ -50,94 +62,132 @@ __device__ __forceinline__ int row_of(const LoraArgs& a, int p)
     return r >= 0 && r < a.rows ? r : -1;
 }
 
-// Eight consecutive x elements, as the matrix operands take them
-template <int TYPE>
-struct X8 {
-    f4_t lo, hi;                               // f32 (bfloat16 widened)
-};
-template <>
-struct X8<kTypeF16> {
-    h8_t v;
-};
-
-template <int TYPE>
-__device__ __forceinline__ X8<TYPE> load_x8(const void* base, int64_t at)
+// The place of 16-byte piece p of row r in LDS rows of 128 bytes (eight
+// pieces) or 64 (four): the 16 rows' reads of a piece do not collide.
+__device__ __forceinline__ int at128(int r, int p)
 {
-    X8<TYPE> r;
-    if constexpr (TYPE == kTypeF16) {
-        r.v = *reinterpret_cast<const h8_t*>(static_cast<const _Float16*>(base) + at);
-    } else if constexpr (TYPE == kTypeF32) {
-        const float* p = static_cast<const float*>(base) + at;
-        r.lo = *reinterpret_cast<const f4_t*>(p);
-        r.hi = *reinterpret_cast<const f4_t*>(p + 4);
-    } else {
-        const u16x8_t v =
-            *reinterpret_cast<const u16x8_t*>(static_cast<const uint16_t*>(base) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            r.lo[i] = __builtin_bit_cast(float, (uint32_t)v[i] << 16);
-            r.hi[i] = __builtin_bit_cast(float, (uint32_t)v[i + 4] << 16);
-        }
-    }
-    return r;
+    return r * 128 + ((p ^ (r & 7)) << 4);
 }
 
-// One wave's part of v for the tile: k steps of 32 from wave * 32 on, every
-// kDownWaves-th, U of them in flight.  acc[i]: rank tile i.
-template <int TYPE, int NT, int U>
-__device__ __forceinline__ void down_part(const LoraArgs& a, int64_t xat, bool there, int group,
-                                          int rank0, int rank, f4_t* acc)
+__device__ __forceinline__ int at64(int r, int p)
 {
+    return r * 64 + ((p ^ ((r >> 3 & 1) * 3)) << 4);
+}
+
+// A step of a wave: 128 bytes of each x row (32 f32 or 64 16-bit elements) and
+// the same elements of the A rows.
+template <int TYPE>
+constexpr int kStep = TYPE == kTypeF32 ? 32 : 64;
+template <int TYPE, int NT>
+constexpr int kDownLds = 16 * 128 + NT * 16 * 2 * kStep<TYPE>;
+
+// One wave's part of v for the tile: every `stride`-th step from `first` on.
+// acc[i]: rank tile i.  lds: the wave's own kDownLds bytes.
+template <int TYPE, int NT>
+__device__ __forceinline__ void down_part(const LoraArgs& a, const GroupTile& t, int rank0,
+                                          int rank, int first, int stride, unsigned char* lds,
+                                          f4_t* acc)
+{
+    constexpr int K = kStep<TYPE>;
+    constexpr int kSize = TYPE == kTypeF32 ? 4 : 2;
+    constexpr int LA = NT * 16 * 2 * K / 1024;   // 1 KB loads of A
+    constexpr int kPieces = 2 * K / 16;          // 16-byte pieces of an A row
     const int lane = threadIdx.x & 63;
     const int j = lane & 15;
     const int g = lane >> 4;
-    // rank tile i: this lane's row of A, read only below the rank
-    const _Float16* arow[NT];
-    bool has[NT];
+    unsigned char* const alds = lds + 16 * 128;
+    // load roles: eight rows of 128 bytes of x, 512 / K rows of A at a time
+    const char* xsrc[2];
+    const char* asrc[LA];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int slot = 8 * i + (lane >> 3);
+        const int row = slot < t.count ? row_of(a, t.begin + slot) : -1;
+        xsrc[i] = row >= 0 ? static_cast<const char*>(a.x) + (int64_t)row * a.k * kSize +
+                                 (lane & 7) * 16
+                           : nullptr;
+    }
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const int rr = rank0 + i * (64 / kPieces) + lane / kPieces;
+        asrc[i] = rr < rank ? static_cast<const char*>(a.a) +
+                                  ((int64_t)t.group * a.r + rr) * a.k * 2 + (lane % kPieces) * 16
+                            : nullptr;
+    }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const int rr = rank0 + 16 * i + j;
-        has[i] = rr < rank;
-        arow[i] = static_cast<const _Float16*>(a.a) +
-                  ((int64_t)group * a.r + (has[i] ? rr : 0)) * a.k;
         acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
     }
-    for (int k0 = (threadIdx.x >> 6) * 32; k0 < a.k; k0 += 32 * kDownWaves * U) {
-        X8<TYPE> x[U];
-        h8_t w[U][NT];
+    u4_t xv[2], av[LA];
+    auto load = [&](int st) __attribute__((always_inline)) {
+        // beyond k: zeros for both (k % 8 == 0: pieces are whole)
+        const bool xin = st * K + (lane & 7) * (16 / kSize) < a.k;
+        const bool ain = st * K + (lane % kPieces) * 8 < a.k;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = k0 + u * 32 * kDownWaves + 8 * g;
-            const bool in = at < a.k;          // k % 8 == 0: all eight or none
-            x[u] = X8<TYPE>{};
-            if (there && in) {
-                x[u] = load_x8<TYPE>(a.x, xat + at);
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                w[u][i] = h8_t{0, 0, 0, 0, 0, 0, 0, 0};
-                if (has[i] && in) {
-                    w[u][i] = *reinterpret_cast<const h8_t*>(arow[i] + at);
-                }
+        for (int i = 0; i < 2; ++i) {
+            xv[i] = u4_t{0u, 0u, 0u, 0u};
+            if (xsrc[i] != nullptr && xin) {
+                xv[i] = *reinterpret_cast<const u4_t*>(xsrc[i] + (int64_t)st * 128);
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int i = 0; i < LA; ++i) {
+            av[i] = u4_t{0u, 0u, 0u, 0u};
+            if (asrc[i] != nullptr && ain) {
+                av[i] = *reinterpret_cast<const u4_t*>(asrc[i] + (int64_t)st * (2 * K));
+            }
+        }
+    };
+    const int steps = (a.k + K - 1) / K;
+    if (first < steps) {
+        load(first);
+    }
+    for (int st = first; st < steps; st += stride) {
+        // one wave's LDS accesses are in order: no barrier
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<u4_t*>(lds + at128(8 * i + (lane >> 3), lane & 7)) = xv[i];
+        }
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            const int row = i * (64 / kPieces) + lane / kPieces;
+            const int at = kPieces == 8 ? at128(row, lane % kPieces) : at64(row, lane % kPieces);
+            *reinterpret_cast<u4_t*>(alds + at) = av[i];
+        }
+        if (st + stride < steps) {
+            load(st + stride);
+        }
+        if constexpr (TYPE == kTypeF32) {
+            const f4_t lo = *reinterpret_cast<const f4_t*>(lds + at128(j, 2 * g));
+            const f4_t hi = *reinterpret_cast<const f4_t*>(lds + at128(j, 2 * g + 1));
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                if constexpr (TYPE == kTypeF16) {
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[u].v, w[u][i], acc[i], 0, 0,
-                                                                    0);
-                } else {
+                const h8_t w = *reinterpret_cast<const h8_t*>(alds + i * 1024 + at64(j, g));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            x[u].lo[c], (float)w[u][i][c], acc[i], 0, 0, 0);
-                    }
+                for (int c = 0; c < 8; ++c) {
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(c < 4 ? lo[c & 3] : hi[c & 3],
+                                                                  (float)w[c], acc[i], 0, 0, 0);
+                }
+            }
+        } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            x[u].hi[c], (float)w[u][i][c + 4], acc[i], 0, 0, 0);
+            for (int s = 0; s < 2; ++s) {
+                const u4_t xw = *reinterpret_cast<const u4_t*>(lds + at128(j, 4 * s + g));
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const h8_t w =
+                        *reinterpret_cast<const h8_t*>(alds + i * 2048 + at128(j, 4 * s + g));
+                    if constexpr (TYPE == kTypeF16) {
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            __builtin_bit_cast(h8_t, xw), w, acc[i], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t two = xw[c / 2];
+                            const uint32_t one = c % 2 ? two & 0xFFFF0000u : two << 16;
+                            acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                __builtin_bit_cast(float, one), (float)w[c], acc[i], 0, 0, 0);
+                        }
                     }
                 }
             }
@@ -145,12 +195,15 @@ __device__ __forceinline__ void down_part(const LoraArgs& a, int64_t xat, bool t
     }
 }
 
-// v[p][rank] for the tile's positions and 64 ranks from blockIdx.y * 64 on
+// v[part][p][rank] for the tile's positions, 64 ranks from blockIdx.y * 64 on,
+// part blockIdx.z of k
 template <int TYPE>
 __global__ void __launch_bounds__(64 * kDownWaves)
 lora_down_kernel(LoraArgs a)
 {
-    __shared__ f4_t part[kDownWaves][kRanks][64];
+    constexpr int kLds = kDownLds<TYPE, kRanks>;
+    static_assert(kLds >= kRanks * 1024, "the waves' sums take the same place");
+    __shared__ __align__(16) unsigned char smem[kDownWaves][kLds];
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     const int j = lane & 15;
@@ -164,25 +217,23 @@ lora_down_kernel(LoraArgs a)
     if (rank0 >= rank) {
         return;
     }
-    const int row = j < t.count ? row_of(a, t.begin + j) : -1;
-    const bool there = row >= 0;
-    const int64_t xat = (int64_t)(there ? row : 0) * a.k;
     f4_t acc[kRanks];
-    // as many rank tiles as the adapter has; steps in flight by the registers
-    // that leaves
     const int left = rank - rank0;
+    const int first = blockIdx.z * kDownWaves + wave;
+    const int stride = gridDim.z * kDownWaves;
+    // as many rank tiles as the adapter has
     if (left <= 16) {
-        down_part<TYPE, 1, TYPE == kTypeF16 ? 8 : 4>(a, xat, there, t.group, rank0, rank, acc);
+        down_part<TYPE, 1>(a, t, rank0, rank, first, stride, smem[wave], acc);
     } else if (left <= 32) {
-        down_part<TYPE, 2, 4>(a, xat, there, t.group, rank0, rank, acc);
+        down_part<TYPE, 2>(a, t, rank0, rank, first, stride, smem[wave], acc);
     } else {
-        down_part<TYPE, 4, TYPE == kTypeF16 ? 4 : 2>(a, xat, there, t.group, rank0, rank, acc);
+        down_part<TYPE, 4>(a, t, rank0, rank, first, stride, smem[wave], acc);
     }
-    const int tiles = left <= 16 ? 1 : left <= 32 ? 2 : 4;
+    f4_t* const mine = reinterpret_cast<f4_t*>(smem[wave]);
 #pragma unroll
     for (int i = 0; i < kRanks; ++i) {
-        if (i < tiles) {
-            part[wave][i][lane] = acc[i];
+        if (16 * i < left) {
+            mine[i * 64 + lane] = acc[i];
         }
     }
     __syncthreads();
@@ -190,135 +241,283 @@ lora_down_kernel(LoraArgs a)
     if (i >= kRanks || 16 * i >= left) {
         return;
     }
-    f4_t sum = part[0][i][lane];
+    f4_t sum = reinterpret_cast<const f4_t*>(smem[0])[i * 64 + lane];
 #pragma unroll
     for (int w = 1; w < kDownWaves; ++w) {
-        sum += part[w][i][lane];
+        sum += reinterpret_cast<const f4_t*>(smem[w])[i * 64 + lane];
     }
     const float scale = a.scales ? a.scales[t.group] : 1.f;
-    // D[4 g + c][j]: position 4 g + c, rank j; zero at ranks that are not there
+    // D[4 g + c][j]: position 4 g + c, rank j
     const int pitch = (a.r + 15) / 16 * 16;
     const int rr = rank0 + 16 * i + j;
+    float* const v = a.v + (int64_t)blockIdx.z * a.rows * pitch;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int slot = 4 * g + c;
         if (slot < t.count) {
-            a.v[(int64_t)(t.begin + slot) * pitch + rr] = rr < rank ? scale * sum[c] : 0.f;
+            v[(int64_t)(t.begin + slot) * pitch + rr] = scale * sum[c];
         }
     }
 }
 
-// y of the tile's positions, 64 columns per wave from blockIdx.y * 256 on.
-// VB: rows of B are multiples of four halves; VY: rows of y and base
-// multiples of four floats.  The base is the accumulators' start.
+// y of a tile of 32 positions, 256 columns from blockIdx.y * 256 on, 64 per
+// wave; 64 ranks of v and B at a time in LDS.  VB: rows of B are multiples of
+// eight halves; VY: rows of y and base multiples of four floats.
+constexpr int kBPitch = 72;            // halves per row of v or B (9 pieces of 16 bytes)
+constexpr int kYPitch = kUpCols + 4;   // floats per row of the products (65 pieces)
+
 template <bool VB, bool VY>
-__global__ void __launch_bounds__(256)
-lora_up_kernel(LoraArgs a)
+__global__ void __launch_bounds__(256, 3)
+lora_up_kernel(LoraArgs a, int parts)
 {
-    const int lane = threadIdx.x & 63;
+    constexpr int kVBytes = kUpTile * kBPitch * 2;
+    constexpr int kLds = 2 * kVBytes + kUpCols * kBPitch * 2;
+    static_assert(kUpTile * kYPitch * 4 <= kLds, "operands and products share LDS");
+    constexpr int U = kUpTile / 16;
+    constexpr int kOwn = kUpTile / 4;          // rows that a wave writes
+    __shared__ __align__(16) unsigned char smem[kLds];
+    __shared__ int exps[kUpTile];              // the rows' scales
+    _Float16* const vs = reinterpret_cast<_Float16*>(smem);            // hi, then lo
+    _Float16* const bs = reinterpret_cast<_Float16*>(smem + 2 * kVBytes);
+    float* const ys = reinterpret_cast<float*>(smem);
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
     const int j = lane & 15;
     const int g = lane >> 4;
-    const int col0 = (int)blockIdx.y * 256 + (threadIdx.x >> 6) * 64;
-    const GroupTile t = find_tile<kTile>(a.offsets, a.adapters, a.rows, blockIdx.x);
-    if (t.count == 0 || col0 >= a.n) {
+    const int col0 = (int)blockIdx.y * kUpCols;
+    const GroupTile t = find_tile<kUpTile>(a.offsets, a.adapters, a.rows, blockIdx.x);
+    if (t.count == 0) {
         return;
     }
     const int rank = rank_of(a, t.group);
-    const int row = j < t.count ? row_of(a, t.begin + j) : -1;
     const int pitch = (a.r + 15) / 16 * 16;
-    const float* v = a.v + (int64_t)(t.begin + min(j, t.count - 1)) * pitch + 4 * g;
-    // D[4 g + c][j]: column col0 + 16 i + 4 g + c of position j
-    f4_t acc[4];
-    const _Float16* b[4];
+    const _Float16* const bg = static_cast<const _Float16*>(a.b) + (int64_t)t.group * a.n * a.r;
+    const f4_t zero = {0.f, 0.f, 0.f, 0.f};
+    f4_t total[U][4];                          // [16 positions][16 columns]
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = col0 + 16 * i + 4 * g;
-        const int64_t o = (int64_t)row * a.n + at;
-        acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
-        if (a.base != nullptr && row >= 0) {
-            if constexpr (VY) {
-                if (at < a.n) {                        // n % 4 == 0: all four or none
-                    acc[i] = *reinterpret_cast<const f4_t*>(a.base + o);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    acc[i][c] = at + c < a.n ? a.base[o + c] : 0.f;
-                }
-            }
-        }
-        // B row of this lane, as a matrix row
-        const int col = min(col0 + 16 * i + j, a.n - 1);
-        b[i] = static_cast<const _Float16*>(a.b) + ((int64_t)t.group * a.n + col) * a.r + 4 * g;
-    }
-    for (int k0 = 0; k0 < rank; k0 += 16) {
-        const int left = rank - k0 - 4 * g;            // ranks of this lane's four
-        const f4_t vv = *reinterpret_cast<const f4_t*>(v + k0);
-        h4_t bv[4];
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            bv[i] = h4_t{0, 0, 0, 0};
-            if (VB && left >= 4) {
-                bv[i] = *reinterpret_cast<const h4_t*>(b[i] + k0);
-            } else {
+            total[u][i] = zero;
+        }
+    }
+    for (int k0 = 0; k0 < rank; k0 += 64) {
+        if (k0 > 0) {
+            __syncthreads();
+        }
+        const int left = rank - k0;
+        // v: positions x 16 quads of ranks, the parts added up; zeros at ranks
+        // and positions that are not there
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int p = 16 * i + (tid >> 4);
+            const int q = (tid & 15) * 4;
+            f4_t sum = {0.f, 0.f, 0.f, 0.f};
+            if (p < t.count && q < left) {
+                const float* src = a.v + (int64_t)(t.begin + p) * pitch + k0 + q;
+                sum = *reinterpret_cast<const f4_t*>(src);
+                for (int z = 1; z < parts; ++z) {
+                    sum += *reinterpret_cast<const f4_t*>(src + (int64_t)z * a.rows * pitch);
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    bv[i][c] = c < left ? b[i][k0 + c] : (_Float16)0;
+                    sum[c] = q + c < left ? sum[c] : 0.f;
+                }
+            }
+            // the 16 lanes of a position
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                top = fmaxf(top, fabsf(sum[c]));
+            }
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) {
+                top = fmaxf(top, __shfl_xor(top, off, 64));
+            }
+            int e = 15;                                // none for zeros and infinities
+            if (top > 0.f && top < __builtin_inff()) {
+                (void)frexpf(top, &e);
+            }
+            h4_t hi, lo;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float x = ldexpf(sum[c], 15 - e);
+                hi[c] = (_Float16)x;
+                lo[c] = (_Float16)(x - (float)hi[c]);
+            }
+            *reinterpret_cast<h4_t*>(vs + p * kBPitch + q) = hi;
+            *reinterpret_cast<h4_t*>(vs + kUpTile * kBPitch + p * kBPitch + q) = lo;
+            if ((tid & 15) == 0) {
+                exps[p] = e - 15;
+            }
+        }
+        if constexpr (VB) {
+            const int q = (tid & 7) * 8;
+            u4_t keep;                                 // the halves below the rank
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int have = left - q - 2 * d;
+                keep[d] = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
+            }
+            u4_t w[kUpCols / 32];
+#pragma unroll
+            for (int i = 0; i < kUpCols / 32; ++i) {
+                const int c = min(col0 + 32 * i + (tid >> 3), a.n - 1);        // rows beyond n: any
+                w[i] = u4_t{0u, 0u, 0u, 0u};
+                if (q < left) {
+                    w[i] = *reinterpret_cast<const u4_t*>(bg + (int64_t)c * a.r + k0 + q);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kUpCols / 32; ++i) {
+                *reinterpret_cast<u4_t*>(bs + (32 * i + (tid >> 3)) * kBPitch + q) = w[i] & keep;
+            }
+        } else {
+            // a row of B per wave and load, a rank per lane
+#pragma unroll 16
+            for (int c = wave; c < kUpCols; c += 4) {
+                _Float16 w = (_Float16)0;
+                if (col0 + c < a.n && lane < left) {
+                    w = bg[(int64_t)(col0 + c) * a.r + k0 + lane];
+                }
+                bs[c * kBPitch + lane] = w;
+            }
+        }
+        __syncthreads();
+        f4_t acc[U][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (32 * s < left || s == 0) {
+                h8_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = *reinterpret_cast<const h8_t*>(
+                        bs + (wave * 64 + 16 * i + j) * kBPitch + 32 * s + 8 * g);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const _Float16* const vp = vs + (16 * u + j) * kBPitch + 32 * s + 8 * g;
+                    const h8_t hi = *reinterpret_cast<const h8_t*>(vp);
+                    const h8_t lo = *reinterpret_cast<const h8_t*>(vp + kUpTile * kBPitch);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acc[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            w[i], hi, s == 0 ? zero : acc[u][i], 0, 0, 0);
+                        acc[u][i] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i], lo, acc[u][i], 0, 0, 0);
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int u = 0; u < U; ++u) {
+            const int e = exps[16 * u + j];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)bv[i][c], vv[c], acc[i], 0, 0,
-                                                              0);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    total[u][i][c] += ldexpf(acc[u][i][c], e);
+                }
             }
         }
     }
-    if (row < 0) {
-        return;
+    __syncthreads();
+    // D[4 g + c][j] of (u, i): column 16 i + 4 g + c of position 16 u + j
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<f4_t*>(ys + (16 * u + j) * kYPitch + wave * 64 + 16 * i + 4 * g) =
+                total[u][i];
+        }
+    }
+    // the base of the rows that this wave will write: positions wave, wave + 4,
+    // ...  (a row of y is this wave's alone, so base may be y)
+    int row[kOwn];
+    f4_t base[kOwn];
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+        const int p = wave + 4 * q;
+        row[q] = p < t.count ? row_of(a, t.begin + p) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = col0 + 16 * i + 4 * g;
-        const int64_t o = (int64_t)row * a.n + at;
+    for (int q = 0; q < kOwn; ++q) {
+        base[q] = f4_t{0.f, 0.f, 0.f, 0.f};
+        if (row[q] >= 0 && a.base != nullptr) {
+            if constexpr (VY) {
+                const int c = col0 + 4 * lane;
+                if (c < a.n) {                         // n % 4 == 0: all four or none
+                    base[q] = *reinterpret_cast<const f4_t*>(a.base + (int64_t)row[q] * a.n + c);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = col0 + 64 * e + lane;
+                    if (c < a.n) {
+                        base[q][e] = a.base[(int64_t)row[q] * a.n + c];
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // whole rows of 256 columns
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+        if (row[q] < 0) {
+            continue;
+        }
+        const float* const yp = ys + (wave + 4 * q) * kYPitch;
+        float* const out = a.y + (int64_t)row[q] * a.n;
         if constexpr (VY) {
-            if (at < a.n) {
-                *reinterpret_cast<f4_t*>(a.y + o) = acc[i];
+            const int c = col0 + 4 * lane;
+            if (c < a.n) {
+                *reinterpret_cast<f4_t*>(out + c) =
+                    base[q] + *reinterpret_cast<const f4_t*>(yp + 4 * lane);
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (at + c < a.n) {
-                    a.y[o + c] = acc[i][c];
+            for (int e = 0; e < 4; ++e) {
+                const int c = col0 + 64 * e + lane;
+                if (c < a.n) {
+                    out[c] = base[q][e] + yp[64 * e + lane];
                 }
             }
         }
     }
+}
+
+// Parts of k: enough workgroups for the chip.  (Sums of v are the caller's
+// workspace, so by the rows alone.)
+int down_parts(int64_t rows)
+{
+    return rows <= 512 ? 4 : rows <= 4096 ? 2 : 1;
 }
 
 }  // namespace
 
 size_t lora_ws_bytes(int64_t rows, int64_t r)
 {
-    return (size_t)rows * (size_t)((r + 15) / 16 * 16) * sizeof(float);
+    return (size_t)down_parts(rows) * (size_t)rows * (size_t)((r + 15) / 16 * 16) * sizeof(float);
 }
 
-// The grids: at most 2^32 threads, 65535 workgroups along y
+// The grids: fewer than 2^32 threads, 65535 workgroups along y
 bool lora_fits(int64_t rows, int64_t adapters, int64_t n, int64_t r)
 {
-    const int64_t tiles = most_tiles(rows, adapters, kTile);
-    const int64_t down = (r + 16 * kRanks - 1) / (16 * kRanks);
-    const int64_t up = (n + 255) / 256;
+    const int64_t down = most_tiles(rows, adapters, kTile) *
+                         ((r + 16 * kRanks - 1) / (16 * kRanks)) * down_parts(rows);
+    const int64_t up = (n + kUpCols - 1) / kUpCols;
     const int64_t most = (int64_t)1 << 32;
-    return tiles * down * 64 * kDownWaves < most && up <= 65535 && tiles * up * 256 < most;
+    return down * 64 * kDownWaves < most && up <= 65535 &&
+           most_tiles(rows, adapters, kUpTile) * up * 256 < most;
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream)
 {
-    const unsigned tiles = (unsigned)most_tiles(a.rows, a.adapters, kTile);
-    const dim3 down(tiles, (unsigned)((a.r + 16 * kRanks - 1) / (16 * kRanks)));
+    const int parts = down_parts(a.rows);
+    const dim3 down((unsigned)most_tiles(a.rows, a.adapters, kTile),
+                    (unsigned)((a.r + 16 * kRanks - 1) / (16 * kRanks)), (unsigned)parts);
     const dim3 threads(64 * kDownWaves);
     if (a.x_type == kTypeF16) {
         hipLaunchKernelGGL(lora_down_kernel<kTypeF16>, down, threads, 0, stream, a);
@@ -327,21 +526,22 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream)
     } else {
         hipLaunchKernelGGL(lora_down_kernel<kTypeF32>, down, threads, 0, stream, a);
     }
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) {
         return e;
     }
-    const dim3 up(tiles, (unsigned)((a.n + 255) / 256));
-    const bool vb = a.r % 4 == 0;
+    const dim3 up((unsigned)most_tiles(a.rows, a.adapters, kUpTile),
+                  (unsigned)((a.n + kUpCols - 1) / kUpCols));
+    const bool vb = a.r % 8 == 0;
     const bool vy = a.n % 4 == 0;
     if (vb && vy) {
-        hipLaunchKernelGGL((lora_up_kernel<true, true>), up, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((lora_up_kernel<true, true>), up, dim3(256), 0, stream, a, parts);
     } else if (vb) {
-        hipLaunchKernelGGL((lora_up_kernel<true, false>), up, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((lora_up_kernel<true, false>), up, dim3(256), 0, stream, a, parts);
     } else if (vy) {
-        hipLaunchKernelGGL((lora_up_kernel<false, true>), up, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((lora_up_kernel<false, true>), up, dim3(256), 0, stream, a, parts);
     } else {
-        hipLaunchKernelGGL((lora_up_kernel<false, false>), up, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((lora_up_kernel<false, false>), up, dim3(256), 0, stream, a, parts);
     }
     return hipGetLastError();
 }

@@ -407,14 +407,26 @@ def q4k_f16_gemm_f32x_noalloc(w16, x, y, m: int, n: int, k: int, stream=None) ->
 # one is given.  A tensor on another device, of another type than the call
 # takes, not dense or too short is refused before the call.
 _torch = None
+_raw_stream = None          # device index -> address of its current stream
+_current_device = None
+
+
+def _import_torch():
+    global _torch, _raw_stream, _current_device
+    import torch
+    # the calls behind torch.cuda.current_stream and current_device, without the
+    # objects around them (about 1.5 us of a call); the public ones where a
+    # torch has them no more
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _torch = torch
 
 
 def _device(*args):
     """Index of the device of the first tensor among args (None: no tensor)."""
-    global _torch
     if _torch is None:
-        import torch
-        _torch = torch
+        _import_torch()
     for a in args:
         if hasattr(a, "get_device"):
             index = a.get_device()
@@ -448,15 +460,14 @@ def _run(fn, where, dev, stream, *args):
     if dev is None:
         rc = fn(*args, _stream(stream))
     else:
-        cuda = _torch.cuda
         if stream is None:
-            stream = cuda.current_stream(dev).cuda_stream
+            stream = _raw_stream(dev)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
-        if dev == cuda.current_device():
+        if dev == _current_device():
             rc = fn(*args, stream)
         else:
-            with cuda.device(dev):
+            with _torch.cuda.device(dev):
                 rc = fn(*args, stream)
     if rc != Q4K_OK:
         raise Q4KError(rc, where)

@@ -538,14 +538,18 @@ size_t q4k_lora_ws(int64_t rows, int64_t r);
  *  base    : device, rows x n f32 (the shared projection's y), may be y; NULL = 0
  *  y       : device, rows x n f32; rows of no adapter stay as they are
  *  ranks   : device, `adapters` int32, the adapters' own ranks (cut to 0 .. r;
- *            rows of a and columns of b at or beyond it are not read), NULL = r
+ *            what rows of a and columns of b at or beyond it hold does not
+ *            matter), NULL = r
  *  scales  : device, `adapters` f32, NULL = 1
  *  offsets, order : the rows grouped by adapter, as q4k_moe_group gives them
  *            (order NULL: position p is row p)
  * n, r, adapters, rows >= 1; r <= 1024; k >= 8, k % 8 == 0
- * (Q4K_ERR_UNSUPPORTED otherwise).  No operand is rounded, sums are f32, A x
- * is kept in f32: y is within (k + r + 2) 2^-23 * (|base| + |scale| sum_r |B|
- * sum_k |A| |x|) of the exact value.  Asynchronous; allocates nothing. */
+ * (Q4K_ERR_UNSUPPORTED otherwise).  A x is kept in f32, its elements carried
+ * to 2^-22 of their value or 2^-39 of their row's largest into B (A x), all
+ * sums are f32: y is within (k + r + 4) 2^-23 * (|base| + |scale| sum_r |B|
+ * sum_k |A| |x|) + 2^-38 |scale| sum_r |B| max_r |A x| of the exact value.  A
+ * row of x with an infinity or NaN gives NaN or an infinity in its y row; other
+ * rows are unaffected.  Asynchronous; allocates nothing. */
 int q4k_lora(const void* x, int x_type, const void* a, const void* b, const float* base,
              float* y, const int32_t* ranks, const float* scales, const int32_t* offsets,
              const int32_t* order, int64_t n, int64_t k, int64_t r, int64_t adapters,

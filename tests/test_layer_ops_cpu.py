@@ -150,7 +150,9 @@ def test_workspace_bytes():
     # x as two halves, its sub-blocks' sums as two halves, an exponent per row
     assert q4k.q4k_gemv_grouped_ws(512, 3) == 3 * (512 * 4 + 16 * 4 + 4)
     assert q4k.q4k_gemv_grouped_ws(500, 3) == 0 and q4k.q4k_gemv_grouped_ws(512, 0) == 0
-    assert q4k.q4k_lora_ws(5, 17) == 5 * 32 * 4
+    # A x in f32, the ranks in whole tiles of 16, by parts of k for few rows
+    assert q4k.q4k_lora_ws(5, 17) == 4 * 5 * 32 * 4
+    assert q4k.q4k_lora_ws(10000, 17) == 10000 * 32 * 4
     assert q4k.q4k_lora_ws(0, 8) == 0 and q4k.q4k_lora_ws(5, 1025) == 0
 
 
