@@ -1167,7 +1167,7 @@ size_t q4k_moe_group_ws(int64_t slots, int64_t groups, int64_t topk)
     if (check_group_shape(slots, groups, topk) != Q4K_OK) {
         return 0;
     }
-    return q4k::group_ws_bytes(slots, groups, topk);
+    return q4k::group_ws_bytes(slots, groups, topk, true);      // routing may need more
 }
 
 int q4k_moe_route(const float* logits, int64_t logits_stride, int32_t* ids, float* weights,
@@ -1190,7 +1190,7 @@ int q4k_moe_route(const float* logits, int64_t logits_stride, int32_t* ids, floa
         return Q4K_ERR_ALIGN;
     }
     if (offsets) {
-        const size_t need = q4k::group_ws_bytes(m * topk, n_experts, topk);
+        const size_t need = q4k::group_ws_bytes(m * topk, n_experts, topk, true);
         if (need && !ws) {
             return Q4K_ERR_NULL;
         }
@@ -1227,7 +1227,7 @@ int q4k_moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, int64_t 
     if (!aligned16(ids) || !aligned16(offsets) || !aligned16(order) || !aligned16(ws)) {
         return Q4K_ERR_ALIGN;
     }
-    const size_t need = q4k::group_ws_bytes(count, groups, 1);
+    const size_t need = q4k::group_ws_bytes(count, groups, 1, false);
     if (need && !ws) {
         return Q4K_ERR_NULL;
     }

@@ -138,7 +138,9 @@ struct RouteArgs {
     int slots;                         // m * topk
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
-size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk);
+constexpr int kRowExperts = 256;       // experts that 16 lanes route
+bool group_in_one(int64_t slots, int64_t groups, int64_t topk, bool route);
+size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk, bool route);
 
 struct CombineArgs {
     const float* y;

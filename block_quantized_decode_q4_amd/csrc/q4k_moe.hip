@@ -12,8 +12,10 @@
 // their ids, equal ids in slot order, and where each id begins.  A slot
 // whose id is no group is in none; the order's tail is -1.
 //
-// A wave routes a token: lane i holds experts i, i + 64, ...; each of the
-// topk steps is a maximum over the wave and a ballot for its lowest expert.
+// A token's logits are spread over 16 lanes (up to 256 experts, four tokens per
+// wave) or a wave; each of the topk steps is a maximum over the lanes and a
+// minimum of the experts that have it, both by lane moves (DPP).  Four tokens
+// per wave instead of one: 8192 tokens of 128 experts, topk 8, see below.
 // The grouping is a counting sort.  Few slots: one workgroup, in one launch
 // with the routing; a slot's place is the number of slots that sort before
 // it, counted by reading all of them from LDS.  More: the routing launch
@@ -35,113 +37,190 @@ namespace {
 
 constexpr int kPlaceThreads = 1024;
 constexpr int kPlaceWaves = kPlaceThreads / 64;
+constexpr int kCountThreads = 512;
 
-// One step of a wave reduction: v of the lane that DPP control CTRL names (its
-// own where there is none).
+// v of the lane that DPP control CTRL names: its own where there is none (OLD
+// v), or 0 there and in the rows outside ROWS
 template <int CTRL>
-__device__ __forceinline__ float dpp_f(float v)
+__device__ __forceinline__ int dpp(int v)
 {
-    const int i = __builtin_bit_cast(int, v);
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, false));
+    return __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
 }
 
-// Wave maximum of f32 values that are not NaN: within rows of 16 lanes (row
-// shifts by 1, 2, 4, 8), then across them (broadcasts of lanes 15 and 31), so
-// lane 63 has it.
-__device__ __forceinline__ float wave_max(float v)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_0(float v)
 {
-    v = fmaxf(v, dpp_f<0x111>(v));
-    v = fmaxf(v, dpp_f<0x112>(v));
-    v = fmaxf(v, dpp_f<0x114>(v));
-    v = fmaxf(v, dpp_f<0x118>(v));
-    v = fmaxf(v, dpp_f<0x142>(v));
-    v = fmaxf(v, dpp_f<0x143>(v));
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                         0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xF, true));
 }
 
-__device__ __forceinline__ float wave_sum_f(float v)
+__device__ __forceinline__ int as_int(float v) { return __builtin_bit_cast(int, v); }
+__device__ __forceinline__ float as_float(int v) { return __builtin_bit_cast(float, v); }
+
+// Reductions over a token's lanes, known to all of them.  16 lanes (a DPP row):
+// rotations by 8, 4, 2, 1.  64: shifts within the rows by 1, 2, 4, 8, then the
+// broadcasts of lanes 15 and 31 across rows, so that lane 63 has the result.
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v)       // no NaN
 {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        v += __shfl_xor(v, off, 64);
+    if constexpr (LANES == 16) {
+        v = fmaxf(v, as_float(dpp<0x128>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x124>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x122>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x121>(as_int(v))));
+        return v;
+    } else {
+        v = fmaxf(v, as_float(dpp<0x111>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x112>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x114>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x118>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x142>(as_int(v))));
+        v = fmaxf(v, as_float(dpp<0x143>(as_int(v))));
+        return as_float(__builtin_amdgcn_readlane(as_int(v), 63));
     }
-    return v;
 }
 
-// One token's experts, by one wave.  NL: logits per lane (experts lane,
-// lane + 64, ...).  Lane j (j < topk) returns the j-th choice and weight.
-template <int NL>
-__device__ __forceinline__ void route_token(const float* logits, int experts, int topk, int renorm,
-                                            int& id, float& weight)
+template <int LANES>
+__device__ __forceinline__ int lanes_min(int v)
 {
-    const float kNone = -__builtin_inff();
+    if constexpr (LANES == 16) {
+        v = min(v, dpp<0x128>(v));
+        v = min(v, dpp<0x124>(v));
+        v = min(v, dpp<0x122>(v));
+        v = min(v, dpp<0x121>(v));
+        return v;
+    } else {
+        v = min(v, dpp<0x111>(v));
+        v = min(v, dpp<0x112>(v));
+        v = min(v, dpp<0x114>(v));
+        v = min(v, dpp<0x118>(v));
+        v = min(v, dpp<0x142>(v));
+        v = min(v, dpp<0x143>(v));
+        return __builtin_amdgcn_readlane(v, 63);
+    }
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    if constexpr (LANES == 16) {
+        v += as_float(dpp<0x128>(as_int(v)));
+        v += as_float(dpp<0x124>(as_int(v)));
+        v += as_float(dpp<0x122>(as_int(v)));
+        v += as_float(dpp<0x121>(as_int(v)));
+        return v;
+    } else {
+        v += dpp_or_0<0x111, 0xF>(v);
+        v += dpp_or_0<0x112, 0xF>(v);
+        v += dpp_or_0<0x114, 0xF>(v);
+        v += dpp_or_0<0x118, 0xF>(v);
+        v += dpp_or_0<0x142, 0xA>(v);
+        v += dpp_or_0<0x143, 0xC>(v);
+        return as_float(__builtin_amdgcn_readlane(as_int(v), 63));
+    }
+}
+
+constexpr float kNone = -__builtin_inff();
+
+// The logits of a wave's 64 / LANES tokens from `token` on, NL per lane: experts
+// i, i + LANES, ... in lane i of a token's LANES.  A token at or beyond `last`
+// has none.
+template <int LANES, int NL>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t token, int64_t last,
+                                            float* l)
+{
     const int lane = threadIdx.x & 63;
-    float l[NL];
+    const int64_t t = token + lane / LANES;
+    const float* p = a.logits + t * a.stride;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-        const int e = i * 64 + lane;
-        const float v = e < experts ? logits[e] : kNone;
-        l[i] = v == v ? v : kNone;
+        const int e = i * LANES + lane % LANES;
+        l[i] = t < last && e < a.groups ? p[e] : kNone;
+    }
+}
+
+// Their experts.  Lane i of a token gets its choices i, i + LANES, ... (those
+// below topk; kMaxTopk / LANES at most).
+template <int LANES>
+constexpr int kChoices = LANES < kMaxTopk ? kMaxTopk / LANES : 1;
+
+template <int LANES, int NL>
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, float* l, int* id, float* weight)
+{
+    constexpr int C = kChoices<LANES>;
+    const int i0 = threadIdx.x & (LANES - 1);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        l[i] = l[i] == l[i] ? l[i] : kNone;
     }
     float all = 0.f;
-    if (!renorm) {
+    if (!a.renorm) {
         float top = kNone;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             top = fmaxf(top, l[i]);
         }
-        top = wave_max(top);
+        top = lanes_max<LANES>(top);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             // equal infinities would leave inf - inf: the largest counts 1
             all += l[i] == kNone ? 0.f : l[i] == top ? 1.f : expf(l[i] - top);
         }
-        all = wave_sum_f(all);
+        all = lanes_sum<LANES>(all);
     }
-    id = -1;
-    weight = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        id[c] = -1;
+        weight[c] = kNone;                     // the chosen logit, so far
+    }
     float first = 0.f;
-    for (int j = 0; j < topk; ++j) {
+    for (int j = 0; j < a.topk; ++j) {
         float best = l[0];
 #pragma unroll
         for (int i = 1; i < NL; ++i) {
             best = fmaxf(best, l[i]);
         }
-        best = wave_max(best);
-        if (best == kNone) {
-            break;                             // nothing left: id -1, weight 0
+        best = lanes_max<LANES>(best);
+        if (__all(best == kNone)) {
+            break;                             // nothing left in any token
         }
-        if (j == 0) {
-            first = best;
+        first = j == 0 ? best : first;
+        // the lowest expert with it
+        int mine = 0x7fffffff;
+#pragma unroll
+        for (int i = NL - 1; i >= 0; --i) {
+            mine = l[i] == best ? i * LANES + i0 : mine;
         }
-        int chosen = -1;
+        const int chosen = lanes_min<LANES>(mine);
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const uint64_t has = __ballot(l[i] == best);
-            if (chosen < 0 && has != 0) {
-                chosen = i * 64 + __builtin_ctzll(has);
-            }
+            l[i] = i * LANES + i0 == chosen ? kNone : l[i];
         }
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            if (i * 64 + lane == chosen) {
-                l[i] = kNone;
-            }
-        }
-        if (lane == j) {
-            id = chosen;
-            weight = best == first ? 1.f : expf(best - first);
+        for (int c = 0; c < C; ++c) {
+            const bool here = j == c * LANES + i0 && best != kNone;
+            id[c] = here ? chosen : id[c];
+            weight[c] = here ? best : weight[c];
         }
     }
-    if (renorm) {
-        all = wave_sum_f(lane < topk ? weight : 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        weight[c] = id[c] < 0 ? 0.f : weight[c] == first ? 1.f : expf(weight[c] - first);
+        sum += weight[c];
     }
-    weight = id >= 0 ? weight / all : 0.f;
+    if (a.renorm) {
+        all = lanes_sum<LANES>(sum);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        weight[c] = id[c] < 0 ? 0.f : weight[c] / all;
+    }
 }
 
-// Few slots: routing and grouping in one workgroup.  ROUTE false: the ids are
-// given.  slots <= kFewSlots.
-template <int NL, bool ROUTE>
+// Few slots: routing and grouping in one workgroup.  NL 0: the ids are given.
+// slots <= kFewSlots.
+template <int LANES, int NL>
 __global__ void __launch_bounds__(kPlaceThreads)
 group_few_kernel(RouteArgs a)
 {
@@ -151,17 +230,24 @@ group_few_kernel(RouteArgs a)
     for (int i = slots + tid; i < kFewSlots; i += kPlaceThreads) {
         ids[i] = 0x7fffffff;                   // sorts behind everything
     }
-    if constexpr (ROUTE) {
+    if constexpr (NL > 0) {
+        constexpr int kTokens = 64 / LANES;    // per wave
         const int lane = tid & 63;
-        for (int t = tid >> 6; t < a.m; t += kPlaceWaves) {
-            int id;
-            float weight;
-            route_token<NL>(a.logits + t * a.stride, a.groups, a.topk, a.renorm, id, weight);
-            if (lane < a.topk) {
-                const int s = t * a.topk + lane;
-                a.ids[s] = id;
-                a.weights[s] = weight;
-                ids[s] = id < 0 ? 0x7fffffff : id;
+        for (int t0 = (tid >> 6) * kTokens; t0 < a.m; t0 += kPlaceWaves * kTokens) {
+            int id[kChoices<LANES>];
+            float weight[kChoices<LANES>], l[NL];
+            load_logits<LANES, NL>(a, t0, a.m, l);
+            route_tokens<LANES, NL>(a, l, id, weight);
+            const int t = t0 + lane / LANES;
+#pragma unroll
+            for (int c = 0; c < kChoices<LANES>; ++c) {
+                const int j = c * LANES + lane % LANES;
+                if (t < a.m && j < a.topk) {
+                    const int s = t * a.topk + j;
+                    a.ids[s] = id[c];
+                    a.weights[s] = weight[c];
+                    ids[s] = id[c] < 0 ? 0x7fffffff : id[c];
+                }
             }
         }
     } else {
@@ -198,36 +284,51 @@ group_few_kernel(RouteArgs a)
 }
 
 // More slots: chunk c counts its slots per group into counts[c][0..groups).
-// With ROUTE it routes the chunk's tokens first.
-template <int NL, bool ROUTE>
-__global__ void __launch_bounds__(kPlaceThreads)
+// With NL > 0 it routes the chunk's tokens first.
+template <int LANES, int NL>
+__global__ void __launch_bounds__(kCountThreads)
 group_count_kernel(RouteArgs a)
 {
     extern __shared__ int hist[];
     const int tid = threadIdx.x;
-    for (int g = tid; g < a.groups; g += kPlaceThreads) {
+    for (int g = tid; g < a.groups; g += kCountThreads) {
         hist[g] = 0;
     }
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * a.chunk;
     const int64_t hi = min(lo + a.chunk, (int64_t)a.slots);
-    if constexpr (ROUTE) {
+    if constexpr (NL > 0) {
+        constexpr int kTokens = 64 / LANES;    // per wave
+        constexpr int kPass = kCountThreads / LANES;
         const int lane = tid & 63;
         const int64_t last = hi / a.topk;      // a chunk holds whole tokens
-        for (int64_t t = lo / a.topk + (tid >> 6); t < last; t += kPlaceWaves) {
-            int id;
-            float weight;
-            route_token<NL>(a.logits + t * a.stride, a.groups, a.topk, a.renorm, id, weight);
-            if (lane < a.topk) {
-                a.ids[t * a.topk + lane] = id;
-                a.weights[t * a.topk + lane] = weight;
-                if (id >= 0) {
-                    atomicAdd(&hist[id], 1);
+        int64_t t0 = lo / a.topk + (tid >> 6) * kTokens;
+        float next[NL];
+        load_logits<LANES, NL>(a, t0, last, next);
+        for (; t0 < last; t0 += kPass) {
+            int id[kChoices<LANES>];
+            float weight[kChoices<LANES>], l[NL];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                l[i] = next[i];
+            }
+            load_logits<LANES, NL>(a, t0 + kPass, last, next);     // on the way
+            route_tokens<LANES, NL>(a, l, id, weight);
+            const int64_t t = t0 + lane / LANES;
+#pragma unroll
+            for (int c = 0; c < kChoices<LANES>; ++c) {
+                const int j = c * LANES + lane % LANES;
+                if (t < last && j < a.topk) {
+                    a.ids[t * a.topk + j] = id[c];
+                    a.weights[t * a.topk + j] = weight[c];
+                    if (id[c] >= 0) {
+                        atomicAdd(&hist[id[c]], 1);
+                    }
                 }
             }
         }
     } else {
-        for (int64_t i = lo + tid; i < hi; i += kPlaceThreads) {
+        for (int64_t i = lo + tid; i < hi; i += kCountThreads) {
             const int id = a.ids[i];
             if (id >= 0 && id < a.groups) {
                 atomicAdd(&hist[id], 1);
@@ -238,7 +339,7 @@ group_count_kernel(RouteArgs a)
     if (a.counts == nullptr) {
         return;                                // routing alone
     }
-    for (int g = tid; g < a.groups; g += kPlaceThreads) {
+    for (int g = tid; g < a.groups; g += kCountThreads) {
         a.counts[(int64_t)blockIdx.x * a.groups + g] = hist[g];
     }
 }
@@ -431,11 +532,11 @@ size_t place_lds(int groups)
     return sizeof(int) * ((size_t)(kPlaceWaves + 1) * groups + 1 + 2 * kPlaceThreads);
 }
 
-template <int NL, bool ROUTE>
+template <int LANES, int NL>
 hipError_t launch_route_t(RouteArgs a, hipStream_t stream)
 {
-    if (a.slots <= kFewSlots) {
-        hipLaunchKernelGGL((group_few_kernel<NL, ROUTE>), dim3(1), dim3(kPlaceThreads), 0, stream,
+    if (group_in_one(a.slots, a.groups, a.topk, NL > 0)) {
+        hipLaunchKernelGGL((group_few_kernel<LANES, NL>), dim3(1), dim3(kPlaceThreads), 0, stream,
                            a);
         return hipGetLastError();
     }
@@ -444,7 +545,7 @@ hipError_t launch_route_t(RouteArgs a, hipStream_t stream)
     if (a.offsets == nullptr) {
         a.counts = nullptr;
     }
-    hipLaunchKernelGGL((group_count_kernel<NL, ROUTE>), dim3(a.chunks), dim3(kPlaceThreads),
+    hipLaunchKernelGGL((group_count_kernel<LANES, NL>), dim3(a.chunks), dim3(kCountThreads),
                        sizeof(int) * a.groups, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.offsets == nullptr) {
@@ -457,9 +558,19 @@ hipError_t launch_route_t(RouteArgs a, hipStream_t stream)
 
 }  // namespace
 
-size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk)
+// Whether one workgroup does it all: few enough slots to count each place
+// directly, and (routing) the tokens in two passes of its waves.  Beyond, two
+// launches over the chip are faster (191 tokens of 85 experts: 20 us in one
+// workgroup with a token per wave, 10 us in two launches).
+bool group_in_one(int64_t slots, int64_t groups, int64_t topk, bool route)
 {
-    if (slots <= kFewSlots) {
+    const int64_t pass = kPlaceThreads / (groups <= kRowExperts ? 16 : 64);
+    return slots <= kFewSlots && (!route || slots <= 2 * pass * topk);
+}
+
+size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk, bool route)
+{
+    if (group_in_one(slots, groups, topk, route)) {
         return 0;
     }
     const int64_t chunk = chunk_slots(slots, topk);
@@ -469,21 +580,24 @@ size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk)
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream)
 {
     if (a.logits == nullptr) {
-        return launch_route_t<1, false>(a, stream);
+        return launch_route_t<64, 0>(a, stream);
+    }
+    if (a.groups <= 32) {
+        return launch_route_t<16, 2>(a, stream);
     }
     if (a.groups <= 64) {
-        return launch_route_t<1, true>(a, stream);
+        return launch_route_t<16, 4>(a, stream);
     }
     if (a.groups <= 128) {
-        return launch_route_t<2, true>(a, stream);
+        return launch_route_t<16, 8>(a, stream);
     }
-    if (a.groups <= 256) {
-        return launch_route_t<4, true>(a, stream);
+    if (a.groups <= kRowExperts) {
+        return launch_route_t<16, 16>(a, stream);
     }
     if (a.groups <= 512) {
-        return launch_route_t<8, true>(a, stream);
+        return launch_route_t<64, 8>(a, stream);
     }
-    return launch_route_t<16, true>(a, stream);
+    return launch_route_t<64, 16>(a, stream);
 }
 
 hipError_t launch_combine(CombineArgs a, hipStream_t stream)
