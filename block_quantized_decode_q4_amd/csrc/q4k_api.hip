@@ -711,14 +711,14 @@ int gemv_grouped_checked(const void* w, const float* x, const int8_t* q, const f
     if (rc != Q4K_OK) {
         return rc;
     }
-    if (!fits_launch(q4k::grouped_grid(g.rows, g.groups, n), 512)) {
+    if (k > q4k::kMaxGroupedK || !fits_launch(q4k::grouped_grid(g.rows, g.groups, n, k), 256)) {
         return Q4K_ERR_SHAPE;
     }
     if (!aligned16(w) || !aligned16(x) || !aligned16(q) || !aligned16(d) || !aligned16(y) ||
         !aligned16(ws)) {
         return Q4K_ERR_ALIGN;
     }
-    if (ws_bytes < q4k::grouped_ws_bytes(k, g.x_count)) {
+    if (ws_bytes < q4k::grouped_ws_bytes(k, g.rows)) {
         return Q4K_ERR_SIZE;
     }
     q4k::GroupedArgs a;
@@ -1274,12 +1274,12 @@ int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
     return hip_status(q4k::launch_combine(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t q4k_gemv_grouped_ws(int64_t k, int64_t x_count)
+size_t q4k_gemv_grouped_ws(int64_t k, int64_t rows)
 {
-    if (check_nk(1, k) != Q4K_OK || !in_range(x_count, 1, kMaxRows)) {
+    if (check_nk(1, k) != Q4K_OK || k > q4k::kMaxGroupedK || !in_range(rows, 1, kMaxRows)) {
         return 0;
     }
-    return q4k::grouped_ws_bytes(k, x_count);
+    return q4k::grouped_ws_bytes(k, rows);
 }
 
 int q4k_gemv_grouped(const void* w, const float* x, float* y, const int32_t* offsets,

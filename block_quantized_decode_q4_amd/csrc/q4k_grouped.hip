@@ -16,29 +16,32 @@
 // m_j and 2^-11 m_j), added up per superblock as f32.  Scales folded into the
 // codes leave nothing to do per sub-block.
 //
-// Two launches: grouped_x_kernel lays each x row out once in the caller's
-// workspace (hi, lo and S in the order in which the lanes of the product
-// kernel read them); grouped_kernel multiplies.
+// Two launches: grouped_x_kernel lays each position's x out once in the
+// caller's workspace (hi, lo and S in the order in which the lanes of the
+// product kernel read them); grouped_kernel multiplies.
 //
 // grouped_kernel: a wave computes 16 weight rows x 16 positions of one group
 // (v_mfma_f32_16x16x32_f16, x as the rows, weights as the columns).  Lane
 // l = 16 g + j holds weight row j and two 16-byte pieces of its codes in each
 // superblock, and needs the scales of their four sub-blocks only: 9
 // instructions for 8 codes (mask, shift, multiply by the scale), and the
-// products with hi and with lo take the same registers.  Weights and x both
-// pass through LDS: the operands' own lane order would take 64 clocks of the
-// vector cache per load instruction where neighbouring lanes on neighbouring
-// bytes take about 20 (measured: a skewed batch 151 -> 125 us).
+// products with hi and with lo take the same registers.  The weights change
+// lanes through LDS: the operand's own lane order would take 64 clocks of the
+// vector cache per load where neighbouring lanes on neighbouring bytes take
+// about 20.  x stays in registers over several row tiles; staging it in LDS for
+// all waves of a workgroup, superblock by superblock with a barrier each, was
+// slower (one token 27 us, 48 tokens on eight wide experts 124 us).
 //
-// What bounds it: about 150 vector instructions a superblock beside 17 matrix
-// ones, on two waves a SIMD for most decode shapes, against the weights' bytes:
-// 264 MB (eight experts 4096 x 14336, 16 rows each) in 80 us, 3.3 TB/s.
-// Tried and not kept: two superblocks or two row tiles per wave and step, the
-// superblocks shared by two waves, 32 positions per tile, x converted by the
-// product kernel itself (each within 10 % on one shape and slower on others).
+// What bounds it: about 150 vector instructions a superblock and row tile
+// beside 17 matrix ones, three waves a SIMD, and the weights' bytes.  One
+// token, two of eight experts 14336 x 4096 (66 MB): 22 us with the x launch;
+// 264 MB (eight experts 4096 x 14336, 16 positions each) 83 us, 3.2 TB/s; 48
+// tokens of uneven experts (ten tiles where six experts are met) 110 us.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "q4k_device.h"
 #include "q4k_groups.h"
@@ -54,22 +57,35 @@ typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
 
-// One x row in the workspace: per superblock 512 bytes of hi, 512 of lo (lane
-// group g's operand of product u at 64 u + 16 g) and 32 of S (lane group g's at
-// 8 g); the rows' scale exponents behind all rows.
+// The workspace: x by position, kXsb bytes per position and superblock.  The
+// positions begin .. begin + count - 1 of a tile share the bytes of theirs: per
+// superblock first the 64 pieces of 16 bytes, c = 32 half + 4 u + g (half 0: hi,
+// 1: lo; product u, lane group g), piece c of the tile's position i at
+// (c count + i) 16; then S, lane group g of position i at (g count + i) 8.  So an
+// operand's load takes consecutive bytes in consecutive lanes, and no byte is
+// spent on positions that are not there.  The positions' scale exponents
+// follow.
 constexpr int kXsb = 1056;
+constexpr int kTile = 16;              // positions per tile
 
 struct XWs {
     char* rows;
     int* exps;
 };
 
-__host__ __device__ inline XWs x_ws(void* ws, int S, int64_t x_count)
+__host__ __device__ inline XWs x_ws(void* ws, int S, int64_t rows)
 {
     XWs r;
     r.rows = static_cast<char*>(ws);
-    r.exps = reinterpret_cast<int*>(r.rows + x_count * S * kXsb);
+    r.exps = reinterpret_cast<int*>(r.rows + rows * S * kXsb);
     return r;
+}
+
+// The x row of position p, -1: left out
+__device__ __forceinline__ int x_row_of(const GroupRows& g, int p)
+{
+    const int r = g.x_rows ? g.x_rows[p] : p;
+    return r < 0 || r / g.x_div >= g.x_count ? -1 : r / g.x_div;
 }
 
 // ------------------------------------------------------------------ x rows
@@ -164,16 +180,22 @@ __device__ __forceinline__ PieceAt piece_at(int v)
     return {(c >> 1) * 4 + (v & 3), (c & 1) * 2 + ((v >> 2) & 1), (c & 1) * 2 + (c >> 1)};
 }
 
+// One workgroup per position.
 template <bool Q8>
 __global__ void __launch_bounds__(1024)
 grouped_x_kernel(GroupedArgs a)
 {
     __shared__ float part[16];
-    const int64_t row = blockIdx.x;
+    const int p = blockIdx.x;
     const int tid = threadIdx.x;
     const int threads = blockDim.x;
     const int S = a.k / kQK;
-    const XWs ws = x_ws(a.ws, S, a.g.x_count);
+    const XWs ws = x_ws(a.ws, S, a.g.rows);
+    const GroupTile t = tile_of<kTile>(a.g.offsets, a.g.groups, a.g.rows, p);
+    const int64_t row = x_row_of(a.g, p);
+    if (t.count == 0 || row < 0) {
+        return;                                // in no group, or left out: never read
+    }
     float top = 0.f;
     for (int v = tid; v < S * 32; v += threads) {
         float4 lo, hi;
@@ -193,9 +215,10 @@ grouped_x_kernel(GroupedArgs a)
     }
     const int s = scale_of(top);
     if (tid == 0) {
-        ws.exps[row] = s;
+        ws.exps[p] = s;
     }
-    char* const out = ws.rows + row * S * kXsb;
+    const int i = p - t.begin;
+    char* const out = ws.rows + (int64_t)t.begin * S * kXsb;
     for (int v = tid; v < S * 32; v += threads) {
         float4 lo4, hi4;
         load_x<Q8>(a, row, v, lo4, hi4);
@@ -203,11 +226,12 @@ grouped_x_kernel(GroupedArgs a)
         h4_t sums;
         convert(lo4, hi4, s, h, l, sums);
         const PieceAt at = piece_at(v);
-        char* p = out + (int64_t)(v >> 5) * kXsb;
-        *reinterpret_cast<h8_t*>(p + at.u * 64 + at.g * 16) = h;
-        *reinterpret_cast<h8_t*>(p + 512 + at.u * 64 + at.g * 16) = l;
+        char* const o = out + (int64_t)(v >> 5) * t.count * kXsb;
+        const int c = 4 * at.u + at.g;
+        *reinterpret_cast<h8_t*>(o + (c * t.count + i) * 16) = h;
+        *reinterpret_cast<h8_t*>(o + ((32 + c) * t.count + i) * 16) = l;
         if ((v & 7) == 0) {
-            *reinterpret_cast<h4_t*>(p + 1024 + at.sg * 8) = sums;
+            *reinterpret_cast<h4_t*>(o + t.count * 1024 + (at.sg * t.count + i) * 8) = sums;
         }
     }
 }
@@ -285,28 +309,26 @@ __device__ __forceinline__ h8_t operand(uint32_t D, h2_t sl, h2_t sh)
     return h8_t{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
-// One superblock of 16 positions' x in LDS: 16-byte pieces c = 32 half + 4 u + g
-// at 256 c, position j's 16 bytes in place j ^ g (the reads of a product's
-// operand do not collide, the stores of four threads' 64 bytes by twos); then S:
-// lane groups 2 h and 2 h + 1 of position j at kXs + 256 h + 16 j.
-constexpr int kXs = 16384;
-constexpr int kStage = kXs + 512;
+// Four waves: kw of them share the superblocks (wave part p takes p, p + kw,
+// ...), 4 / kw take rows of their own, T tiles of 16 rows each.  A wave keeps the
+// x of one superblock in registers, straight from the workspace, and goes
+// through its row tiles with it; the sums of all its tiles stay in registers
+// too, and the parts are added up once, at the end.  No barrier before that: a
+// wave waits for its own loads only.  Three waves a SIMD (x alone takes 66
+// registers).
+constexpr int kWaves = 4;
 
-// Eight waves of 16 weight rows each; a step is a superblock.  The tile's x is
-// staged through two LDS buffers by all waves; the x and the weights of the
-// step after the next load while one is computed.
-constexpr int kTile = 16;              // positions per tile
-constexpr int kWaves = 8;
-constexpr int kBlockRows = 16 * kWaves;
-
-__global__ void __launch_bounds__(64 * kWaves, 4)
-grouped_kernel(GroupedArgs a, int row_blocks)
+template <int T>
+__global__ void __launch_bounds__(64 * kWaves, 3)
+grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
 {
-    __shared__ __align__(16) unsigned char xbuf[2][kStage];
-    __shared__ __align__(16) unsigned char wbufs[kWaves][kWStage];
+    // a wave's weights; its sums take their place
+    constexpr int kLds = T * 1024 > kWStage ? T * 1024 : kWStage;
+    __shared__ __align__(16) unsigned char smem[kWaves * kLds];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = tid >> 6;
+    // wave-uniform, as are all addresses but the lanes' 32-bit offsets below
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15;
     const int g = lane >> 4;
     const GroupWork work =
@@ -316,118 +338,91 @@ grouped_kernel(GroupedArgs a, int row_blocks)
         return;
     }
     const int S = a.k / kQK;
+    const int kw = 1 << kw_log2;
+    const int wk = wave & (kw - 1);
+    const int rows_per_group = 16 * T;
+    const int row0 = (work.block * (kWaves >> kw_log2) + (wave >> kw_log2)) * rows_per_group;
+    const int slabs = (S + kw - 1) >> kw_log2;
 
-    // weights: rows beyond the last are the last again, not written
-    const int row0 = work.block * kBlockRows + wave * 16;
+    // weights: a row tile that would pass the last row ends there instead (its
+    // rows are then written twice, with the same bits); fewer than 16 rows: the
+    // last again, not written
     const int64_t pitch = (int64_t)S * kBlockBytes;
     const uint8_t* const wrows = static_cast<const uint8_t*>(a.w) + (int64_t)t.group * a.n * pitch;
-    const uint8_t* const wp0 =
-        wrows + min(row0 + (lane >> 3), a.n - 1) * pitch + 16 + (lane & 7) * 16;
-    const uint8_t* const wp1 =
-        wrows + min(row0 + 8 + (lane >> 3), a.n - 1) * pitch + 16 + (lane & 7) * 16;
-    const uint8_t* const hp = wrows + min(row0 + (lane >> 2), a.n - 1) * pitch + (lane & 3) * 4;
-    unsigned char* const wbuf = wbufs[wave];
-    WPiece w;
-    auto load_w = [&](int sb) __attribute__((always_inline)) {
-        const int64_t at = (int64_t)min(sb, S - 1) * kBlockBytes;
-        w.c0 = *reinterpret_cast<const u4_t*>(wp0 + at);
-        w.c1 = *reinterpret_cast<const u4_t*>(wp1 + at);
-        w.h = *reinterpret_cast<const uint32_t*>(hp + at);
+    const int last = max(a.n - 16, 0);
+    const uint32_t off0 = (uint32_t)(min(lane >> 3, a.n - 1) * (int)pitch + 16 + (lane & 7) * 16);
+    const uint32_t off1 =
+        (uint32_t)(min(8 + (lane >> 3), a.n - 1) * (int)pitch + 16 + (lane & 7) * 16);
+    const uint32_t offh = (uint32_t)(min(lane >> 2, a.n - 1) * (int)pitch + (lane & 3) * 4);
+    unsigned char* const wbuf = smem + wave * kLds;
+    WPiece w[2];
+    // row tile `tile` (0 .. T - 1) of slab `slab` into set `tile % 2`
+    auto load_w = [&](int slab, int tile, auto set) __attribute__((always_inline)) {
+        const uint8_t* const at = wrows + min(row0 + 16 * tile, last) * pitch +
+                                  (int64_t)min(slab * kw + wk, S - 1) * kBlockBytes;
+        WPiece& p = w[decltype(set)::value];
+        p.c0 = *reinterpret_cast<const u4_t*>(at + off0);
+        p.c1 = *reinterpret_cast<const u4_t*>(at + off1);
+        p.h = *reinterpret_cast<const uint32_t*>(at + offh);
     };
-    // into the wave's own LDS; its reads of the superblock before are behind it
-    // (one wave's LDS accesses are in order)
-    auto stage_w = [&]() __attribute__((always_inline)) {
-        unsigned char* const c = wbuf + (lane >> 3) * kBlockBytes + 16 + (lane & 7) * 16;
-        *reinterpret_cast<u4_t*>(c) = w.c0;
-        *reinterpret_cast<u4_t*>(c + 8 * kBlockBytes) = w.c1;
-        *reinterpret_cast<uint32_t*>(wbuf + (lane >> 2) * kBlockBytes + (lane & 3) * 4) = w.h;
+    // x: positions behind the last read the last's, whose products are its own
+    const XWs ws = x_ws(a.ws, S, a.g.rows);
+    const int slot = min(j, t.count - 1);
+    const char* const xrows = ws.rows + (int64_t)t.begin * S * kXsb;
+    const uint32_t xoff = (uint32_t)((g * t.count + slot) * 16);
+    u4_t xh[8], xl[8];
+    uint2 xs;
+    auto load_x = [&](int slab) __attribute__((always_inline)) {
+        const char* const at =
+            xrows + (int64_t)min(slab * kw + wk, S - 1) * t.count * kXsb;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            xh[u] = *reinterpret_cast<const u4_t*>(at + u * t.count * 64 + xoff);
+            xl[u] = *reinterpret_cast<const u4_t*>(at + (8 + u) * t.count * 64 + xoff);
+        }
+        xs = *reinterpret_cast<const uint2*>(at + t.count * 1024 + xoff / 2);
     };
-    load_w(0);
-
-    // x: pieces 4 wave + tid % 4 (and 32 more) of position (tid / 4) % 16, and 16
-    // bytes of S of position (tid / 2) % 16.  A position that is left out takes x
-    // row 0, nothing is loaded behind the last one; no product of either is
-    // written.
-    const XWs ws = x_ws(a.ws, S, a.g.x_count);
-    auto x_row = [&](int i) -> int {           // -1: left out
-        if (i >= t.count) {
-            return -1;
-        }
-        const int p = t.begin + i;
-        const int r = a.g.x_rows ? a.g.x_rows[p] : p;
-        return r < 0 || r / a.g.x_div >= a.g.x_count ? -1 : r / a.g.x_div;
-    };
-    const int lj = (tid >> 2) & 15;
-    const int sj = (tid >> 1) & 15;
-    const bool has_x = lj < t.count;
-    const bool has_s = tid < 32 && sj < t.count;
-    const char* const xsrc =
-        ws.rows + (int64_t)max(x_row(lj), 0) * S * kXsb + wave * 64 + (tid & 3) * 16;
-    const char* const ssrc =
-        ws.rows + (int64_t)max(x_row(sj), 0) * S * kXsb + 1024 + (tid & 1) * 16;
-    const int xdst = wave * 1024 + (tid & 3) * 256 + ((lj ^ (tid & 3)) << 4);
-    const int sdst = kXs + (tid & 1) * 256 + sj * 16;
-    u4_t xv[2], sv;
-    auto load_x = [&](int sb) __attribute__((always_inline)) {
-        const int64_t at = (int64_t)min(sb, S - 1) * kXsb;
-        if (has_s) {
-            sv = *reinterpret_cast<const u4_t*>(ssrc + at);
-        }
-        if (has_x) {
-            xv[0] = *reinterpret_cast<const u4_t*>(xsrc + at);
-            xv[1] = *reinterpret_cast<const u4_t*>(xsrc + at + 512);
-        }
-    };
-    auto stage_x = [&](int buf) __attribute__((always_inline)) {
-        unsigned char* const base = xbuf[buf];
-        if (has_x) {
-            *reinterpret_cast<u4_t*>(base + xdst) = xv[0];
-            *reinterpret_cast<u4_t*>(base + xdst + 8192) = xv[1];
-        }
-        if (has_s) {
-            *reinterpret_cast<u4_t*>(base + sdst) = sv;
-        }
-    };
-    load_x(0);
-    const int xr = x_row(j);
-    int yr = -1;
-    if (xr >= 0) {
-        yr = a.g.y_rows ? a.g.y_rows[t.begin + j] : t.begin + j;
-        yr = yr < a.g.y_count ? yr : -1;
-    }
-    const int exps = xr >= 0 ? ws.exps[xr] : 0;
     const uint32_t shift = 16 * (g >> 1);
     const uint32_t odd = g & 1 ? 0xFFFFFFFFu : 0u;
-    const int xlane = g * 256 + ((j ^ g) << 4);
     const f4_t zero = {0.f, 0.f, 0.f, 0.f};
-    f4_t total = zero;
-
-    stage_w();
-    stage_x(0);
-    load_x(1);
-    load_w(1);
-    __syncthreads();
-    for (int sb = 0; sb < S; ++sb) {
-        if (row0 < a.n) {
-            const unsigned char* const xs = xbuf[sb & 1];
+    f4_t total[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        total[i] = zero;
+    }
+    load_w(0, 0, std::integral_constant<int, 0>());
+    load_w(0, 1, std::integral_constant<int, 1>());
+    for (int slab = 0; slab < slabs; ++slab) {
+        load_x(slab);
+        const bool in = slab * kw + wk < S;
+        auto tile = [&](int i, auto set) __attribute__((always_inline)) {
+            // through the wave's own LDS (one wave's accesses are in order)
+            const WPiece& p = w[decltype(set)::value];
+            unsigned char* const c = wbuf + (lane >> 3) * kBlockBytes + 16 + (lane & 7) * 16;
+            *reinterpret_cast<u4_t*>(c) = p.c0;
+            *reinterpret_cast<u4_t*>(c + 8 * kBlockBytes) = p.c1;
+            *reinterpret_cast<uint32_t*>(wbuf + (lane >> 2) * kBlockBytes + (lane & 3) * 4) = p.h;
+            // the tile after the next (of the next slab behind the last two)
+            load_w(i + 2 < T ? slab : min(slab + 1, slabs - 1), (i + 2) % T, set);
+            if (!in) {
+                return;
+            }
             const unsigned char* const wr = wbuf + j * kBlockBytes;
             const uint4 h = *reinterpret_cast<const uint4*>(wr);
             const uint4 c0 = *reinterpret_cast<const uint4*>(wr + 16 + 16 * g);
             const uint4 c1 = *reinterpret_cast<const uint4*>(wr + 80 + 16 * g);
             const WScales sc = scales_of(h, shift, odd);
-            const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+            const uint32_t cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
             f4_t ah = zero, al = zero;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const h8_t b = operand(c[u], sc.sl[u / 4], sc.sh[u / 4]);
-                const h8_t xh = *reinterpret_cast<const h8_t*>(xs + u * 1024 + xlane);
-                const h8_t xl = *reinterpret_cast<const h8_t*>(xs + 8192 + u * 1024 + xlane);
-                ah = __builtin_amdgcn_mfma_f32_16x16x32_f16(xh, b, ah, 0, 0, 0);
-                al = __builtin_amdgcn_mfma_f32_16x16x32_f16(xl, b, al, 0, 0, 0);
+                const h8_t b = operand(cc[u], sc.sl[u / 4], sc.sh[u / 4]);
+                ah = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, xh[u]), b, ah,
+                                                            0, 0, 0);
+                al = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, xl[u]), b, al,
+                                                            0, 0, 0);
             }
-            const uint2 s2 = *reinterpret_cast<const uint2*>(xs + kXs + (g >> 1) * 256 + j * 16 +
-                                                             (g & 1) * 8);
-            const u4_t sx = {s2.x, s2.y, 0u, 0u};
+            const u4_t sx = {xs.x, xs.y, 0u, 0u};
             const f4_t am = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, sx),
                                                                    sc.m, zero, 0, 0, 0);
             // 2^14: the operands' 2^-14; lo carries 2^11 more; S is 2^-6
@@ -436,47 +431,104 @@ grouped_kernel(GroupedArgs a, int row_blocks)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float v = __builtin_fmaf(al[e], 1.0f / 2048.0f, ah[e]);
-                total[e] = __builtin_fmaf(dh, v, total[e]);
-                total[e] = __builtin_fmaf(-dm, am[e], total[e]);
+                total[i][e] = __builtin_fmaf(dh, v, total[i][e]);
+                total[i][e] = __builtin_fmaf(-dm, am[e], total[i][e]);
+            }
+        };
+        static_assert(T % 2 == 0, "two sets in turn");
+#pragma unroll
+        for (int i = 0; i < T; i += 2) {
+            tile(i, std::integral_constant<int, 0>());
+            tile(i + 1, std::integral_constant<int, 1>());
+        }
+    }
+    // the parts of k, in their order; every wave joins and writes some tiles
+    f4_t* const part = reinterpret_cast<f4_t*>(wbuf);
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        part[i * 64 + lane] = total[i];
+    }
+    const int p = t.begin + slot;
+    int yr = -1;
+    if (j < t.count && x_row_of(a.g, p) >= 0) {
+        yr = a.g.y_rows ? a.g.y_rows[p] : p;
+        yr = yr < a.g.y_count ? yr : -1;
+    }
+    const int exps = ws.exps[p];
+    __syncthreads();
+    for (int q = wave; q < (kWaves >> kw_log2) * T; q += kWaves) {
+        const int rg = q / T;
+        const int i = q % T;
+        const unsigned char* const from = smem + (rg << kw_log2) * kLds + (i * 64 + lane) * 16;
+        f4_t sum = *reinterpret_cast<const f4_t*>(from);
+        for (int z = 1; z < kw; ++z) {
+            sum += *reinterpret_cast<const f4_t*>(from + z * kLds);
+        }
+        const int row =
+            min((work.block * (kWaves >> kw_log2) + rg) * rows_per_group + 16 * i, last) + j;
+        // D[4 g + e][j]: position 4 g + e, weight row j
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int yrow = __shfl(yr, 4 * g + e, 64);
+            const int exp = __shfl(exps, 4 * g + e, 64);
+            if (row < a.n && yrow >= 0) {
+                a.y[(int64_t)yrow * a.n + row] = ldexpf(sum[e], -exp);
             }
         }
-        stage_w();
-        stage_x((sb + 1) & 1);
-        // x before weights: waiting for x leaves the newest weights in flight
-        load_x(sb + 2);
-        load_w(sb + 2);
-        __syncthreads();
     }
-    // D[4 g + e][j]: position 4 g + e, weight row j
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int yrow = __shfl(yr, 4 * g + e, 64);
-        const int exp = __shfl(exps, 4 * g + e, 64);
-        if (row0 + j < a.n && yrow >= 0) {
-            a.y[(int64_t)yrow * a.n + row0 + j] = ldexpf(total[e], -exp);
-        }
+}
+
+// How the rows are cut: T row tiles per wave and kw waves along k.
+//  - T = 2 while T = 4 would give fewer workgroups than CUs (one token, two
+//    experts 4096 x 14336: 25.6 us against 35.1);
+//  - T = 8 where the groups hold 8 positions or more: x is read once per T
+//    tiles (eight experts 4096 x 14336 with 16 positions each 83 us against 93,
+//    128 positions each 141 / 157 us), and T = 4 otherwise (one token, eight of
+//    64 experts 1536 x 2048: 11.7 us against 15.3).
+//  - kw = 4, so that a row's loads are 576 consecutive bytes, but less at T = 8
+//    where more than a fifth of the waves' steps would find no superblock
+//    (k = 1536, 32 positions a group: kw 4 / 2 88.5 / 80.0 us; with few rows the
+//    shorter way is as good, 17.2 / 18.7 us at k = 1536, 4 tokens).
+struct GroupedCut {
+    int T, kw_log2, blocks;            // blocks of rows
+    int64_t grid;
+};
+
+GroupedCut grouped_cut(int64_t rows, int64_t groups, int64_t n, int64_t k)
+{
+    const int64_t tiles = most_tiles(rows, groups, kTile);
+    const int64_t S = k / kQK;
+    GroupedCut c;
+    c.T = tiles * ((n + 63) / 64) < 256 ? 2 : rows >= 8 * groups ? 8 : 4;
+    c.kw_log2 = 2;
+    auto steps = [&](int log2) { return (((S - 1) >> log2) + 1) << log2; };  // of all parts
+    while (c.T == 8 && c.kw_log2 > 0 && steps(c.kw_log2) * 4 > S * 5) {
+        --c.kw_log2;
     }
+    const int64_t per = 16 * c.T * (kWaves >> c.kw_log2);
+    c.blocks = (int)((n + per - 1) / per);
+    c.grid = (tiles * c.blocks + 7) / 8 * 8;
+    return c;
 }
 
 }  // namespace
 
-size_t grouped_ws_bytes(int64_t k, int64_t x_count)
+size_t grouped_ws_bytes(int64_t k, int64_t rows)
 {
-    return (size_t)x_count * (size_t)(k / kQK) * kXsb + (size_t)x_count * sizeof(int);
+    return (size_t)rows * (size_t)(k / kQK) * kXsb + (size_t)rows * sizeof(int);
 }
 
 // The workgroups of the products
-int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n)
+int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k)
 {
-    const int64_t blocks = (n + kBlockRows - 1) / kBlockRows;
-    return (most_tiles(rows, groups, kTile) * blocks + 7) / 8 * 8;
+    return grouped_cut(rows, groups, n, k).grid;
 }
 
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream)
 {
     // a piece of eight elements per thread and pass
     const int pieces = a.k / 8;
-    const dim3 rows((unsigned)a.g.x_count), threads(pieces < 1024 ? (pieces + 63) / 64 * 64 : 1024);
+    const dim3 rows((unsigned)a.g.rows), threads(pieces < 1024 ? (pieces + 63) / 64 * 64 : 1024);
     if (a.q != nullptr) {
         hipLaunchKernelGGL(grouped_x_kernel<true>, rows, threads, 0, stream, a);
     } else {
@@ -486,9 +538,15 @@ hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream)
     if (e != hipSuccess) {
         return e;
     }
-    const int64_t grid = grouped_grid(a.g.rows, a.g.groups, a.n);
-    hipLaunchKernelGGL(grouped_kernel, dim3((unsigned)grid), dim3(64 * kWaves), 0, stream, a,
-                       (a.n + kBlockRows - 1) / kBlockRows);
+    const GroupedCut c = grouped_cut(a.g.rows, a.g.groups, a.n, a.k);
+    const dim3 grid((unsigned)c.grid), block(64 * kWaves);
+    if (c.T == 2) {
+        hipLaunchKernelGGL(grouped_kernel<2>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+    } else if (c.T == 4) {
+        hipLaunchKernelGGL(grouped_kernel<4>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+    } else {
+        hipLaunchKernelGGL(grouped_kernel<8>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+    }
     return hipGetLastError();
 }
 

@@ -77,6 +77,33 @@ __device__ __forceinline__ GroupTile find_tile(const int* offsets, int groups, i
     return r;
 }
 
+// The tile that holds position p (the first group's that has it); count = 0:
+// it is in no group.
+template <int ROWS>
+__device__ __forceinline__ GroupTile tile_of(const int* offsets, int groups, int rows, int p)
+{
+    const int lane = threadIdx.x & 63;
+    GroupTile r = {0, 0, 0};
+    for (int base = 0; base < groups; base += 64) {
+        const int g = base + lane;
+        int lo = 0, hi = 0;
+        if (g < groups) {
+            lo = min(max(offsets[g], 0), rows);
+            hi = min(max(offsets[g + 1], 0), rows);
+        }
+        const uint64_t has = __ballot(lo <= p && p < hi);
+        if (has != 0) {
+            const int l = __builtin_ctzll(has);
+            const int begin = __builtin_amdgcn_readlane(lo, l);
+            r.group = base + l;
+            r.begin = begin + (p - begin) / ROWS * ROWS;
+            r.count = min(ROWS, __builtin_amdgcn_readlane(hi, l) - r.begin);
+            return r;
+        }
+    }
+    return r;
+}
+
 // One workgroup's share of (tiles) x (column blocks).  Workgroup b runs on XCD
 // b % 8, so XCD x takes the x-th eighth of the list that runs over the groups,
 // their column blocks and, innermost, the group's tiles: every XCD gets as

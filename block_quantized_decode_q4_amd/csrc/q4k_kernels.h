@@ -177,8 +177,9 @@ struct GroupedArgs {
     int n, k;
 };
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
-size_t grouped_ws_bytes(int64_t k, int64_t x_count);
-int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n);
+size_t grouped_ws_bytes(int64_t k, int64_t rows);
+int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k);
+constexpr int64_t kMaxGroupedK = (int64_t)1 << 24;   // 16 rows within 32-bit offsets
 
 // The fp16 mirror (q4k_f16.hip).
 hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,

@@ -564,9 +564,9 @@ def q4k_moe_combine(y, weights, ids, out, n: int, topk: int, m: int = 1, *, resi
          int(m))
 
 
-def q4k_gemv_grouped_ws(k: int, x_count: int) -> int:
+def q4k_gemv_grouped_ws(k: int, rows: int) -> int:
     """Bytes of workspace of q4k_gemv_grouped and q4k_gemv_grouped_q8."""
-    return int(load_library().q4k_gemv_grouped_ws(int(k), int(x_count)))
+    return int(load_library().q4k_gemv_grouped_ws(int(k), int(rows)))
 
 
 def q4k_gemv_grouped(w, x, y, offsets, n: int, k: int, groups: int, rows: int, *, x_rows=None,

@@ -477,7 +477,7 @@ int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
 
 /* Grouped rows.  Of `rows` positions, group g (of `groups`) holds positions
  * offsets[g] .. offsets[g + 1] - 1 (device, groups + 1 int32, not decreasing;
- * cut to 0 .. rows).  Position p multiplies x row
+ * cut to 0 .. rows: others give wrong products, but no access outside).  Position p multiplies x row
  *   (x_rows ? x_rows[p] : p) / x_div      of x_count rows
  * and writes y row
  *   (y_rows ? y_rows[p] : p)              of y_count rows
@@ -488,16 +488,16 @@ int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
  * q4k_moe_route serves as x_rows with x_div = topk (x by token: the up
  * projections) or as y_rows (y by slot: the down projection). */
 
-/* Bytes of workspace of q4k_gemv_grouped and q4k_gemv_grouped_q8 (0 for
- * arguments that they refuse). */
-size_t q4k_gemv_grouped_ws(int64_t k, int64_t x_count);
+/* Bytes of workspace of q4k_gemv_grouped and q4k_gemv_grouped_q8 for `rows`
+ * positions (0 for arguments that they refuse). */
+size_t q4k_gemv_grouped_ws(int64_t k, int64_t rows);
 
 /* y[row] = W_g x[row] over grouped rows, W_g n x k in Q4_K (the rows of
  * q4k_gemv; group g's begin at row g*n of w): the experts' products of a decode
  * batch.
  *  w : device, groups*n Q4_K rows;  x : device, x_count x k f32
  *  y : device, y_count x n f32
- * 1 <= n, k as for q4k_gemv.  x is carried to 2^-22 of its value or 2^-50 of
+ * 1 <= n, k as for q4k_gemv and at most 2^24.  x is carried to 2^-22 of its value or 2^-50 of
  * its row's largest, the weights' two terms (d sc q and dmin m, times x) are
  * added up apart in f32: with T = sum (|d sc q| + |dmin m|) |x| and U the same
  * sum with the row's largest |x| for every x, y is within

@@ -59,12 +59,11 @@ def _gpu(kind, w, x, y, off, n, k, groups, rows, **kw):
     """x: f32 array, (q, d), or f16 array by kind."""
     y_d = torch.from_numpy(y).cuda()
     w_d = torch.from_numpy(w).cuda()
-    x_count = kw.get("x_count") or rows
     if kind == "f16":
         q4k.q4k_f16_gemm_grouped(w_d, torch.from_numpy(x).cuda(), y_d, _i32(off), n, k, groups,
                                  rows, **kw)
     else:
-        nb = q4k.q4k_gemv_grouped_ws(k, x_count)
+        nb = q4k.q4k_gemv_grouped_ws(k, rows)
         ws = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda")     # NaN patterns
         if kind == "f32":
             q4k.q4k_gemv_grouped(w_d, torch.from_numpy(x).cuda(), y_d, _i32(off), n, k, groups,
@@ -140,6 +139,15 @@ SIZES = [
 ]
 
 
+# enough tiles for every way of cutting rows and k: few positions a group (four
+# row tiles a wave), many (eight), the last with one, two and four waves along k
+SIZES += [
+    ([2] * 40, 450, 768), ([1, 0, 3] * 20, 600, 256), ([10] * 20, 1000, 256),
+    ([9, 12] * 10, 1010, 512), ([17, 3, 8] * 7, 1500, 768), ([8] * 20, 840, 1280),
+    ([30, 5] * 10, 700, 1024),
+]
+
+
 @pytest.mark.parametrize("kind", ["f32", "q8", "f16"])
 @pytest.mark.parametrize("sizes,n,k", SIZES)
 def test_grouped_sizes(kind, sizes, n, k):
@@ -204,28 +212,21 @@ def test_grouped_rows_gathered_scattered_and_left_out(kind):
 @pytest.mark.parametrize("kind", ["f32", "f16"])
 def test_grouped_bad_offsets_stay_inside(kind):
     """Offsets that decrease, or lie outside the rows, give no access outside:
-    the groups are cut to the rows."""
+    the groups are cut to the rows.  Positions that two groups claim get either
+    product or neither; a group apart from the others is as it should be."""
     rng = np.random.default_rng(9)
-    n, k, groups, rows = 20, 256, 4, 10
+    n, k, groups, rows = 20, 256, 5, 14
     W = (Mirror if kind == "f16" else Weights)(rng, groups, n, k)
     x = _make_x(rng, kind, rows, k)
-    y0 = np.full((rows, n), 5.0, np.float32)
-    off = np.array([-7, 3, 2, 6, 1000], np.int32)
-    got = _gpu(kind, W.bytes, x, y0, off, n, k, groups, rows)
-    cut = np.array([0, 3, 2, 6, 10])
-    y1 = y0.copy()
-    for g in range(groups):                           # group 2 holds 2 .. 5, group 1 none
-        lo, hi = cut[g], cut[g + 1]
-        for p in range(lo, max(lo, hi)):
-            if g == 0 and p == 2:
-                continue                              # named by groups 0 and 2: either product
-            ref = W.w[g] @ x[p].astype(np.float64)
-            T = W.mag[g] @ np.abs(x[p].astype(np.float64))
-            if p != 2:
-                assert (np.abs(got[p] - ref) <= 300 * 2.0 ** -23 * T + 1e-30).all(), (g, p)
-                y1[p] = got[p]
-    rest = [p for p in range(rows) if p != 2]
-    assert np.array_equal(got[rest], y1[rest])
+    y0 = np.full((rows + 2, n), 5.0, np.float32)
+    off = np.array([-7, 3, 2, 6, 10, 1000], np.int32)
+    got = _gpu(kind, W.bytes, x, y0, off, n, k, groups, rows, y_count=rows)
+    assert (got[rows:] == 5.0).all()
+    for g, lo, hi in ((3, 6, 10), (4, 10, 14)):
+        for p in range(lo, hi):
+            v = x[p].astype(np.float64)
+            err = np.abs(got[p] - W.w[g] @ v)
+            assert (err <= 300 * 2.0 ** -23 * (W.mag[g] @ np.abs(v)) + 1e-30).all(), (g, p)
 
 
 def test_grouped_ranges_of_x():

@@ -67,7 +67,7 @@ class Layer:
         self.ws_group = ws(max(q4k.q4k_moe_group_ws(slots, experts, topk),
                                q4k.q4k_moe_group_ws(m, adapters, 1)))
         self.ws_lora = ws(q4k.q4k_lora_ws(m, r))
-        self.ws_up = ws(q4k.q4k_gemv_grouped_ws(k, m))
+        self.ws_up = ws(q4k.q4k_gemv_grouped_ws(k, slots))
         self.ws_down = ws(q4k.q4k_gemv_grouped_ws(ff, slots))
 
     def run(self):

@@ -87,7 +87,7 @@ def test_combine_refusals(lib):
 
 def _grouped(lib, name, **kw):
     a = dict(w=A, x=A, d=A, y=A, off=A, xr=A, yr=A, n=100, k=512, groups=4, rows=9, div=2, xc=5,
-             yc=9, ws=A, wsb=q4k.q4k_gemv_grouped_ws(512, 5))
+             yc=9, ws=A, wsb=q4k.q4k_gemv_grouped_ws(512, 9))
     a.update(kw)
     rows = (a["off"], a["xr"], a["yr"], a["n"], a["k"], a["groups"], a["rows"], a["div"], a["xc"],
             a["yc"])
@@ -115,7 +115,8 @@ def test_grouped_refusals(lib, name):
         assert _grouped(lib, name, k=96) == q4k.Q4K_ERR_UNSUPPORTED
     else:
         assert _grouped(lib, name, k=384) == q4k.Q4K_ERR_SHAPE
-        assert _grouped(lib, name, wsb=q4k.q4k_gemv_grouped_ws(512, 5) - 1) == q4k.Q4K_ERR_SIZE
+        assert _grouped(lib, name, k=2 ** 24 + 256, wsb=2 ** 62) == q4k.Q4K_ERR_SHAPE
+        assert _grouped(lib, name, wsb=q4k.q4k_gemv_grouped_ws(512, 9) - 1) == q4k.Q4K_ERR_SIZE
 
 
 def _lora(lib, **kw):
@@ -147,7 +148,7 @@ def test_workspace_bytes():
         assert q4k.q4k_moe_group_ws(slots, groups, topk) == 0
     # counts per chunk and group; about 256 chunks at most
     assert 0 < q4k.q4k_moe_group_ws(BIG - 1, 1024, 1) <= 257 * 1024 * 4
-    # x as two halves, its sub-blocks' sums as two halves, an exponent per row
+    # x as two halves, its sub-blocks' sums as two halves, an exponent per position
     assert q4k.q4k_gemv_grouped_ws(512, 3) == 3 * (512 * 4 + 16 * 4 + 4)
     assert q4k.q4k_gemv_grouped_ws(500, 3) == 0 and q4k.q4k_gemv_grouped_ws(512, 0) == 0
     # A x in f32, the ranks in whole tiles of 16, by parts of k for few rows
