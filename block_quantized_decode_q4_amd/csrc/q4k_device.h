@@ -98,6 +98,14 @@ __device__ __forceinline__ int dpp_i(int v)
     return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
 }
 
+// A wave's LDS accesses on both sides, of all its lanes, in the order written:
+// the hardware keeps one wave's in order, so this holds the compiler only and
+// costs no instruction.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+}
+
 __device__ __forceinline__ double wave_sum(double v)
 {
 #pragma unroll

@@ -396,12 +396,14 @@ grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
         load_x(slab);
         const bool in = slab * kw + wk < S;
         auto tile = [&](int i, auto set) __attribute__((always_inline)) {
-            // through the wave's own LDS (one wave's accesses are in order)
+            // through the wave's own LDS
+            wave_lds_order();
             const WPiece& p = w[decltype(set)::value];
             unsigned char* const c = wbuf + (lane >> 3) * kBlockBytes + 16 + (lane & 7) * 16;
             *reinterpret_cast<u4_t*>(c) = p.c0;
             *reinterpret_cast<u4_t*>(c + 8 * kBlockBytes) = p.c1;
             *reinterpret_cast<uint32_t*>(wbuf + (lane >> 2) * kBlockBytes + (lane & 3) * 4) = p.h;
+            wave_lds_order();
             // the tile after the next (of the next slab behind the last two)
             load_w(i + 2 < T ? slab : min(slab + 1, slabs - 1), (i + 2) % T, set);
             if (!in) {
@@ -443,6 +445,7 @@ grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
         }
     }
     // the parts of k, in their order; every wave joins and writes some tiles
+    wave_lds_order();
     f4_t* const part = reinterpret_cast<f4_t*>(wbuf);
 #pragma unroll
     for (int i = 0; i < T; ++i) {

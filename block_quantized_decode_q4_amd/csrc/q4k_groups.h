@@ -119,17 +119,20 @@ __device__ __forceinline__ GroupWork find_work(const int* offsets, int groups, i
                                                int b)
 {
     const int lane = threadIdx.x & 63;
+    // offsets that decrease can name more tiles than the grid has: cut there, so
+    // that no number below passes 32 bits
+    const int most = (int)gridDim.x / blocks;
     int total = 0;
     for (int g = lane; g < groups; g += 64) {
         const int lo = min(max(offsets[g], 0), rows);
         const int hi = min(max(offsets[g + 1], 0), rows);
-        total += hi > lo ? (hi - lo - 1) / ROWS + 1 : 0;
+        total = min(total + (hi > lo ? (hi - lo - 1) / ROWS + 1 : 0), most);
     }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) {
         total += __shfl_xor(total, off, 64);
     }
-    total = __builtin_amdgcn_readfirstlane(total) * blocks;
+    total = min(__builtin_amdgcn_readfirstlane(total), most) * blocks;
     const int share = (total + 7) / 8;
     const int at = (b & 7) * share + (b >> 3);
     GroupWork r = {{0, 0, 0}, 0};

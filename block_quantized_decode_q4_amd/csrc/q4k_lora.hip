@@ -32,6 +32,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "q4k_device.h"
 #include "q4k_groups.h"
 #include "q4k_kernels.h"
 
@@ -143,7 +144,8 @@ __device__ __forceinline__ void down_part(const LoraArgs& a, const GroupTile& t,
         load(first);
     }
     for (int st = first; st < steps; st += stride) {
-        // one wave's LDS accesses are in order: no barrier
+        // the wave's own LDS: no barrier
+        wave_lds_order();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             *reinterpret_cast<u4_t*>(lds + at128(8 * i + (lane >> 3), lane & 7)) = xv[i];
@@ -154,6 +156,7 @@ __device__ __forceinline__ void down_part(const LoraArgs& a, const GroupTile& t,
             const int at = kPieces == 8 ? at128(row, lane % kPieces) : at64(row, lane % kPieces);
             *reinterpret_cast<u4_t*>(alds + at) = av[i];
         }
+        wave_lds_order();
         if (st + stride < steps) {
             load(st + stride);
         }
@@ -229,6 +232,7 @@ lora_down_kernel(LoraArgs a)
     } else {
         down_part<TYPE, 4>(a, t, rank0, rank, first, stride, smem[wave], acc);
     }
+    wave_lds_order();
     f4_t* const mine = reinterpret_cast<f4_t*>(smem[wave]);
 #pragma unroll
     for (int i = 0; i < kRanks; ++i) {

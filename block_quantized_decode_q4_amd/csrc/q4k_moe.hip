@@ -452,7 +452,10 @@ group_place_kernel(RouteArgs a)
         if (in) {
             const int rank = __popcll(peers & ((1ull << lane) - 1));
             const int at = mine[id];
-            a.order[at + rank] = (int)i;
+            // always, unless another call writes the workspace or the ids meanwhile
+            if ((uint32_t)(at + rank) < (uint32_t)a.slots) {
+                a.order[at + rank] = (int)i;
+            }
             // every peer has read `at` (one wave, in lockstep); the last moves it on
             __builtin_amdgcn_wave_barrier();
             if ((peers >> lane) == 1) {
@@ -462,7 +465,7 @@ group_place_kernel(RouteArgs a)
         __builtin_amdgcn_wave_barrier();
     }
     // the tail: slots in no group
-    for (int64_t i = (int64_t)begin[G] + (int64_t)c * kPlaceThreads + tid; i < a.slots;
+    for (int64_t i = max(begin[G], 0) + (int64_t)c * kPlaceThreads + tid; i < a.slots;
          i += (int64_t)a.chunks * kPlaceThreads) {
         a.order[i] = -1;
     }

@@ -455,6 +455,26 @@ def _at(a, dtype, count, dev):
     return a.data_ptr()
 
 
+def _rows_at(a, dtype, rows, width, stride, dev):
+    """Address of rows of width elements, stride apart (0: dense); a tensor may
+    be a view that skips the rest of each row."""
+    if not stride or not hasattr(a, "get_device") or a.is_contiguous():
+        return _at(a, dtype, (rows - 1) * (stride or width) + width, dev)
+    if a.get_device() != dev:
+        raise ValueError("tensors on more than one device: %s and cuda:%s" % (a.device, dev))
+    if a.dtype is not dtype and dtype is not None:
+        raise TypeError("expected %s, got %s" % (dtype, a.dtype))
+    want = stride
+    fits = a.dim() > 1 and a.stride(-1) == 1 and a.shape[-1] >= width
+    for i in range(a.dim() - 2, -1, -1):
+        fits = fits and (a.shape[i] == 1 or a.stride(i) == want)
+        want *= a.shape[i]
+    if not fits or want < rows * stride:
+        raise ValueError("%d rows of %d elements, %d apart, in a tensor of shape %s and strides %s"
+                         % (rows, width, stride, tuple(a.shape), a.stride()))
+    return a.data_ptr()
+
+
 def _run(fn, where, dev, stream, *args):
     """fn(*args, stream) with device dev current; raises for its status."""
     if dev is None:
@@ -474,25 +494,31 @@ def _run(fn, where, dev, stream, *args):
 
 
 def _act_type(x, x_type):
-    """The q4k_type of x: given, or its tensor's."""
-    if x_type is not None:
-        return int(x_type)
+    """The q4k_type of x: its tensor's, or given beside an address."""
     if not hasattr(x, "get_device"):
-        return Q4K_F32
+        return Q4K_F32 if x_type is None else int(x_type)
     dtype = x.dtype
     if dtype is _torch.float32:
-        return Q4K_F32
-    if dtype is _torch.float16:
-        return Q4K_F16
-    if dtype is _torch.bfloat16:
-        return Q4K_BF16
-    raise TypeError("expected f32, f16 or bf16 activations, got %s" % dtype)
+        have = Q4K_F32
+    elif dtype is _torch.float16:
+        have = Q4K_F16
+    elif dtype is _torch.bfloat16:
+        have = Q4K_BF16
+    else:
+        raise TypeError("expected f32, f16 or bf16 activations, got %s" % dtype)
+    if x_type is not None and x_type != have:
+        raise TypeError("x_type %s for activations of type %s" % (x_type, dtype))
+    return have
 
 
 def _ws_bytes(ws, ws_bytes):
-    if ws_bytes is not None:
-        return int(ws_bytes)
-    return ws.numel() * ws.element_size() if hasattr(ws, "element_size") else 0
+    """Bytes of ws: its tensor's, or given beside an address."""
+    if not hasattr(ws, "element_size"):
+        return 0 if ws_bytes is None else int(ws_bytes)
+    have = ws.numel() * ws.element_size()
+    if ws_bytes is not None and ws_bytes > have:
+        raise ValueError("a workspace of %d bytes where %d are given" % (have, ws_bytes))
+    return have if ws_bytes is None else int(ws_bytes)
 
 
 def q4k_rmsnorm(x, weight, k: int, m: int = 1, *, eps: float = 1e-5, residual=None, sum_out=None,
@@ -504,17 +530,10 @@ def q4k_rmsnorm(x, weight, k: int, m: int = 1, *, eps: float = 1e-5, residual=No
     asynchronous on stream."""
     dev = _device(x, weight)
     mk = m * k
-    if x_stride and hasattr(x, "get_device"):
-        # a view with strided rows: dense within each row only
-        have = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
-        if have < (m - 1) * x_stride + k:
-            raise ValueError("x does not hold %d rows at stride %d" % (m, x_stride))
-        xa = x.data_ptr()
-    else:
-        xa = _at(x, None, mk, dev)
     f32, i8, f16 = _torch.float32, _torch.int8, _torch.float16
-    _run(load_library().q4k_rmsnorm, "q4k_rmsnorm", dev, stream, xa, _act_type(x, x_type),
-         int(x_stride), _at(residual, f32, mk, dev), _at(weight, f32, k, dev), _at(sum_out, f32, mk, dev),
+    _run(load_library().q4k_rmsnorm, "q4k_rmsnorm", dev, stream,
+         _rows_at(x, None, m, k, x_stride, dev), _act_type(x, x_type), int(x_stride),
+         _at(residual, f32, mk, dev), _at(weight, f32, k, dev), _at(sum_out, f32, mk, dev),
          _at(y, f32, mk, dev), _at(y16, f16, mk, dev), _at(q, i8, mk, dev),
          _at(d, f32, mk // 32, dev), int(k), int(m), float(eps))
 
@@ -532,11 +551,11 @@ def q4k_moe_route(logits, ids, weights, n_experts: int, topk: int, m: int = 1, *
     dev = _device(logits, ids)
     f32, i32 = _torch.float32, _torch.int32
     slots = m * topk
-    span = (m - 1) * (logits_stride or n_experts) + n_experts
-    _run(load_library().q4k_moe_route, "q4k_moe_route", dev, stream, _at(logits, f32, span, dev),
-         int(logits_stride), _at(ids, i32, slots, dev), _at(weights, f32, slots, dev),
-         _at(offsets, i32, n_experts + 1, dev), _at(order, i32, slots, dev), int(n_experts),
-         int(topk), 1 if renorm else 0, int(m), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
+    _run(load_library().q4k_moe_route, "q4k_moe_route", dev, stream,
+         _rows_at(logits, f32, m, n_experts, logits_stride, dev), int(logits_stride),
+         _at(ids, i32, slots, dev), _at(weights, f32, slots, dev), _at(offsets, i32, n_experts + 1, dev),
+         _at(order, i32, slots, dev), int(n_experts), int(topk), 1 if renorm else 0, int(m),
+         _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_moe_group(ids, offsets, order, count: int, groups: int, *, ws=None, ws_bytes=None,
@@ -547,8 +566,7 @@ def q4k_moe_group(ids, offsets, order, count: int, groups: int, *, ws=None, ws_b
     i32 = _torch.int32
     _run(load_library().q4k_moe_group, "q4k_moe_group", dev, stream, _at(ids, i32, count, dev),
          _at(offsets, i32, groups + 1, dev), _at(order, i32, count, dev), int(count),
-         int(groups),
-         _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
+         int(groups), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_moe_combine(y, weights, ids, out, n: int, topk: int, m: int = 1, *, residual=None,
@@ -582,7 +600,8 @@ def q4k_gemv_grouped(w, x, y, offsets, n: int, k: int, groups: int, rows: int, *
          _at(w, _torch.uint8, groups * n * (k // 256) * 144, dev), _at(x, f32, x_count * k, dev),
          _at(y, f32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
          _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
-         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
+         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev),
+         _ws_bytes(ws, ws_bytes))
 
 
 def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: int, *,
@@ -599,7 +618,8 @@ def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: 
          _at(q, _torch.int8, x_count * k, dev), _at(d, f32, x_count * (k // 32), dev),
          _at(y, f32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
          _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
-         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
+         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev),
+         _ws_bytes(ws, ws_bytes))
 
 
 def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows: int, *,
@@ -636,11 +656,12 @@ def q4k_lora(x, a, b, y, offsets, order, n: int, k: int, r: int, adapters: int, 
     dev = _device(x, a)
     f32, i32, f16 = _torch.float32, _torch.int32, _torch.float16
     _run(load_library().q4k_lora, "q4k_lora", dev, stream, _at(x, None, rows * k, dev),
-         _act_type(x, x_type), _at(a, f16, adapters * r * k, dev), _at(b, f16, adapters * n * r, dev),
+         _act_type(x, x_type), _at(a, f16, adapters * r * k, dev),
+         _at(b, f16, adapters * n * r, dev),
          _at(base, f32, rows * n, dev), _at(y, f32, rows * n, dev), _at(ranks, i32, adapters, dev),
          _at(scales, f32, adapters, dev), _at(offsets, i32, adapters + 1, dev),
-         _at(order, i32, rows, dev), int(n), int(k), int(r), int(adapters), int(rows), _at(ws, None, 0, dev),
-         _ws_bytes(ws, ws_bytes))
+         _at(order, i32, rows, dev), int(n), int(k), int(r), int(adapters), int(rows),
+         _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
 
 
 def q4k_read_calibrate_blocks() -> int:

@@ -393,6 +393,8 @@ int q4k_f16_gemm_f32x_noalloc(const void* w16, const float* x, float* y, int64_t
  *    call gives the bytes it needs (Q4K_ERR_SIZE when there are fewer).  Calls
  *    that may run at the same time need workspaces of their own, captured
  *    graphs included.  Its contents mean nothing between calls.
+ *  - Outputs and workspaces overlap neither inputs nor one another, unless the
+ *    call says so.
  *  - Rows and positions number fewer than 2^22 (Q4K_ERR_SHAPE beyond), and a
  *    launch fewer than 2^32 threads.
  * ------------------------------------------------------------------- */
@@ -465,6 +467,7 @@ int q4k_moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, int64_t 
 
 /* out[t][c] = residual[t][c] + sum_j weights[t][j] * y[t*topk + j][c] over the
  * choices j with ids[t][j] >= 0 (f32, in the order of j, the residual last).
+ * Every choice with such an id needs its row of y.
  *  y : device, m*topk x n f32;  weights : device, m x topk f32
  *  ids : device, m x topk int32, or NULL (every choice counts); rows of y
  *        whose id is negative are not read
@@ -477,7 +480,8 @@ int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
 
 /* Grouped rows.  Of `rows` positions, group g (of `groups`) holds positions
  * offsets[g] .. offsets[g + 1] - 1 (device, groups + 1 int32, not decreasing;
- * cut to 0 .. rows: others give wrong products, but no access outside).  Position p multiplies x row
+ * cut to 0 .. rows: others give wrong products, but no access outside).
+ * Position p multiplies x row
  *   (x_rows ? x_rows[p] : p) / x_div      of x_count rows
  * and writes y row
  *   (y_rows ? y_rows[p] : p)              of y_count rows
@@ -497,9 +501,9 @@ size_t q4k_gemv_grouped_ws(int64_t k, int64_t rows);
  * batch.
  *  w : device, groups*n Q4_K rows;  x : device, x_count x k f32
  *  y : device, y_count x n f32
- * 1 <= n, k as for q4k_gemv and at most 2^24.  x is carried to 2^-22 of its value or 2^-50 of
- * its row's largest, the weights' two terms (d sc q and dmin m, times x) are
- * added up apart in f32: with T = sum (|d sc q| + |dmin m|) |x| and U the same
+ * 1 <= n, k as for q4k_gemv and at most 2^24.  x is carried to 2^-22 of its
+ * value or 2^-50 of its row's largest, the weights' two terms (d sc q and
+ * dmin m, times x) are added up apart in f32: with T = sum (|d sc q| + |dmin m|) |x| and U the same
  * sum with the row's largest |x| for every x, y is within
  * (280 + k/128) 2^-23 T + 2^-48 U of the exact value (the bound of f32 sums of
  * 256 terms; in practice a few 2^-23 of the row's scale).  A row of x with an
@@ -542,7 +546,8 @@ size_t q4k_lora_ws(int64_t rows, int64_t r);
  *            matter), NULL = r
  *  scales  : device, `adapters` f32, NULL = 1
  *  offsets, order : the rows grouped by adapter, as q4k_moe_group gives them
- *            (order NULL: position p is row p)
+ *            (order NULL: position p is row p); no row twice, and a row that
+ *            is negative or at or beyond `rows` is left out
  * n, r, adapters, rows >= 1; r <= 1024; k >= 8, k % 8 == 0
  * (Q4K_ERR_UNSUPPORTED otherwise).  A x is kept in f32, its elements carried
  * to 2^-22 of their value or 2^-39 of their row's largest into B (A x), all

@@ -284,3 +284,25 @@ def test_grouped_same_bits_each_time():
     # a position's result does not depend on who shares its tile
     c = _gpu("f32", W.bytes, x[:5], y0[:5], _offsets([5, 0, 0]), 200, 1536, 3, 5)
     np.testing.assert_allclose(c, a[:5], rtol=0, atol=2e-4 * np.abs(a).max())
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+def test_grouped_offsets_that_name_more_tiles_than_32_bits(kind):
+    """Every second group claims all the rows: 4096 groups of 2^21 rows, which
+    the grid does not hold; the rows around y stay."""
+    n, groups, rows = 1024, 8192, 2 ** 21
+    k = 256 if kind == "f32" else 64
+    off = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = rows
+    y = torch.full((3, n), 5.0, device="cuda")
+    if kind == "f32":
+        w = torch.zeros((groups * n, 144), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(q4k.q4k_gemv_grouped_ws(k, rows), dtype=torch.uint8, device="cuda")
+        q4k.q4k_gemv_grouped(w, torch.ones((1, k), device="cuda"), y, off, n, k, groups, rows,
+                             x_count=1, y_count=1, ws=ws)
+    else:
+        w = torch.zeros((groups * n, k), dtype=torch.float16, device="cuda")
+        q4k.q4k_f16_gemm_grouped(w, torch.ones((1, k), dtype=torch.float16, device="cuda"), y,
+                                 off, n, k, groups, rows, x_count=1, y_count=1)
+    torch.cuda.synchronize()
+    assert (y[1:] == 5.0).all()

@@ -175,3 +175,30 @@ def test_combine(m, n, topk, residual, masked):
     if not masked:
         q4k.q4k_moe_combine(y_d, w_d, None, out, n, topk, m, residual=None)
         assert (np.abs(out.cpu().numpy() - terms.sum(1)) <= (topk + 2) * 2.0 ** -24 * mag).all()
+
+
+def test_route_takes_views_of_wider_rows():
+    g = torch.Generator().manual_seed(72)
+    wide = torch.randn((9, 80), generator=g).cuda()
+    a = _route(wide[:, :64], 64, 4, 9, True, stride=80)
+    b = _route(wide[:, :64].contiguous(), 64, 4, 9, True)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+    with pytest.raises(ValueError):
+        _route(wide[:, :64], 64, 4, 9, True, stride=96)
+    with pytest.raises(ValueError):
+        _route(wide[:, :64], 64, 4, 9, True)
+    with pytest.raises(ValueError):
+        _route(wide[:, :64], 64, 4, 10, True, stride=80)
+
+
+def test_group_refuses_a_workspace_said_to_be_longer():
+    n = 20000
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda")
+    off = torch.empty(5, dtype=torch.int32, device="cuda")
+    order = torch.empty(n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        q4k.q4k_moe_group(ids, off, order, n, 4, ws=ws, ws_bytes=1 << 20)
+    with pytest.raises(q4k.Q4KError):
+        q4k.q4k_moe_group(ids, off, order, n, 4, ws=ws)

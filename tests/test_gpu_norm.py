@@ -155,3 +155,21 @@ def test_rmsnorm_refuses_short_tensors():
         q4k.q4k_rmsnorm(x, w, 256, 2, y16=torch.empty((2, 256), device="cuda"))
     with pytest.raises(TypeError):
         q4k.q4k_rmsnorm(x.double(), w, 256, 2, y=torch.empty((2, 256), device="cuda"))
+
+
+def test_rmsnorm_takes_views_of_wider_rows():
+    g = torch.Generator().manual_seed(71)
+    wide = torch.randn((2, 3, 320), generator=g).cuda()
+    w = torch.randn(256, generator=g).cuda()
+    a = torch.empty((6, 256), device="cuda")
+    b = torch.empty((6, 256), device="cuda")
+    q4k.q4k_rmsnorm(wide[:, :, :256], w, 256, 6, x_stride=320, y=a)
+    q4k.q4k_rmsnorm(wide[:, :, :256].contiguous(), w, 256, 6, y=b)
+    assert torch.equal(a, b)
+    for bad, stride in ((wide[:, :, :256], 384), (wide[:, :2, :256], 320),
+                        (wide[:, :, :128], 320), (wide.transpose(1, 2), 320),
+                        (wide[:, :, ::2], 320)):
+        with pytest.raises(ValueError):
+            q4k.q4k_rmsnorm(bad, w, 256, 6, x_stride=stride, y=a)
+    with pytest.raises(TypeError):          # f16 read as f32 would pass the end
+        q4k.q4k_rmsnorm(b.half(), w, 256, 6, x_type=q4k.Q4K_F32, y=a)
