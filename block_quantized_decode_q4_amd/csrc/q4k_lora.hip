@@ -270,9 +270,9 @@ lora_down_kernel(LoraArgs a)
 constexpr int kBPitch = 72;            // halves per row of v or B (9 pieces of 16 bytes)
 constexpr int kYPitch = kUpCols + 4;   // floats per row of the products (65 pieces)
 
-template <bool VB, bool VY>
+template <int PARTS, bool VB, bool VY>
 __global__ void __launch_bounds__(256, 3)
-lora_up_kernel(LoraArgs a, int parts)
+lora_up_kernel(LoraArgs a)
 {
     constexpr int kVBytes = kUpTile * kBPitch * 2;
     constexpr int kLds = 2 * kVBytes + kUpCols * kBPitch * 2;
@@ -280,13 +280,14 @@ lora_up_kernel(LoraArgs a, int parts)
     constexpr int U = kUpTile / 16;
     constexpr int kOwn = kUpTile / 4;          // rows that a wave writes
     __shared__ __align__(16) unsigned char smem[kLds];
-    __shared__ int exps[kUpTile];              // the rows' scales
+    __shared__ int exps[kUpTile], steps[kUpTile];    // the rows' scales, and by how much they rose
     _Float16* const vs = reinterpret_cast<_Float16*>(smem);            // hi, then lo
     _Float16* const bs = reinterpret_cast<_Float16*>(smem + 2 * kVBytes);
     float* const ys = reinterpret_cast<float*>(smem);
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = tid >> 6;
+    // wave-uniform, as are all addresses but the lanes' 32-bit offsets below
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int j = lane & 15;
     const int g = lane >> 4;
     const int col0 = (int)blockIdx.y * kUpCols;
@@ -296,7 +297,7 @@ lora_up_kernel(LoraArgs a, int parts)
     }
     const int rank = rank_of(a, t.group);
     const int pitch = (a.r + 15) / 16 * 16;
-    const _Float16* const bg = static_cast<const _Float16*>(a.b) + (int64_t)t.group * a.n * a.r;
+    const _Float16* const bg = static_cast<const _Float16*>(a.b) + ((int64_t)t.group * a.n + col0) * a.r;
     const f4_t zero = {0.f, 0.f, 0.f, 0.f};
     f4_t total[U][4];                          // [16 positions][16 columns]
 #pragma unroll
@@ -306,28 +307,96 @@ lora_up_kernel(LoraArgs a, int parts)
             total[u][i] = zero;
         }
     }
+    // All that comes from memory is asked for here, in the order in which it is
+    // waited for: the rows to write, v, B, the base.  None of these loads is
+    // conditional (a wait behind a branch would wait for all of them): what is
+    // not there reads something that is, and is masked or not written later.
+    // The rows that this wave will write: positions wave, wave + 4, ...
+    const int mine = t.begin + min(wave + 4 * (lane & (kOwn - 1)), t.count - 1);
+    const int ordered = (a.order ? a.order : a.offsets)[a.order ? mine : 0];
+    // v: positions x 16 quads of ranks, by parts of k
+    f4_t vp[U][PARTS];
+    const int vq = (tid & 15) * 4;
+    auto load_v = [&](int k0) __attribute__((always_inline)) {
+        const int quad = min(vq, max(rank - k0 - 1, 0) / 4 * 4);
+#pragma unroll
+        for (int z = 0; z < PARTS; ++z) {
+            const char* const from = reinterpret_cast<const char*>(
+                a.v + ((int64_t)z * a.rows + t.begin) * pitch + k0);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int p = min(16 * i + (tid >> 4), t.count - 1);
+                vp[i][z] =
+                    *reinterpret_cast<const f4_t*>(from + (uint32_t)(p * pitch + quad) * 4u);
+            }
+        }
+    };
+    // B (VB): eight ranks of every 32nd column
+    u4_t w[kUpCols / 32];
+    const int bq = (tid & 7) * 8;
+    auto load_b = [&](int k0) __attribute__((always_inline)) {
+        const char* const from = reinterpret_cast<const char*>(bg + k0);
+        const int q = min(bq, max(rank - k0 - 1, 0) / 8 * 8);
+#pragma unroll
+        for (int i = 0; i < kUpCols / 32; ++i) {
+            const int c = min(32 * i + (tid >> 3), a.n - 1 - col0);
+            w[i] = *reinterpret_cast<const u4_t*>(from + (uint32_t)(c * a.r + q) * 2u);
+        }
+    };
+    load_v(0);
+    if constexpr (VB) {
+        load_b(0);
+    }
+    // the base (a row of y is this wave's alone, so base may be y)
+    const int lane_row = a.order ? ordered : mine;
+    int row[kOwn];
+    f4_t base[kOwn];
+#pragma unroll
+    for (int q = 0; q < kOwn; ++q) {
+        row[q] = wave + 4 * q < t.count ? __builtin_amdgcn_readlane(lane_row, q) : -1;
+        row[q] = row[q] < a.rows ? row[q] : -1;
+        const float* const from =
+            a.base ? a.base + (int64_t)max(row[q], 0) * a.n + col0 : a.v;
+        if constexpr (VY) {                            // n % 4 == 0
+            const int c = a.base ? min(4 * lane, a.n - 4 - col0) : 0;
+            base[q] = *reinterpret_cast<const f4_t*>(reinterpret_cast<const char*>(from) +
+                                                     (uint32_t)c * 4u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = a.base ? min(64 * e + lane, a.n - 1 - col0) : 0;
+                base[q][e] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(from) +
+                                                             (uint32_t)c * 4u);
+            }
+        }
+    }
+    // a row's scale so far: 2^-seen brings the largest |v| into [2^14, 2^15)
+    int seen[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        seen[u] = -1000;                       // below any
+    }
     for (int k0 = 0; k0 < rank; k0 += 64) {
         if (k0 > 0) {
             __syncthreads();
+            load_v(k0);
+            if constexpr (VB) {
+                load_b(k0);
+            }
         }
         const int left = rank - k0;
-        // v: positions x 16 quads of ranks, the parts added up; zeros at ranks
-        // and positions that are not there
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int p = 16 * i + (tid >> 4);
-            const int q = (tid & 15) * 4;
-            f4_t sum = {0.f, 0.f, 0.f, 0.f};
-            if (p < t.count && q < left) {
-                const float* src = a.v + (int64_t)(t.begin + p) * pitch + k0 + q;
-                sum = *reinterpret_cast<const f4_t*>(src);
-                for (int z = 1; z < parts; ++z) {
-                    sum += *reinterpret_cast<const f4_t*>(src + (int64_t)z * a.rows * pitch);
-                }
+            const int q = vq;
+            f4_t sum = vp[i][0];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    sum[c] = q + c < left ? sum[c] : 0.f;
-                }
+            for (int z = 1; z < PARTS; ++z) {
+                sum += vp[i][z];
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                sum[c] = q + c < left ? sum[c] : 0.f;
             }
             // the 16 lanes of a position
             float top = 0.f;
@@ -339,43 +408,37 @@ lora_up_kernel(LoraArgs a, int parts)
             for (int off = 1; off < 16; off <<= 1) {
                 top = fmaxf(top, __shfl_xor(top, off, 64));
             }
-            int e = 15;                                // none for zeros and infinities
+            int e = seen[i];
             if (top > 0.f && top < __builtin_inff()) {
                 (void)frexpf(top, &e);
+                e = max(e - 15, seen[i]);
             }
+            const int step = seen[i] - e;
+            seen[i] = e;
             h4_t hi, lo;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float x = ldexpf(sum[c], 15 - e);
+                const float x = ldexpf(sum[c], -e);
                 hi[c] = (_Float16)x;
                 lo[c] = (_Float16)(x - (float)hi[c]);
             }
             *reinterpret_cast<h4_t*>(vs + p * kBPitch + q) = hi;
             *reinterpret_cast<h4_t*>(vs + kUpTile * kBPitch + p * kBPitch + q) = lo;
             if ((tid & 15) == 0) {
-                exps[p] = e - 15;
+                exps[p] = e;
+                steps[p] = step;
             }
         }
         if constexpr (VB) {
-            const int q = (tid & 7) * 8;
             u4_t keep;                                 // the halves below the rank
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                const int have = left - q - 2 * d;
+                const int have = left - bq - 2 * d;
                 keep[d] = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
             }
-            u4_t w[kUpCols / 32];
 #pragma unroll
             for (int i = 0; i < kUpCols / 32; ++i) {
-                const int c = min(col0 + 32 * i + (tid >> 3), a.n - 1);        // rows beyond n: any
-                w[i] = u4_t{0u, 0u, 0u, 0u};
-                if (q < left) {
-                    w[i] = *reinterpret_cast<const u4_t*>(bg + (int64_t)c * a.r + k0 + q);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kUpCols / 32; ++i) {
-                *reinterpret_cast<u4_t*>(bs + (32 * i + (tid >> 3)) * kBPitch + q) = w[i] & keep;
+                *reinterpret_cast<u4_t*>(bs + (32 * i + (tid >> 3)) * kBPitch + bq) = w[i] & keep;
             }
         } else {
             // a row of B per wave and load, a rank per lane
@@ -383,16 +446,28 @@ lora_up_kernel(LoraArgs a, int parts)
             for (int c = wave; c < kUpCols; c += 4) {
                 _Float16 w = (_Float16)0;
                 if (col0 + c < a.n && lane < left) {
-                    w = bg[(int64_t)(col0 + c) * a.r + k0 + lane];
+                    w = bg[c * a.r + k0 + lane];
                 }
                 bs[c * kBPitch + lane] = w;
             }
         }
         __syncthreads();
-        f4_t acc[U][4];
+        if (k0 > 0) {                              // sums so far, in the new scale
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int step = steps[16 * u + j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        total[u][i][c] = ldexpf(total[u][i][c], step);
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            if (32 * s < left || s == 0) {
+            if (32 * s < left) {
                 h8_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -406,63 +481,29 @@ lora_up_kernel(LoraArgs a, int parts)
                     const h8_t lo = *reinterpret_cast<const h8_t*>(vp + kUpTile * kBPitch);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        acc[u][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            w[i], hi, s == 0 ? zero : acc[u][i], 0, 0, 0);
-                        acc[u][i] =
-                            __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i], lo, acc[u][i], 0, 0, 0);
+                        total[u][i] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i], hi, total[u][i], 0, 0, 0);
+                        total[u][i] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_f16(w[i], lo, total[u][i], 0, 0, 0);
                     }
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = exps[16 * u + j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    total[u][i][c] += ldexpf(acc[u][i][c], e);
                 }
             }
         }
     }
     __syncthreads();
+    // (rank 0: the sums are zeros, in no scale)
     // D[4 g + c][j] of (u, i): column 16 i + 4 g + c of position 16 u + j
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+        const int e = rank > 0 ? exps[16 * u + j] : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                total[u][i][c] = ldexpf(total[u][i][c], e);
+            }
             *reinterpret_cast<f4_t*>(ys + (16 * u + j) * kYPitch + wave * 64 + 16 * i + 4 * g) =
                 total[u][i];
-        }
-    }
-    // the base of the rows that this wave will write: positions wave, wave + 4,
-    // ...  (a row of y is this wave's alone, so base may be y)
-    int row[kOwn];
-    f4_t base[kOwn];
-#pragma unroll
-    for (int q = 0; q < kOwn; ++q) {
-        const int p = wave + 4 * q;
-        row[q] = p < t.count ? row_of(a, t.begin + p) : -1;
-    }
-#pragma unroll
-    for (int q = 0; q < kOwn; ++q) {
-        base[q] = f4_t{0.f, 0.f, 0.f, 0.f};
-        if (row[q] >= 0 && a.base != nullptr) {
-            if constexpr (VY) {
-                const int c = col0 + 4 * lane;
-                if (c < a.n) {                         // n % 4 == 0: all four or none
-                    base[q] = *reinterpret_cast<const f4_t*>(a.base + (int64_t)row[q] * a.n + c);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = col0 + 64 * e + lane;
-                    if (c < a.n) {
-                        base[q][e] = a.base[(int64_t)row[q] * a.n + c];
-                    }
-                }
-            }
         }
     }
     __syncthreads();
@@ -471,6 +512,9 @@ lora_up_kernel(LoraArgs a, int parts)
     for (int q = 0; q < kOwn; ++q) {
         if (row[q] < 0) {
             continue;
+        }
+        if (a.base == nullptr) {
+            base[q] = zero;
         }
         const float* const yp = ys + (wave + 4 * q) * kYPitch;
         float* const out = a.y + (int64_t)row[q] * a.n;
@@ -489,6 +533,22 @@ lora_up_kernel(LoraArgs a, int parts)
                 }
             }
         }
+    }
+}
+
+template <int PARTS>
+void launch_up(const LoraArgs& a, dim3 up, hipStream_t stream)
+{
+    const bool vb = a.r % 8 == 0;
+    const bool vy = a.n % 4 == 0;
+    if (vb && vy) {
+        hipLaunchKernelGGL((lora_up_kernel<PARTS, true, true>), up, dim3(256), 0, stream, a);
+    } else if (vb) {
+        hipLaunchKernelGGL((lora_up_kernel<PARTS, true, false>), up, dim3(256), 0, stream, a);
+    } else if (vy) {
+        hipLaunchKernelGGL((lora_up_kernel<PARTS, false, true>), up, dim3(256), 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((lora_up_kernel<PARTS, false, false>), up, dim3(256), 0, stream, a);
     }
 }
 
@@ -536,16 +596,10 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream)
     }
     const dim3 up((unsigned)most_tiles(a.rows, a.adapters, kUpTile),
                   (unsigned)((a.n + kUpCols - 1) / kUpCols));
-    const bool vb = a.r % 8 == 0;
-    const bool vy = a.n % 4 == 0;
-    if (vb && vy) {
-        hipLaunchKernelGGL((lora_up_kernel<true, true>), up, dim3(256), 0, stream, a, parts);
-    } else if (vb) {
-        hipLaunchKernelGGL((lora_up_kernel<true, false>), up, dim3(256), 0, stream, a, parts);
-    } else if (vy) {
-        hipLaunchKernelGGL((lora_up_kernel<false, true>), up, dim3(256), 0, stream, a, parts);
-    } else {
-        hipLaunchKernelGGL((lora_up_kernel<false, false>), up, dim3(256), 0, stream, a, parts);
+    switch (parts) {
+    case 1: launch_up<1>(a, up, stream); break;
+    case 2: launch_up<2>(a, up, stream); break;
+    default: launch_up<4>(a, up, stream); break;
     }
     return hipGetLastError();
 }
