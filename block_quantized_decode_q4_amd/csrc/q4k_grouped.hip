@@ -180,7 +180,11 @@ __device__ __forceinline__ PieceAt piece_at(int v)
     return {(c >> 1) * 4 + (v & 3), (c & 1) * 2 + ((v >> 2) & 1), (c & 1) * 2 + (c >> 1)};
 }
 
-// One workgroup per position.
+// One workgroup per position.  Up to kHeld pieces per thread stay in registers
+// between the row's largest and the conversion (k to 16384); the rest of a
+// longer row is read again.
+constexpr int kHeld = 2;
+
 template <bool Q8>
 __global__ void __launch_bounds__(1024)
 grouped_x_kernel(GroupedArgs a)
@@ -191,13 +195,25 @@ grouped_x_kernel(GroupedArgs a)
     const int threads = blockDim.x;
     const int S = a.k / kQK;
     const XWs ws = x_ws(a.ws, S, a.g.rows);
-    const GroupTile t = tile_of<kTile>(a.g.offsets, a.g.groups, a.g.rows, p);
     const int64_t row = x_row_of(a.g, p);
-    if (t.count == 0 || row < 0) {
-        return;                                // in no group, or left out: never read
+    if (row < 0) {
+        return;                                // left out: never read
+    }
+    float4 held[kHeld][2];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {          // the row's last piece for those behind it
+        load_x<Q8>(a, row, min(h * threads + tid, S * 32 - 1), held[h][0], held[h][1]);
+    }
+    const GroupTile t = tile_of<kTile>(a.g.offsets, a.g.groups, a.g.rows, p);
+    if (t.count == 0) {
+        return;                                // in no group
     }
     float top = 0.f;
-    for (int v = tid; v < S * 32; v += threads) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        top = piece_top(held[h][0], held[h][1], top);
+    }
+    for (int v = kHeld * threads + tid; v < S * 32; v += threads) {
         float4 lo, hi;
         load_x<Q8>(a, row, v, lo, hi);
         top = piece_top(lo, hi, top);
@@ -219,9 +235,7 @@ grouped_x_kernel(GroupedArgs a)
     }
     const int i = p - t.begin;
     char* const out = ws.rows + (int64_t)t.begin * S * kXsb;
-    for (int v = tid; v < S * 32; v += threads) {
-        float4 lo4, hi4;
-        load_x<Q8>(a, row, v, lo4, hi4);
+    auto put = [&](int v, const float4& lo4, const float4& hi4) __attribute__((always_inline)) {
         h8_t h, l;
         h4_t sums;
         convert(lo4, hi4, s, h, l, sums);
@@ -233,6 +247,18 @@ grouped_x_kernel(GroupedArgs a)
         if ((v & 7) == 0) {
             *reinterpret_cast<h4_t*>(o + t.count * 1024 + (at.sg * t.count + i) * 8) = sums;
         }
+    };
+    // whole eights of lanes: S * 32 is a multiple of 8
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        if (h * threads + tid < S * 32) {
+            put(h * threads + tid, held[h][0], held[h][1]);
+        }
+    }
+    for (int v = kHeld * threads + tid; v < S * 32; v += threads) {
+        float4 lo4, hi4;
+        load_x<Q8>(a, row, v, lo4, hi4);
+        put(v, lo4, hi4);
     }
 }
 

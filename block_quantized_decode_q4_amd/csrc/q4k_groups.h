@@ -13,52 +13,82 @@ struct GroupTile {
     int group, begin, count;
 };
 
-__device__ __forceinline__ int wave_scan_add(int v, int lane)
+// v of the lanes up to this one, added up: shifts within rows of 16 lanes (DPP),
+// then lanes 15 and 31 broadcast into the rows behind them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int scan_step(int v)
 {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(v, off, 64);
-        v += lane >= off ? o : 0;
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, true);
+}
+
+__device__ __forceinline__ int wave_scan_add(int v)
+{
+    v = scan_step<0x111, 0xF>(v);
+    v = scan_step<0x112, 0xF>(v);
+    v = scan_step<0x114, 0xF>(v);
+    v = scan_step<0x118, 0xF>(v);
+    v = scan_step<0x142, 0xA>(v);
+    return scan_step<0x143, 0xC>(v);
+}
+
+// Lane l's group base + l: its positions lo .. hi - 1, cut to 0 .. rows - 1
+// whatever the offsets say (a range that ends before it begins is empty), its
+// tiles of ROWS, and the tiles of the lanes up to this one.  A whole wave.
+struct GroupLanes {
+    int lo, hi, tiles, upto;
+};
+
+template <int ROWS>
+__device__ __forceinline__ GroupLanes group_lanes(const int* offsets, int groups, int rows,
+                                                  int base)
+{
+    const int g = base + (int)(threadIdx.x & 63);
+    GroupLanes r = {0, 0, 0, 0};
+    if (g < groups) {
+        r.lo = min(max(offsets[g], 0), rows);
+        r.hi = min(max(offsets[g + 1], 0), rows);
     }
-    return v;
+    r.tiles = r.hi > r.lo ? (r.hi - r.lo - 1) / ROWS + 1 : 0;
+    r.upto = wave_scan_add(r.tiles);
+    return r;
 }
 
 // The group that holds tile t when every group's positions are cut into tiles
 // of ROWS: its positions begin .. end - 1, its first tile and its tiles (0: no
-// such tile).  Group g holds positions offsets[g] .. offsets[g + 1] - 1, cut to
-// 0 .. rows - 1 whatever the offsets say (a range that ends before it begins
-// is empty).  Every wave of the workgroup finds the same by itself: 64 groups
+// such tile).  Every wave of the workgroup finds the same by itself: 64 groups
 // at a time, a scan of their tile counts and one ballot.
 struct GroupSpan {
     int group, begin, end, first, tiles;
 };
 
+// Tile t among the 64 groups from base on, `before` tiles before them
+__device__ __forceinline__ bool span_in(const GroupLanes& v, int base, int before, int t,
+                                        GroupSpan& r)
+{
+    const uint64_t past = __ballot(t < before + v.upto);
+    if (past == 0) {
+        return false;
+    }
+    const int l = __builtin_ctzll(past);
+    r.group = base + l;
+    r.begin = __builtin_amdgcn_readlane(v.lo, l);
+    r.end = __builtin_amdgcn_readlane(v.hi, l);
+    r.tiles = __builtin_amdgcn_readlane(v.tiles, l);
+    r.first = before + __builtin_amdgcn_readlane(v.upto, l) - r.tiles;
+    return true;
+}
+
 template <int ROWS>
 __device__ __forceinline__ GroupSpan find_span(const int* offsets, int groups, int rows, int t)
 {
-    const int lane = threadIdx.x & 63;
     int before = 0;                        // tiles of the groups already passed
     GroupSpan r = {0, 0, 0, 0, 0};
     for (int base = 0; base < groups; base += 64) {
-        const int g = base + lane;
-        int lo = 0, hi = 0;
-        if (g < groups) {
-            lo = min(max(offsets[g], 0), rows);
-            hi = min(max(offsets[g + 1], 0), rows);
-        }
-        const int tiles = hi > lo ? (hi - lo - 1) / ROWS + 1 : 0;
-        const int upto = wave_scan_add(tiles, lane);
-        const uint64_t past = __ballot(t < before + upto);
-        if (past != 0) {
-            const int l = __builtin_ctzll(past);
-            r.group = base + l;
-            r.begin = __builtin_amdgcn_readlane(lo, l);
-            r.end = __builtin_amdgcn_readlane(hi, l);
-            r.tiles = __builtin_amdgcn_readlane(tiles, l);
-            r.first = __builtin_amdgcn_readlane(before + upto, l) - r.tiles;
+        const GroupLanes v = group_lanes<ROWS>(offsets, groups, rows, base);
+        if (span_in(v, base, before, t, r)) {
             return r;
         }
-        before += __builtin_amdgcn_readlane(upto, 63);
+        before += __builtin_amdgcn_readlane(v.upto, 63);
     }
     return r;
 }
@@ -118,28 +148,27 @@ template <int ROWS>
 __device__ __forceinline__ GroupWork find_work(const int* offsets, int groups, int rows, int blocks,
                                                int b)
 {
-    const int lane = threadIdx.x & 63;
     // offsets that decrease can name more tiles than the grid has: cut there, so
     // that no number below passes 32 bits
     const int most = (int)gridDim.x / blocks;
-    int total = 0;
-    for (int g = lane; g < groups; g += 64) {
-        const int lo = min(max(offsets[g], 0), rows);
-        const int hi = min(max(offsets[g + 1], 0), rows);
-        total = min(total + (hi > lo ? (hi - lo - 1) / ROWS + 1 : 0), most);
+    const GroupLanes v = group_lanes<ROWS>(offsets, groups, rows, 0);
+    int total = min(__builtin_amdgcn_readlane(v.upto, 63), most);
+    for (int base = 64; base < groups; base += 64) {
+        const GroupLanes o = group_lanes<ROWS>(offsets, groups, rows, base);
+        total = min(total + __builtin_amdgcn_readlane(o.upto, 63), most);
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        total += __shfl_xor(total, off, 64);
-    }
-    total = min(__builtin_amdgcn_readfirstlane(total), most) * blocks;
+    total *= blocks;
     const int share = (total + 7) / 8;
     const int at = (b & 7) * share + (b >> 3);
     GroupWork r = {{0, 0, 0}, 0};
     if ((b >> 3) >= share || at >= total) {
         return r;
     }
-    const GroupSpan s = find_span<ROWS>(offsets, groups, rows, at / blocks);
+    // one look at the offsets is enough for 64 groups
+    GroupSpan s = {0, 0, 0, 0, 0};
+    if (!span_in(v, 0, 0, at / blocks, s)) {
+        s = find_span<ROWS>(offsets, groups, rows, at / blocks);
+    }
     const int in = at - s.first * blocks;              // within the group
     r.block = in / s.tiles;
     r.tile.group = s.group;

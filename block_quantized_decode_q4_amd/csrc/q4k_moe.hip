@@ -393,7 +393,7 @@ group_place_kernel(RouteArgs a)
         for (int base = 0; base < G; base += 64) {
             const int g = base + lane;
             const int v = g < G ? part[g] : 0;
-            const int upto = wave_scan_add(v, lane);
+            const int upto = wave_scan_add(v);
             if (g < G) {
                 begin[g] = sum + upto - v;
             }
