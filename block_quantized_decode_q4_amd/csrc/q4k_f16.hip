@@ -379,7 +379,10 @@ f16_gemm_grouped_kernel(const _Float16* __restrict__ w16, const _Float16* __rest
                         float* __restrict__ y, GroupRows rows, int n, int k, int NT)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    const GroupWork work = find_work<BM>(rows.offsets, rows.groups, rows.rows, NT, blockIdx.x);
+    const GroupTiles tiles =
+        count_tiles<BM>(rows.offsets, rows.groups, rows.rows, (int)gridDim.x / NT);
+    const GroupWork work =
+        find_work<BM>(tiles, rows.offsets, rows.groups, rows.rows, NT, blockIdx.x);
     const GroupTile t = work.tile;
     if (t.count == 0) {
         return;

@@ -345,12 +345,13 @@ __device__ __forceinline__ h8_t operand(uint32_t D, h2_t sl, h2_t sh)
 constexpr int kWaves = 4;
 
 template <int T>
-__global__ void __launch_bounds__(64 * kWaves, 3)
-grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
+constexpr int kWaveLds = T * 1024 > kWStage ? T * 1024 : kWStage;   // weights, then sums
+
+template <int T>
+__device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupTiles& tiles,
+                                              int row_blocks, int kw_log2, unsigned char* smem)
 {
-    // a wave's weights; its sums take their place
-    constexpr int kLds = T * 1024 > kWStage ? T * 1024 : kWStage;
-    __shared__ __align__(16) unsigned char smem[kWaves * kLds];
+    constexpr int kLds = kWaveLds<T>;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     // wave-uniform, as are all addresses but the lanes' 32-bit offsets below
@@ -358,7 +359,7 @@ grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
     const int j = lane & 15;
     const int g = lane >> 4;
     const GroupWork work =
-        find_work<kTile>(a.g.offsets, a.g.groups, a.g.rows, row_blocks, blockIdx.x);
+        find_work<kTile>(tiles, a.g.offsets, a.g.groups, a.g.rows, row_blocks, blockIdx.x);
     const GroupTile t = work.tile;
     if (t.count == 0) {
         return;
@@ -507,6 +508,38 @@ grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
     }
 }
 
+constexpr int kCus = 256;
+
+template <int T>
+__global__ void __launch_bounds__(64 * kWaves, 3)
+grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
+{
+    __shared__ __align__(16) unsigned char smem[kWaves * kWaveLds<T>];
+    const GroupTiles t =
+        count_tiles<kTile>(a.g.offsets, a.g.groups, a.g.rows, (int)gridDim.x / row_blocks);
+    grouped_tiles<T>(a, t, row_blocks, kw_log2, smem);
+}
+
+// T = 8 or, in fine_blocks, T = 4, by the number of tiles, which the host does not
+// know: rounds of the chip times the work of one, a tile of the finer cut counting
+// 9/8 (x is read twice as often).  So the finer cut is taken where the coarse one
+// leaves much of its last round empty: ten tiles of 4096 x 14336, 320 workgroups
+// at T = 8, 105 us against 96 us; eight tiles, 256 workgroups, 78 us against 87 us.
+__global__ void __launch_bounds__(64 * kWaves, 3)
+grouped_either_kernel(GroupedArgs a, int row_blocks, int fine_blocks, int kw_log2)
+{
+    __shared__ __align__(16) unsigned char smem[kWaves * kWaveLds<8>];
+    const GroupTiles t =
+        count_tiles<kTile>(a.g.offsets, a.g.groups, a.g.rows, (int)gridDim.x / fine_blocks);
+    const int coarse = (t.tiles * row_blocks + kCus - 1) / kCus;
+    const int fine = (t.tiles * fine_blocks + kCus - 1) / kCus;
+    if (coarse * 2 * 8 <= fine * 9) {
+        grouped_tiles<8>(a, t, row_blocks, kw_log2, smem);
+    } else {
+        grouped_tiles<4>(a, t, fine_blocks, kw_log2, smem);
+    }
+}
+
 // How the rows are cut: T row tiles per wave and kw waves along k.
 //  - T = 2 while T = 4 would give fewer workgroups than CUs (one token, two
 //    experts 4096 x 14336: 25.6 us against 35.1);
@@ -514,12 +547,13 @@ grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
 //    tiles (eight experts 4096 x 14336 with 16 positions each 83 us against 93,
 //    128 positions each 141 / 157 us), and T = 4 otherwise (one token, eight of
 //    64 experts 1536 x 2048: 11.7 us against 15.3).
-//  - kw = 4, so that a row's loads are 576 consecutive bytes, but less at T = 8
-//    where more than a fifth of the waves' steps would find no superblock
-//    (k = 1536, 32 positions a group: kw 4 / 2 88.5 / 80.0 us; with few rows the
-//    shorter way is as good, 17.2 / 18.7 us at k = 1536, 4 tokens).
+//  - kw = 4, so that a row's loads are 576 consecutive bytes, but less where more
+//    than a fifth of the waves' steps would find no superblock (k = 1536, 64
+//    experts of 2048 rows with two positions each: kw 4 / 2 39.5 / 34.9 us); T = 2
+//    keeps 4, the shorter way.
 struct GroupedCut {
-    int T, kw_log2, blocks;            // blocks of rows
+    int T, kw_log2;
+    int blocks, fine;                  // blocks of rows
     int64_t grid;
 };
 
@@ -531,12 +565,16 @@ GroupedCut grouped_cut(int64_t rows, int64_t groups, int64_t n, int64_t k)
     c.T = tiles * ((n + 63) / 64) < 256 ? 2 : rows >= 8 * groups ? 8 : 4;
     c.kw_log2 = 2;
     auto steps = [&](int log2) { return (((S - 1) >> log2) + 1) << log2; };  // of all parts
-    while (c.T == 8 && c.kw_log2 > 0 && steps(c.kw_log2) * 4 > S * 5) {
+    while (c.T > 2 && c.kw_log2 > 0 && steps(c.kw_log2) * 4 > S * 5) {
         --c.kw_log2;
     }
     const int64_t per = 16 * c.T * (kWaves >> c.kw_log2);
     c.blocks = (int)((n + per - 1) / per);
-    c.grid = (tiles * c.blocks + 7) / 8 * 8;
+    // The finer cut's larger grid is only worth its empty workgroups (16 tiles of
+    // 4096 x 2048, 23 possible: 26.5 us instead of 24.7) while two rounds of the
+    // chip hold the coarse one.
+    c.fine = c.T == 8 && tiles * c.blocks <= 2 * kCus ? (int)((2 * n + per - 1) / per) : 0;
+    c.grid = (tiles * (c.fine > 0 ? c.fine : c.blocks) + 7) / 8 * 8;
     return c;
 }
 
@@ -573,6 +611,9 @@ hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream)
         hipLaunchKernelGGL(grouped_kernel<2>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
     } else if (c.T == 4) {
         hipLaunchKernelGGL(grouped_kernel<4>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+    } else if (c.fine > 0) {
+        hipLaunchKernelGGL(grouped_either_kernel, grid, block, 0, stream, a, c.blocks, c.fine,
+                           c.kw_log2);
     } else {
         hipLaunchKernelGGL(grouped_kernel<8>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
     }

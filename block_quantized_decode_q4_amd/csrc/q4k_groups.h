@@ -144,20 +144,33 @@ struct GroupWork {
     int block;
 };
 
+// Tiles of all groups, and the first 64 groups' lanes
+struct GroupTiles {
+    GroupLanes first;
+    int tiles;
+};
+
+// most: as many tiles as the grid has (offsets that decrease can name more),
+// so that no number below passes 32 bits
 template <int ROWS>
-__device__ __forceinline__ GroupWork find_work(const int* offsets, int groups, int rows, int blocks,
-                                               int b)
+__device__ __forceinline__ GroupTiles count_tiles(const int* offsets, int groups, int rows,
+                                                  int most)
 {
-    // offsets that decrease can name more tiles than the grid has: cut there, so
-    // that no number below passes 32 bits
-    const int most = (int)gridDim.x / blocks;
-    const GroupLanes v = group_lanes<ROWS>(offsets, groups, rows, 0);
-    int total = min(__builtin_amdgcn_readlane(v.upto, 63), most);
+    GroupTiles r;
+    r.first = group_lanes<ROWS>(offsets, groups, rows, 0);
+    r.tiles = min(__builtin_amdgcn_readlane(r.first.upto, 63), most);
     for (int base = 64; base < groups; base += 64) {
         const GroupLanes o = group_lanes<ROWS>(offsets, groups, rows, base);
-        total = min(total + __builtin_amdgcn_readlane(o.upto, 63), most);
+        r.tiles = min(r.tiles + __builtin_amdgcn_readlane(o.upto, 63), most);
     }
-    total *= blocks;
+    return r;
+}
+
+template <int ROWS>
+__device__ __forceinline__ GroupWork find_work(const GroupTiles& tiles, const int* offsets,
+                                               int groups, int rows, int blocks, int b)
+{
+    const int total = tiles.tiles * blocks;
     const int share = (total + 7) / 8;
     const int at = (b & 7) * share + (b >> 3);
     GroupWork r = {{0, 0, 0}, 0};
@@ -166,7 +179,7 @@ __device__ __forceinline__ GroupWork find_work(const int* offsets, int groups, i
     }
     // one look at the offsets is enough for 64 groups
     GroupSpan s = {0, 0, 0, 0, 0};
-    if (!span_in(v, 0, 0, at / blocks, s)) {
+    if (!span_in(tiles.first, 0, 0, at / blocks, s)) {
         s = find_span<ROWS>(offsets, groups, rows, at / blocks);
     }
     const int in = at - s.first * blocks;              // within the group

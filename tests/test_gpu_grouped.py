@@ -146,6 +146,9 @@ SIZES += [
     ([9, 12] * 10, 1010, 512), ([17, 3, 8] * 7, 1500, 768), ([8] * 20, 840, 1280),
     ([30, 5] * 10, 700, 1024),
 ]
+# the cut that the number of tiles decides: the coarse one, the fine one, and one
+# where fewer tiles are there than the sizes allow
+SIZES += [([40, 8], 20500, 256), ([40, 8], 4100, 512), ([0, 0, 70, 0, 0, 1], 5000, 1280)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "q8", "f16"])
