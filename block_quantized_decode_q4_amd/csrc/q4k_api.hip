@@ -1255,7 +1255,7 @@ int q4k_moe_combine(const float* y, const float* weights, const int32_t* ids,
     }
     if (n < 1 || n > kInt32Max / 2 || !in_range(topk, 1, q4k::kMaxTopk) ||
         !in_range(m, 1, kMaxRows) ||
-        !fits_launch(m * (n % 4 == 0 ? (n + 1023) / 1024 : (n + 255) / 256), 256)) {
+        !fits_launch(m * ((n + 1023) / 1024), 256)) {
         return Q4K_ERR_SHAPE;
     }
     if (!aligned16(y) || !aligned16(weights) || !aligned16(out) || !aligned16(ids) ||

@@ -121,7 +121,7 @@ struct NormArgs {
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
 
 // Routing and grouping (q4k_moe.hip).  logits null: the ids are given.
-constexpr int kFewSlots = 512;         // slots that one workgroup groups in one launch
+constexpr int kFewSlots = 192;         // slots that one workgroup groups in one launch
 constexpr int kMaxGroups = 1024;       // experts (ids) that routing and grouping take
 constexpr int kMaxTopk = 32;
 struct RouteArgs {

@@ -295,12 +295,16 @@ lora_down_kernel(LoraArgs a)
 }
 
 // y of a tile of 32 positions, 256 columns from blockIdx.y * 256 on, 64 per
-// wave; 64 ranks of v and B at a time in LDS.  VB: rows of B are multiples of
-// eight halves; VY: rows of y and base multiples of four floats.
+// wave; 64 ranks of v and B at a time in LDS.  Rows of any n and r begin on any
+// element: the accesses of B, base and y ask for an element's alignment only (rank
+// 61, n = 4095, 2048 rows, both products: 66 us element by element, 37 us so).
+// WHOLE: r is a multiple of eight, so that no eight ranks pass the end of B.
+typedef uint32_t u4u_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));
 constexpr int kBPitch = 72;            // halves per row of v or B (9 pieces of 16 bytes)
 constexpr int kYPitch = kUpCols + 4;   // floats per row of the products (65 pieces)
 
-template <int PARTS, bool VB, bool VY>
+template <int PARTS, bool WHOLE>
 __global__ void __launch_bounds__(256, 3)
 lora_up_kernel(LoraArgs a)
 {
@@ -327,7 +331,8 @@ lora_up_kernel(LoraArgs a)
     }
     const int rank = rank_of(a, t.group);
     const int pitch = (a.r + 15) / 16 * 16;
-    const _Float16* const bg = static_cast<const _Float16*>(a.b) + ((int64_t)t.group * a.n + col0) * a.r;
+    const _Float16* const bg =
+        static_cast<const _Float16*>(a.b) + ((int64_t)t.group * a.n + col0) * a.r;
     const f4_t zero = {0.f, 0.f, 0.f, 0.f};
     f4_t total[U][4];                          // [16 positions][16 columns]
 #pragma unroll
@@ -361,44 +366,52 @@ lora_up_kernel(LoraArgs a)
             }
         }
     };
-    // B (VB): eight ranks of every 32nd column
+    // B: eight ranks of every 32nd column
     u4_t w[kUpCols / 32];
     const int bq = (tid & 7) * 8;
     auto load_b = [&](int k0) __attribute__((always_inline)) {
-        const char* const from = reinterpret_cast<const char*>(bg + k0);
+        const _Float16* const first = bg + k0;
+        const char* const from = reinterpret_cast<const char*>(first);
         const int q = min(bq, max(rank - k0 - 1, 0) / 8 * 8);
+        // the last half that eight may begin at, from `first` on
+        const int64_t halves = ((int64_t)(a.adapters - t.group) * a.n - col0) * a.r - k0;
+        const int end = (int)min(halves, (int64_t)1 << 30) - 8;
 #pragma unroll
         for (int i = 0; i < kUpCols / 32; ++i) {
-            const int c = min(32 * i + (tid >> 3), a.n - 1 - col0);
-            w[i] = *reinterpret_cast<const u4_t*>(from + (uint32_t)(c * a.r + q) * 2u);
+            const int at = min(32 * i + (tid >> 3), a.n - 1 - col0) * a.r + q;
+            if constexpr (WHOLE) {
+                w[i] = *reinterpret_cast<const u4u_t*>(from + (uint32_t)at * 2u);
+            } else {
+                if (end >= 0) {
+                    w[i] = *reinterpret_cast<const u4u_t*>(from + (uint32_t)min(at, end) * 2u);
+                }
+                if (at > end) {                    // the last columns: one by one
+                    h8_t v;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = at + e < end + 8 ? first[at + e] : (_Float16)0;
+                    }
+                    w[i] = __builtin_bit_cast(u4_t, v);
+                }
+            }
         }
     };
     load_v(0);
-    if constexpr (VB) {
-        load_b(0);
-    }
+    load_b(0);
     // the base (a row of y is this wave's alone, so base may be y)
     const int lane_row = a.order ? ordered : mine;
     int row[kOwn];
     f4_t base[kOwn];
+    const bool four = a.base != nullptr && a.n >= 4;
 #pragma unroll
     for (int q = 0; q < kOwn; ++q) {
         row[q] = wave + 4 * q < t.count ? __builtin_amdgcn_readlane(lane_row, q) : -1;
         row[q] = row[q] < a.rows ? row[q] : -1;
-        const float* const from =
-            a.base ? a.base + (int64_t)max(row[q], 0) * a.n + col0 : a.v;
-        if constexpr (VY) {                            // n % 4 == 0
-            const int c = a.base ? min(4 * lane, a.n - 4 - col0) : 0;
-            base[q] = *reinterpret_cast<const f4_t*>(reinterpret_cast<const char*>(from) +
-                                                     (uint32_t)c * 4u);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = a.base ? min(64 * e + lane, a.n - 1 - col0) : 0;
-                base[q][e] = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(from) +
-                                                             (uint32_t)c * 4u);
-            }
-        }
+        // the last columns read the row's last four (n >= 4), and again below
+        const float* const from = four ? a.base + (int64_t)max(row[q], 0) * a.n : a.v;
+        const int c = four ? min(col0 + 4 * lane, a.n - 4) : 0;
+        base[q] = *reinterpret_cast<const f4u_t*>(reinterpret_cast<const char*>(from) +
+                                                  (uint32_t)c * 4u);
     }
     // a row's scale so far: 2^-seen brings the largest |v| into [2^14, 2^15)
     int seen[U];
@@ -410,9 +423,7 @@ lora_up_kernel(LoraArgs a)
         if (k0 > 0) {
             __syncthreads();
             load_v(k0);
-            if constexpr (VB) {
-                load_b(k0);
-            }
+            load_b(k0);
         }
         const int left = rank - k0;
 #pragma unroll
@@ -459,27 +470,15 @@ lora_up_kernel(LoraArgs a)
                 steps[p] = step;
             }
         }
-        if constexpr (VB) {
-            u4_t keep;                                 // the halves below the rank
+        u4_t keep;                                     // the halves below the rank
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                const int have = left - bq - 2 * d;
-                keep[d] = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
-            }
+        for (int d = 0; d < 4; ++d) {
+            const int have = left - bq - 2 * d;
+            keep[d] = have >= 2 ? 0xFFFFFFFFu : have == 1 ? 0xFFFFu : 0u;
+        }
 #pragma unroll
-            for (int i = 0; i < kUpCols / 32; ++i) {
-                *reinterpret_cast<u4_t*>(bs + (32 * i + (tid >> 3)) * kBPitch + bq) = w[i] & keep;
-            }
-        } else {
-            // a row of B per wave and load, a rank per lane
-#pragma unroll 16
-            for (int c = wave; c < kUpCols; c += 4) {
-                _Float16 w = (_Float16)0;
-                if (col0 + c < a.n && lane < left) {
-                    w = bg[c * a.r + k0 + lane];
-                }
-                bs[c * kBPitch + lane] = w;
-            }
+        for (int i = 0; i < kUpCols / 32; ++i) {
+            *reinterpret_cast<u4_t*>(bs + (32 * i + (tid >> 3)) * kBPitch + bq) = w[i] & keep;
         }
         __syncthreads();
         if (k0 > 0) {                              // sums so far, in the new scale
@@ -548,19 +547,14 @@ lora_up_kernel(LoraArgs a)
         }
         const float* const yp = ys + (wave + 4 * q) * kYPitch;
         float* const out = a.y + (int64_t)row[q] * a.n;
-        if constexpr (VY) {
-            const int c = col0 + 4 * lane;
-            if (c < a.n) {
-                *reinterpret_cast<f4_t*>(out + c) =
-                    base[q] + *reinterpret_cast<const f4_t*>(yp + 4 * lane);
-            }
+        const int c = col0 + 4 * lane;
+        if (a.n - c >= 4) {
+            *reinterpret_cast<f4u_t*>(out + c) =
+                base[q] + *reinterpret_cast<const f4_t*>(yp + 4 * lane);
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = col0 + 64 * e + lane;
-                if (c < a.n) {
-                    out[c] = base[q][e] + yp[64 * e + lane];
-                }
+            for (int e = 0; e < a.n - c; ++e) {
+                const float b = a.base ? a.base[(int64_t)row[q] * a.n + c + e] : 0.f;
+                out[c + e] = b + yp[4 * lane + e];
             }
         }
     }
@@ -569,16 +563,10 @@ lora_up_kernel(LoraArgs a)
 template <int PARTS>
 void launch_up(const LoraArgs& a, dim3 up, hipStream_t stream)
 {
-    const bool vb = a.r % 8 == 0;
-    const bool vy = a.n % 4 == 0;
-    if (vb && vy) {
-        hipLaunchKernelGGL((lora_up_kernel<PARTS, true, true>), up, dim3(256), 0, stream, a);
-    } else if (vb) {
-        hipLaunchKernelGGL((lora_up_kernel<PARTS, true, false>), up, dim3(256), 0, stream, a);
-    } else if (vy) {
-        hipLaunchKernelGGL((lora_up_kernel<PARTS, false, true>), up, dim3(256), 0, stream, a);
+    if (a.r % 8 == 0) {
+        hipLaunchKernelGGL((lora_up_kernel<PARTS, true>), up, dim3(256), 0, stream, a);
     } else {
-        hipLaunchKernelGGL((lora_up_kernel<PARTS, false, false>), up, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((lora_up_kernel<PARTS, false>), up, dim3(256), 0, stream, a);
     }
 }
 

@@ -478,23 +478,29 @@ group_place_kernel(RouteArgs a)
 }
 
 // out[t][c] = residual[t][c] + sum_j weights[t][j] y[t * topk + j][c], over
-// the choices with an id (f32, in the order of j).  A thread owns V
-// consecutive columns of one token.
+// the choices with an id (f32, in the order of j).  A thread owns V consecutive
+// columns of one token; with V = 4 (n >= 4) a row's last ones read the row's last
+// four and write what is theirs.  Rows of any n begin on any element: the accesses
+// ask for an element's alignment only (4096 tokens, topk 2, n = 4095, residual: one
+// column a thread 88 us, four 48 us).
+typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));
+
 template <int V>
 __global__ void __launch_bounds__(256)
 combine_kernel(CombineArgs a)
 {
     const int64_t t = blockIdx.x / a.parts;
-    const int c = ((int)(blockIdx.x % a.parts) * 256 + (int)threadIdx.x) * V;
+    const int c = ((int)(blockIdx.x % a.parts) * (int)blockDim.x + (int)threadIdx.x) * V;
     if (c >= a.n) {
         return;
     }
+    const int from = min(c, a.n - V);
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         acc[i] = 0.f;
     }
-    const float* y = a.y + t * a.topk * a.n + c;
+    const float* y = a.y + t * a.topk * a.n + from;
 #pragma unroll 4
     for (int j = 0; j < a.topk; ++j) {
         const float w = a.weights[t * a.topk + j];
@@ -503,27 +509,37 @@ combine_kernel(CombineArgs a)
         }
         const float* p = y + (int64_t)j * a.n;
         if constexpr (V == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(p);
-            acc[0] = __builtin_fmaf(w, v.x, acc[0]);
-            acc[1] = __builtin_fmaf(w, v.y, acc[1]);
-            acc[2] = __builtin_fmaf(w, v.z, acc[2]);
-            acc[3] = __builtin_fmaf(w, v.w, acc[3]);
+            const f4u_t v = *reinterpret_cast<const f4u_t*>(p);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+            }
         } else {
             acc[0] = __builtin_fmaf(w, p[0], acc[0]);
         }
     }
+    float* const out = a.out + t * a.n + from;
     if constexpr (V == 4) {
+        f4u_t r = {acc[0], acc[1], acc[2], acc[3]};
         if (a.residual != nullptr) {
-            const float4 r = *reinterpret_cast<const float4*>(a.residual + t * a.n + c);
-            acc[0] += r.x; acc[1] += r.y; acc[2] += r.z; acc[3] += r.w;
+            r += *reinterpret_cast<const f4u_t*>(a.residual + t * a.n + from);
         }
-        *reinterpret_cast<float4*>(a.out + t * a.n + c) =
-            make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (from == c) {
+            *reinterpret_cast<f4u_t*>(out) = r;
+        } else {
+            // out may be residual: the elements before c are another thread's
+#pragma unroll
+            for (int i = 1; i < V; ++i) {
+                if (from + i >= c) {
+                    out[i] = r[i];
+                }
+            }
+        }
     } else {
         if (a.residual != nullptr) {
             acc[0] += a.residual[t * a.n + c];
         }
-        a.out[t * a.n + c] = acc[0];
+        out[0] = acc[0];
     }
 }
 
@@ -569,13 +585,15 @@ hipError_t launch_route_t(RouteArgs a, hipStream_t stream)
 }  // namespace
 
 // Whether one workgroup does it all: few enough slots to count each place
-// directly, and (routing) the tokens in two passes of its waves.  Beyond, two
-// launches over the chip are faster (191 tokens of 85 experts: 20 us in one
-// workgroup with a token per wave, 10 us in two launches).
+// directly (the work is their square), and (routing) the tokens in a pass or two
+// of its waves.  One workgroup against two launches over the chip, a call: 64
+// slots 5.8 / 8.5 us, 192 slots 7.5 / 8.6 us, 256 slots 9.3 / 8.6 us; routing, topk
+// 8: 8 tokens of 64 experts 6.7 / 9.4 us, 24 tokens 9.9 / 9.8 us, 64 tokens 23 /
+// 10 us, 8 tokens of 512 experts 7.5 / 10 us, 30 tokens 21 / 11 us.
 bool group_in_one(int64_t slots, int64_t groups, int64_t topk, bool route)
 {
-    const int64_t pass = kPlaceThreads / (groups <= kRowExperts ? 16 : 64);
-    return slots <= kFewSlots && (!route || slots <= 2 * pass * topk);
+    const int64_t tokens = groups <= kRowExperts ? 2 * kPlaceThreads / 16 : kPlaceThreads / 64;
+    return slots <= kFewSlots && (!route || slots <= tokens * topk);
 }
 
 size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk, bool route)
@@ -612,13 +630,15 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream)
 
 hipError_t launch_combine(CombineArgs a, hipStream_t stream)
 {
-    const int v = a.n % 4 == 0 ? 4 : 1;
-    a.parts = (a.n + 256 * v - 1) / (256 * v);
+    const int v = a.n >= 4 ? 4 : 1;
+    const int pieces = (a.n + v - 1) / v;
+    const int threads = pieces < 256 ? (pieces + 63) / 64 * 64 : 256;
+    a.parts = (pieces + threads - 1) / threads;
     const dim3 grid((unsigned)((int64_t)a.m * a.parts));
     if (v == 4) {
-        hipLaunchKernelGGL(combine_kernel<4>, grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(combine_kernel<4>, grid, dim3(threads), 0, stream, a);
     } else {
-        hipLaunchKernelGGL(combine_kernel<1>, grid, dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(combine_kernel<1>, grid, dim3(threads), 0, stream, a);
     }
     return hipGetLastError();
 }

@@ -33,38 +33,38 @@ namespace q4k {
 
 namespace {
 
-typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+// Rows of any length begin on any element: the vector accesses ask for an
+// element's alignment only (they cost the same; element by element, eight
+// consecutive ones to a lane, a row of 8189 took four times as long).
+typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x8_t __attribute__((ext_vector_type(8), aligned(2)));
+typedef _Float16 h8u_t __attribute__((ext_vector_type(8), aligned(2)));
 
-// Eight elements at p[0..], those at or beyond `left` as zero.  VEC: all
-// eight are there and p is 16-byte aligned.
-template <int TYPE, bool VEC>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int left, float* e)
+template <int TYPE>
+__device__ __forceinline__ float element(const void* base, int64_t at)
+{
+    if constexpr (TYPE == kTypeF32) {
+        return static_cast<const float*>(base)[at];
+    } else {
+        const uint16_t b = static_cast<const uint16_t*>(base)[at];
+        return TYPE == kTypeF16 ? (float)__builtin_bit_cast(_Float16, b)
+                                : __builtin_bit_cast(float, (uint32_t)b << 16);
+    }
+}
+
+// Eight elements of base from `at` on
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* base, int64_t at, float* e)
 {
     if constexpr (TYPE == kTypeF32) {
         const float* p = static_cast<const float*>(base) + at;
-        if constexpr (VEC) {
-            const float4 a = *reinterpret_cast<const float4*>(p);
-            const float4 b = *reinterpret_cast<const float4*>(p + 4);
-            e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
-            e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                e[i] = i < left ? p[i] : 0.f;
-            }
-        }
+        const f4u_t a = *reinterpret_cast<const f4u_t*>(p);
+        const f4u_t b = *reinterpret_cast<const f4u_t*>(p + 4);
+        e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w;
+        e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-        u16x8_t v;
-        if constexpr (VEC) {
-            v = *reinterpret_cast<const u16x8_t*>(p);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = i < left ? p[i] : (uint16_t)0;
-            }
-        }
+        const u16x8_t v =
+            *reinterpret_cast<const u16x8_t*>(static_cast<const uint16_t*>(base) + at);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint16_t b = v[i];
@@ -74,75 +74,108 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int left, fl
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(float* base, int64_t at, int left, const float* e)
+__device__ __forceinline__ void store8(float* p, const float* e)
 {
-    float* p = base + at;
-    if constexpr (VEC) {
-        *reinterpret_cast<float4*>(p) = make_float4(e[0], e[1], e[2], e[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(e[4], e[5], e[6], e[7]);
+    *reinterpret_cast<f4u_t*>(p) = f4u_t{e[0], e[1], e[2], e[3]};
+    *reinterpret_cast<f4u_t*>(p + 4) = f4u_t{e[4], e[5], e[6], e[7]};
+}
+
+// Where the group at column c is read: TAIL (k is no multiple of eight), a last
+// group that is not whole reads the row's last eight elements and is then read
+// again element by element.
+template <bool TAIL>
+__device__ __forceinline__ int read_at(const NormArgs& a, int c)
+{
+    return TAIL ? min(c, a.k - 8) : c;
+}
+
+// h of the group at column c: x + residual (rounded once), or x; zeros beyond
+// the row
+template <int TYPE, bool TAIL>
+__device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c, float* h)
+{
+    if (!TAIL || a.k >= 8) {
+        load8<TYPE>(a.x, row * a.x_stride + read_at<TAIL>(a, c), h);
+        if (a.residual != nullptr) {
+            float r[8];
+            load8<kTypeF32>(a.residual, row * a.k + read_at<TAIL>(a, c), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                h[i] += r[i];
+            }
+        }
+    }
+    if (TAIL && a.k - c < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[i] = 0.f;
+            if (c + i < a.k) {
+                h[i] = element<TYPE>(a.x, row * a.x_stride + c + i);
+                h[i] += a.residual != nullptr ? a.residual[row * a.k + c + i] : 0.f;
+            }
+        }
+    }
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void put_f32(const NormArgs& a, float* base, int64_t row, int c,
+                                        const float* e)
+{
+    float* const p = base + row * a.k + c;
+    if (!TAIL || a.k - c >= 8) {
+        store8(p, e);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i < left) {
+            if (c + i < a.k) {
                 p[i] = e[i];
             }
         }
     }
 }
 
-// h of the group at column c: x + residual (rounded once), or x.  XVEC: x's
-// rows are 16-byte aligned too.
-template <int TYPE, bool VEC, bool XVEC>
-__device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c, float* h)
-{
-    const int left = a.k - c;
-    load8<TYPE, XVEC>(a.x, row * a.x_stride + c, left, h);
-    if (a.residual != nullptr) {
-        float r[8];
-        load8<kTypeF32, VEC>(a.residual, row * a.k + c, left, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            h[i] += r[i];
-        }
-    }
-}
-
 // The outputs of one group from its h (and the row's factor r)
-template <bool VEC>
+template <bool TAIL>
 __device__ __forceinline__ void put_y(const NormArgs& a, int64_t row, int c, const float* h,
                                       double r)
 {
-    const int left = a.k - c;
     float w[8], y[8];
-    load8<kTypeF32, VEC>(a.weight, c, left, w);
+    if (!TAIL || a.k >= 8) {
+        load8<kTypeF32>(a.weight, read_at<TAIL>(a, c), w);
+    }
+    if (TAIL && a.k - c < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = c + i < a.k ? a.weight[c + i] : 0.f;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[i] = (float)((double)h[i] * r * (double)w[i]);
     }
     const int64_t at = row * a.k + c;
     if (a.y != nullptr) {
-        store8<VEC>(a.y, at, left, y);
+        put_f32<TAIL>(a, a.y, row, c, y);
     }
     if (a.y16 != nullptr) {
-        h8_t v;
+        h8u_t v;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[i] = (_Float16)y[i];
         }
         _Float16* p = static_cast<_Float16*>(a.y16) + at;
-        if constexpr (VEC) {
-            *reinterpret_cast<h8_t*>(p) = v;
+        if (!TAIL || a.k - c >= 8) {
+            *reinterpret_cast<h8u_t*>(p) = v;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (i < left) {
+                if (c + i < a.k) {
                     p[i] = v[i];
                 }
             }
         }
     }
-    if constexpr (VEC) {
+    if constexpr (!TAIL) {
         if (a.q != nullptr) {              // k % 32 == 0: four whole groups per block
             float amax = 0.f;
             int nan = 0;
@@ -171,9 +204,8 @@ __device__ __forceinline__ void put_y(const NormArgs& a, int64_t row, int c, con
 }
 
 // P: groups of eight elements that a thread keeps in registers; the groups
-// beyond P * threads are read twice.  VEC: 16-byte accesses (k a multiple of
-// eight); XVEC: for x too (and its row stride).
-template <int TYPE, int P, bool VEC, bool XVEC>
+// beyond P * threads are read twice.
+template <int TYPE, int P, bool TAIL>
 __global__ void __launch_bounds__(1024)
 rmsnorm_kernel(NormArgs a)
 {
@@ -181,14 +213,14 @@ rmsnorm_kernel(NormArgs a)
     const int64_t row = blockIdx.x;
     const int tid = threadIdx.x;
     const int threads = blockDim.x;
-    const int groups = (a.k + 7) / 8;
+    const int groups = (a.k - 1) / 8 + 1;
     float h[P][8];
     double sum = 0.0;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int gi = p * threads + tid;
         if (gi < groups) {
-            load_h<TYPE, VEC, XVEC>(a, row, gi * 8, h[p]);
+            load_h<TYPE, TAIL>(a, row, gi * 8, h[p]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -200,7 +232,7 @@ rmsnorm_kernel(NormArgs a)
     for (int p = 0; p < P; ++p) {
         const int gi = p * threads + tid;
         if (a.sum != nullptr && gi < groups) {
-            store8<VEC>(a.sum, row * a.k + gi * 8, a.k - gi * 8, h[p]);
+            put_f32<TAIL>(a, a.sum, row, gi * 8, h[p]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -209,9 +241,9 @@ rmsnorm_kernel(NormArgs a)
     }
     for (int gi = P * threads + tid; gi < groups; gi += threads) {
         float t[8];
-        load_h<TYPE, VEC, XVEC>(a, row, gi * 8, t);
+        load_h<TYPE, TAIL>(a, row, gi * 8, t);
         if (a.sum != nullptr) {
-            store8<VEC>(a.sum, row * a.k + gi * 8, a.k - gi * 8, t);
+            put_f32<TAIL>(a, a.sum, row, gi * 8, t);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -235,17 +267,22 @@ rmsnorm_kernel(NormArgs a)
     for (int p = 0; p < P; ++p) {
         const int gi = p * threads + tid;
         if (gi < groups) {
-            put_y<VEC>(a, row, gi * 8, h[p], r);
+            put_y<TAIL>(a, row, gi * 8, h[p], r);
         }
     }
     for (int gi = P * threads + tid; gi < groups; gi += threads) {
         float t[8];
-        if (a.sum != nullptr) {                // this thread's own stores
-            load8<kTypeF32, VEC>(a.sum, row * a.k + gi * 8, a.k - gi * 8, t);
+        if (a.sum != nullptr && (!TAIL || a.k - gi * 8 >= 8)) {
+            load8<kTypeF32>(a.sum, row * a.k + gi * 8, t);       // this thread's own stores
+        } else if (a.sum != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                t[i] = gi * 8 + i < a.k ? a.sum[row * a.k + gi * 8 + i] : 0.f;
+            }
         } else {
-            load_h<TYPE, VEC, XVEC>(a, row, gi * 8, t);
+            load_h<TYPE, TAIL>(a, row, gi * 8, t);
         }
-        put_y<VEC>(a, row, gi * 8, t, r);
+        put_y<TAIL>(a, row, gi * 8, t, r);
     }
 }
 
@@ -254,11 +291,9 @@ hipError_t launch_p(const NormArgs& a, int threads, hipStream_t stream)
 {
     const dim3 grid((unsigned)a.m), block(threads);
     if (a.k % 8 != 0) {
-        hipLaunchKernelGGL((rmsnorm_kernel<TYPE, P, false, false>), grid, block, 0, stream, a);
-    } else if (a.x_stride % 8 != 0) {
-        hipLaunchKernelGGL((rmsnorm_kernel<TYPE, P, true, false>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((rmsnorm_kernel<TYPE, P, true>), grid, block, 0, stream, a);
     } else {
-        hipLaunchKernelGGL((rmsnorm_kernel<TYPE, P, true, true>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((rmsnorm_kernel<TYPE, P, false>), grid, block, 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -266,7 +301,7 @@ hipError_t launch_p(const NormArgs& a, int threads, hipStream_t stream)
 template <int TYPE>
 hipError_t launch_t(const NormArgs& a, hipStream_t stream)
 {
-    const int groups = (a.k + 7) / 8;
+    const int groups = (a.k - 1) / 8 + 1;
     // One group per thread where a workgroup holds the row (8192 rows of 4096,
     // binary16 in and out, with the residual: 73 us, against 78 with two and 87
     // with four groups per thread; 64 rows 6.6 / 6.9 / 6.7 us).  Longer rows, four

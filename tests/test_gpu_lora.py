@@ -41,6 +41,10 @@ def _group(ids, adapters):
     (70, 70, 64, 129, 1024, "f16", True, "apart"), (100, 3, 65, 67, 136, "f32", True, "in place"),
     (257, 5, 130, 260, 320, "bf16", False, "none"), (600, 2, 4, 1024, 256, "f16", True, "apart"),
     (40, 90, 6, 50, 72, "f32", True, "apart"), (3, 2, 1024, 20, 64, "f16", True, "apart"),
+    # odd ranks and widths: pieces of B at its very end, rows of y on any element
+    (2, 1, 1, 3, 8, "f16", False, "in place"), (9, 1, 3, 2, 64, "f32", False, "in place"),
+    (37, 3, 7, 5, 128, "f16", False, "in place"), (600, 3, 61, 257, 256, "f16", True, "in place"),
+    (4100, 2, 13, 259, 64, "f32", False, "in place"), (50, 2, 67, 1023, 128, "bf16", True, "apart"),
 ])
 def test_lora(rows, adapters, r, n, k, kind, ragged, base):
     rng = np.random.default_rng(rows + adapters + r + n + k)

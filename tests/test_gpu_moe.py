@@ -73,7 +73,8 @@ def _route(logits, E, topk, m, renorm, stride=0, group=True):
 
 CASES = [(1, 1, 1), (1, 4, 2), (1, 64, 8), (8, 64, 8), (3, 65, 3), (64, 8, 2), (65, 8, 8),
          (100, 128, 8), (513, 5, 1), (300, 100, 7), (2000, 60, 6), (1000, 1024, 32),
-         (4097, 256, 8), (700, 512, 1), (16, 32, 32), (17, 32, 32), (1, 1024, 32)]
+         (4097, 256, 8), (700, 512, 1), (16, 32, 32), (17, 32, 32), (1, 1024, 32),
+         (24, 64, 8), (25, 64, 8), (128, 9, 1), (129, 9, 1), (16, 300, 4), (17, 300, 4)]
 
 
 @pytest.mark.parametrize("m,E,topk", CASES)
@@ -147,7 +148,9 @@ def test_group_all_in_one_and_none():
 
 @pytest.mark.parametrize("m,n,topk,residual,masked", [
     (1, 1, 1, False, False), (1, 2048, 8, True, False), (3, 1027, 2, True, True),
-    (5, 4096, 32, False, True), (700, 260, 3, True, True), (2, 33, 5, False, True)])
+    (5, 4096, 32, False, True), (700, 260, 3, True, True), (2, 33, 5, False, True),
+    (9, 2, 2, True, False), (9, 3, 1, True, True), (9, 5, 4, True, True), (40, 1023, 2, True, False),
+    (300, 1025, 3, True, True), (70, 7, 8, True, True)])
 def test_combine(m, n, topk, residual, masked):
     rng = np.random.default_rng(m + n)
     y = rng.standard_normal((m * topk, n)).astype(np.float32)

@@ -120,6 +120,27 @@ def test_rmsnorm_in_place_and_single_outputs():
         assert torch.equal(h2, h_d)
 
 
+@pytest.mark.parametrize("m,k", [(4, 1), (7, 5), (3, 9), (5, 2051), (2, 8189), (1100, 8201),
+                                 (2, 40961)])
+def test_rmsnorm_in_place_rows_of_odd_length(m, k):
+    """Groups that pass the end of a row: in place, nothing is added twice, and
+    the row behind stays."""
+    g = torch.Generator().manual_seed(k)
+    x = torch.randn((m, k), generator=g)
+    res = torch.randn((m, k), generator=g)
+    w = torch.randn(k, generator=g)
+    stream = torch.cat((res.reshape(-1), torch.full((16,), 3.0))).cuda()
+    y = torch.full((m * k + 16,), 3.0, device="cuda")
+    y16 = torch.full((m * k + 16,), 3.0, dtype=torch.float16, device="cuda")
+    q4k.q4k_rmsnorm(x.cuda(), w.cuda(), k, m, residual=stream, sum_out=stream, y=y, y16=y16)
+    h = x + res
+    assert torch.equal(stream[:m * k].cpu().view(m, k), h)
+    got = y[:m * k].cpu().numpy().reshape(m, k)
+    _check(got, _ref(h.numpy(), w.numpy(), 1e-5))
+    assert torch.equal(y16[:m * k], y[:m * k].half())
+    assert (stream[m * k:] == 3.0).all() and (y[m * k:] == 3.0).all() and (y16[m * k:] == 3.0).all()
+
+
 def test_rmsnorm_non_finite_rows():
     """An infinity: NaN there, 0 elsewhere; a NaN: the row; zeros with eps 0:
     NaN.  Other rows are untouched by it."""
