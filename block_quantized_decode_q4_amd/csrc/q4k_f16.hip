@@ -475,27 +475,40 @@ hipError_t launch_f16_gemm(const void* w16, const void* x16, float* y, int m, in
     return launch_f16_gemm_t<64, 64>(w16, x16, y, m, n, k, stream);
 }
 
-// The tile: 128 x 256 where the groups hold about a tile's positions and there
-// are at least half as many tiles as CUs, else 64 x 128, where a product is
-// mostly the mirror's bytes or the tiles are few.  Both sides measured: 128 x
-// 256 against 64 x 128 at 256 positions a group and 176 tiles 71 / 88 us, at
-// 128 positions and 900 tiles 139 / 138 us; at 64 positions and 176 tiles
-// 84 / 75 us, at 256 positions and 46 tiles 23 / 14 us.
-static bool f16_grouped_wide(int64_t rows, int64_t groups, int64_t n)
-{
-    return rows >= 96 * groups && most_tiles(rows, groups, 128) * ((n + 255) / 256) >= 128;
-}
+// The tile.  64 x 128 where the groups are short or the tiles few: a product is
+// mostly the mirror's bytes then (128 x 256 against 64 x 128 at 64 positions a
+// group and 176 tiles 84 / 75 us, at 256 positions and 46 tiles 23 / 14 us; at 256
+// positions and 176 tiles 71 / 88 us).  Else 128 rows by 256 or 192 columns, which
+// are as fast per column; one workgroup of the first fits a CU, two of the second.
+// 256 while the rounds of the chip times the columns of one say so (a group of any
+// length ends half a tile early), up to four rounds; beyond, 192, whose last round
+// is shorter.  256 / 192 columns, uneven groups: 19 tiles of n = k = 4096 138 / 114
+// us, 25 tiles of n 4096, k 2048 85 / 91 us, 95 tiles of n 1001, k 2048 94 / 102 us, 37
+// tiles of n 14336, k 4096 633 / 594 us, 36 tiles 593 / 598 us.
+constexpr int64_t kCus = 256;
 
-template <int BM, int BN>
-static int64_t f16_grouped_tiles(int64_t rows, int64_t groups, int64_t n)
+struct F16GroupedTile {
+    int rows, columns;
+};
+
+static F16GroupedTile f16_grouped_tile(int64_t rows, int64_t groups, int64_t n)
 {
-    return (most_tiles(rows, groups, BM) * ((n + BN - 1) / BN) + 7) / 8 * 8;
+    if (rows < 96 * groups || most_tiles(rows, groups, 128) * ((n + 255) / 256) < 128) {
+        return {64, 128};
+    }
+    const int64_t halves = rows / 64 + groups;         // twice the tiles to expect
+    const int64_t wide = halves * ((n + 255) / 256), narrow = halves * ((n + 191) / 192);
+    auto rounds = [](int64_t half_tiles) { return (half_tiles + 2 * kCus - 1) / (2 * kCus); };
+    if (rounds(narrow) > 4 || rounds(narrow) * 192 < rounds(wide) * 256) {
+        return {128, 192};
+    }
+    return {128, 256};
 }
 
 int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n)
 {
-    return f16_grouped_wide(rows, groups, n) ? f16_grouped_tiles<128, 256>(rows, groups, n)
-                                             : f16_grouped_tiles<64, 128>(rows, groups, n);
+    const F16GroupedTile t = f16_grouped_tile(rows, groups, n);
+    return (most_tiles(rows, groups, t.rows) * ((n + t.columns - 1) / t.columns) + 7) / 8 * 8;
 }
 
 template <int BM, int BN, int WM, int WN>
@@ -503,7 +516,7 @@ static hipError_t launch_f16_grouped_t(const void* w16, const void* x16, float* 
                                        const GroupRows& g, int n, int k, hipStream_t stream)
 {
     const int NT = (n + BN - 1) / BN;
-    const int64_t grid = f16_grouped_tiles<BM, BN>(g.rows, g.groups, n);
+    const int64_t grid = f16_grouped_grid(g.rows, g.groups, n);
     hipLaunchKernelGGL((f16_gemm_grouped_kernel<BM, BN, WM, WN>), dim3((unsigned)grid),
                        dim3(64 * WM * WN), 2 * (BM + BN) * kGK * 2, stream,
                        static_cast<const _Float16*>(w16), static_cast<const _Float16*>(x16), y, g,
@@ -514,8 +527,12 @@ static hipError_t launch_f16_grouped_t(const void* w16, const void* x16, float* 
 hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
                                    int n, int k, hipStream_t stream)
 {
-    if (f16_grouped_wide(g.rows, g.groups, n)) {
+    const F16GroupedTile t = f16_grouped_tile(g.rows, g.groups, n);
+    if (t.columns == 256) {
         return launch_f16_grouped_t<128, 256, 2, 4>(w16, x16, y, g, n, k, stream);
+    }
+    if (t.columns == 192) {
+        return launch_f16_grouped_t<128, 192, 2, 4>(w16, x16, y, g, n, k, stream);
     }
     return launch_f16_grouped_t<64, 128, 2, 4>(w16, x16, y, g, n, k, stream);
 }

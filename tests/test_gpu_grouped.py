@@ -166,10 +166,12 @@ def test_grouped_sizes(kind, sizes, n, k):
 
 
 def test_grouped_f16_wide_tiles():
-    """Shapes that take the 128 x 256 tile (groups of about a tile or more and
-    enough of them), ragged in rows and columns; sampled columns."""
+    """Shapes that take the 128-row tiles (groups of about a tile or more and
+    enough of them), ragged in rows and columns; of 256 columns (the third) and of
+    192 (the last)."""
     rng = np.random.default_rng(14)
-    for sizes, n, k in (([300, 0, 5, 190], 8229, 128), ([129, 128, 127], 12300, 192)):
+    for sizes, n, k in (([300, 0, 5, 190], 8229, 128), ([129, 128, 127], 12300, 192),
+                        ([200], 32700, 64), ([200], 16400, 64)):
         groups, rows = len(sizes), sum(sizes)
         w = torch.randn((groups, n, k), generator=torch.Generator("cuda").manual_seed(n),
                         device="cuda").mul_(0.05).half()
