@@ -1337,7 +1337,7 @@ int q4k_f16_gemm_grouped(const void* w16, const void* x16, float* y, const int32
     if (k % 64 != 0) {
         return Q4K_ERR_UNSUPPORTED;      // the k step of the tile
     }
-    if (!fits_launch(q4k::f16_grouped_grid(rows, groups, n), 512)) {
+    if (!fits_launch(q4k::f16_grouped_grid(rows, groups, n, k), 512)) {
         return Q4K_ERR_SHAPE;
     }
     if (!aligned16(w16) || !aligned16(x16) || !aligned16(y)) {

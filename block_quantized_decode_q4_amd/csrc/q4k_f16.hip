@@ -227,23 +227,27 @@ f16_gemm_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x
 // per product, which is what bounds the 128 x 128 tile above (4096 rows in
 // eight groups, n 14336, k 4096: 757 us with it, 619 us with 128 x 256 on
 // eight waves, 780 TFLOP/s; 256 x 256 617 us, but 20-70 % slower where the
-// groups are shorter).  LDS rows of 64 halves without padding, the 16-byte piece c of row r at place
-// c ^ (r % 8): neither the stores of eight threads' 128 bytes nor the reads of
-// a 16 x 32 operand collide.  One register set: a step has twice the products
-// to hide a load behind.
-template <int BM, int BN, int WM, int WN, typename XRow, typename Put>
+// groups are shorter).  A step takes GK of k (64; 256 where the tiles are few, see
+// the rule below).  LDS rows of GK halves without padding, the 16-byte piece c of
+// row r at place c ^ r in its low three bits (four from 16 pieces on): neither the
+// stores of a row's consecutive bytes nor the reads of a 16 x 32 operand collide.
+// One register set: a step has twice the products to hide a load behind.
+template <int BM, int BN, int GK, int WM, int WN, typename XRow, typename Put>
 __device__ __forceinline__ void
 f16_wide_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, int n, int k,
               unsigned char* smem)
 {
     constexpr int kThreads = 64 * WM * WN;
-    constexpr int kRows = kThreads / 8;      // tile rows per load of all threads
+    constexpr int kPieces = GK / 8;          // 16-byte pieces of a tile row
+    constexpr int kSpread = kPieces < 16 ? 7 : 15;        // the pieces' bits that rows permute
+    constexpr int kRows = kThreads / kPieces;             // tile rows per load of all threads
     constexpr int LA = BM / kRows;           // 16-byte loads of the x tile per thread and step
     constexpr int LB = BN / kRows;
     constexpr int FA = BM / WM / 16;         // 16-row MFMA blocks per wave
     constexpr int FB = BN / WN / 16;
-    constexpr int kXs = BM * kGK * 2;        // LDS bytes of one x tile
-    constexpr int kStage = (BM + BN) * kGK * 2;
+    constexpr int kXs = BM * GK * 2;         // LDS bytes of one x tile
+    constexpr int kStage = (BM + BN) * GK * 2;
+    static_assert(kRows % (kSpread + 1) == 0, "a thread's rows share their permutation");
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = tid >> 6;
@@ -254,36 +258,37 @@ f16_wide_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, 
     // load role: 16 bytes of a tile row per thread and load
     const _Float16* xsrc[LA];
     const _Float16* wsrc[LB];
-    const int lrow = tid >> 3;
-    const int loff = lrow * 128 + (((tid & 7) ^ (lrow & 7)) << 4);       // kRows % 8 == 0
+    const int lrow = tid / kPieces;
+    const int lpiece = tid % kPieces;
+    const int loff = lrow * (2 * GK) + ((lpiece ^ (lrow & kSpread)) << 4);
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-        xsrc[i] = xrow(lrow + kRows * i) + (tid & 7) * 8;
+        xsrc[i] = xrow(lrow + kRows * i) + lpiece * 8;
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-        wsrc[i] = w16 + (int64_t)min(row_w0 + lrow + kRows * i, n - 1) * k + (tid & 7) * 8;
+        wsrc[i] = w16 + (int64_t)min(row_w0 + lrow + kRows * i, n - 1) * k + lpiece * 8;
     }
     v4u_t xa[LA], wa[LB];
     auto load = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
-            xa[i] = *reinterpret_cast<const v4u_t*>(xsrc[i] + kb * kGK);
+            xa[i] = *reinterpret_cast<const v4u_t*>(xsrc[i] + kb * GK);
         }
 #pragma unroll
         for (int i = 0; i < LB; ++i) {
-            wa[i] = *reinterpret_cast<const v4u_t*>(wsrc[i] + kb * kGK);
+            wa[i] = *reinterpret_cast<const v4u_t*>(wsrc[i] + kb * GK);
         }
     };
     auto stage = [&](int st) __attribute__((always_inline)) {
         unsigned char* base = smem + st * kStage + loff;
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
-            *reinterpret_cast<v4u_t*>(base + i * (kRows * 128)) = xa[i];
+            *reinterpret_cast<v4u_t*>(base + i * (kRows * 2 * GK)) = xa[i];
         }
 #pragma unroll
         for (int i = 0; i < LB; ++i) {
-            *reinterpret_cast<v4u_t*>(base + kXs + i * (kRows * 128)) = wa[i];
+            *reinterpret_cast<v4u_t*>(base + kXs + i * (kRows * 2 * GK)) = wa[i];
         }
     };
     f32x4_t acc[FA][FB];
@@ -294,25 +299,25 @@ f16_wide_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, 
             acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
     }
-    const int KB = k / kGK;
+    const int KB = k / GK;
     load(0);
     stage(0);
     load(min(1, KB - 1));
     __syncthreads();
     for (int kb = 0; kb < KB; ++kb) {
-        const unsigned char* xs = smem + (kb & 1) * kStage + (BM / WM) * wm * 128 + j * 128;
-        const unsigned char* ws = smem + (kb & 1) * kStage + kXs + (BN / WN) * wn * 128 + j * 128;
+        const unsigned char* xs = smem + (kb & 1) * kStage + ((BM / WM) * wm + j) * (2 * GK);
+        const unsigned char* ws = smem + (kb & 1) * kStage + kXs + ((BN / WN) * wn + j) * (2 * GK);
 #pragma unroll
-        for (int s = 0; s < kGK / 32; ++s) {
-            const int c = ((4 * s + g) ^ (j & 7)) << 4;
+        for (int s = 0; s < GK / 32; ++s) {
+            const int c = ((4 * s + g) ^ (j & kSpread)) << 4;
             half8_t av[FA], bv[FB];
 #pragma unroll
             for (int a = 0; a < FA; ++a) {
-                av[a] = *reinterpret_cast<const half8_t*>(xs + a * 2048 + c);
+                av[a] = *reinterpret_cast<const half8_t*>(xs + a * (32 * GK) + c);
             }
 #pragma unroll
             for (int b = 0; b < FB; ++b) {
-                bv[b] = *reinterpret_cast<const half8_t*>(ws + b * 2048 + c);
+                bv[b] = *reinterpret_cast<const half8_t*>(ws + b * (32 * GK) + c);
             }
 #pragma unroll
             for (int a = 0; a < FA; ++a) {
@@ -325,30 +330,32 @@ f16_wide_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, 
         }
         stage((kb + 1) & 1);
         load(min(kb + 2, KB - 1));
-        // the order of a step's instructions (masks: 0x8 matrix, 0x100 LDS
-        // read, 0x200 LDS write, 0x20 load): operand reads run ahead of the
-        // products that take them, then a store or a load after each product
-        // (128 x 256: 639 -> 619 us on the shape below)
-        constexpr int kReads = 2 * (FA + FB);
-        constexpr int kAhead = FB + 3;
-        constexpr int kMfma = 2 * FA * FB;
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+        if constexpr (GK == kGK) {
+            // the order of a step's instructions (masks: 0x8 matrix, 0x100 LDS
+            // read, 0x200 LDS write, 0x20 load): operand reads run ahead of the
+            // products that take them, then a store or a load after each product
+            // (128 x 256: 639 -> 619 us on the shape below)
+            constexpr int kReads = 2 * (FA + FB);
+            constexpr int kAhead = FB + 3;
+            constexpr int kMfma = 2 * FA * FB;
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
 #pragma unroll
-        for (int i = 0; i < kReads - kAhead; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
+            for (int i = 0; i < kReads - kAhead; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
 #pragma unroll
-        for (int i = 0; i < LA + LB; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
-        }
+            for (int i = 0; i < LA + LB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+            }
 #pragma unroll
-        for (int i = 0; i < LA + LB; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+            for (int i = 0; i < LA + LB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x8, kMfma, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x8, kMfma, 0);
         __syncthreads();
     }
     // D[4 g + r][j] of block (a, b)
@@ -373,7 +380,7 @@ f16_wide_tile(const _Float16* __restrict__ w16, XRow xrow, Put put, int row_w0, 
 // The same product for rows grouped by matrix: a tile holds up to BM positions
 // of one group, its mirror is the group's; NT column blocks of BN.  Positions
 // that are left out read x row 0 and are not written.
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int GK, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN, WM * WN / 4)
 f16_gemm_grouped_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict__ x16,
                         float* __restrict__ y, GroupRows rows, int n, int k, int NT)
@@ -406,7 +413,7 @@ f16_gemm_grouped_kernel(const _Float16* __restrict__ w16, const _Float16* __rest
         }
     };
     const _Float16* const w = w16 + (int64_t)t.group * n * k;
-    f16_wide_tile<BM, BN, WM, WN>(w, xrow, put, work.block * BN, n, k, smem);
+    f16_wide_tile<BM, BN, GK, WM, WN>(w, xrow, put, work.block * BN, n, k, smem);
 }
 
 hipError_t launch_f16_cvt(const float* x, void* out, int64_t count, hipStream_t stream)
@@ -485,40 +492,56 @@ hipError_t launch_f16_gemm(const void* w16, const void* x16, float* y, int m, in
 // is shorter.  256 / 192 columns, uneven groups: 19 tiles of n = k = 4096 138 / 114
 // us, 25 tiles of n 4096, k 2048 85 / 91 us, 95 tiles of n 1001, k 2048 94 / 102 us, 37
 // tiles of n 14336, k 4096 633 / 594 us, 36 tiles 593 / 598 us.
+// Where even 64 columns leave CUs without work, a step's latency is what counts:
+// 256 of k a step instead of 64, and 32 or 64 rows by 64 columns (68 rows in five
+// groups, n 398, k 7168: 64 x 128 / 32 x 64 / 64 x 64 47 / 26 / 33 us; 910 rows in 23,
+// n 534, k 8192: 87 / 70 / 54 us; more tiles than CUs, 400 rows in eight groups, n = k
+// = 2048: 29 / 35 / 33 us).
 constexpr int64_t kCus = 256;
+constexpr int kDeepGK = 256;
 
 struct F16GroupedTile {
-    int rows, columns;
+    int rows, columns, depth;
 };
 
-static F16GroupedTile f16_grouped_tile(int64_t rows, int64_t groups, int64_t n)
+static F16GroupedTile f16_grouped_tile(int64_t rows, int64_t groups, int64_t n, int64_t k)
 {
-    if (rows < 96 * groups || most_tiles(rows, groups, 128) * ((n + 255) / 256) < 128) {
-        return {64, 128};
+    // twice the tiles to expect: a group of any length ends half a tile early
+    const int64_t ends = groups < rows ? groups : rows;
+    auto halves = [&](int64_t tile) { return 2 * rows / tile + ends; };
+    const int64_t columns64 = (n + 63) / 64;
+    if (k % kDeepGK == 0 && halves(32) * columns64 <= 2 * kCus) {
+        return {32, 64, kDeepGK};
     }
-    const int64_t halves = rows / 64 + groups;         // twice the tiles to expect
-    const int64_t wide = halves * ((n + 255) / 256), narrow = halves * ((n + 191) / 192);
+    if (k % kDeepGK == 0 && halves(64) * columns64 <= 2 * kCus) {
+        return {64, 64, kDeepGK};
+    }
+    if (rows < 96 * groups || most_tiles(rows, groups, 128) * ((n + 255) / 256) < 128) {
+        return {64, 128, kGK};
+    }
+    const int64_t wide = halves(128) * ((n + 255) / 256);
+    const int64_t narrow = halves(128) * ((n + 191) / 192);
     auto rounds = [](int64_t half_tiles) { return (half_tiles + 2 * kCus - 1) / (2 * kCus); };
     if (rounds(narrow) > 4 || rounds(narrow) * 192 < rounds(wide) * 256) {
-        return {128, 192};
+        return {128, 192, kGK};
     }
-    return {128, 256};
+    return {128, 256, kGK};
 }
 
-int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n)
+int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k)
 {
-    const F16GroupedTile t = f16_grouped_tile(rows, groups, n);
+    const F16GroupedTile t = f16_grouped_tile(rows, groups, n, k);
     return (most_tiles(rows, groups, t.rows) * ((n + t.columns - 1) / t.columns) + 7) / 8 * 8;
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int GK, int WM, int WN>
 static hipError_t launch_f16_grouped_t(const void* w16, const void* x16, float* y,
                                        const GroupRows& g, int n, int k, hipStream_t stream)
 {
     const int NT = (n + BN - 1) / BN;
-    const int64_t grid = f16_grouped_grid(g.rows, g.groups, n);
-    hipLaunchKernelGGL((f16_gemm_grouped_kernel<BM, BN, WM, WN>), dim3((unsigned)grid),
-                       dim3(64 * WM * WN), 2 * (BM + BN) * kGK * 2, stream,
+    const int64_t grid = f16_grouped_grid(g.rows, g.groups, n, k);
+    hipLaunchKernelGGL((f16_gemm_grouped_kernel<BM, BN, GK, WM, WN>), dim3((unsigned)grid),
+                       dim3(64 * WM * WN), 2 * (BM + BN) * GK * 2, stream,
                        static_cast<const _Float16*>(w16), static_cast<const _Float16*>(x16), y, g,
                        n, k, NT);
     return hipGetLastError();
@@ -527,14 +550,20 @@ static hipError_t launch_f16_grouped_t(const void* w16, const void* x16, float* 
 hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
                                    int n, int k, hipStream_t stream)
 {
-    const F16GroupedTile t = f16_grouped_tile(g.rows, g.groups, n);
+    const F16GroupedTile t = f16_grouped_tile(g.rows, g.groups, n, k);
     if (t.columns == 256) {
-        return launch_f16_grouped_t<128, 256, 2, 4>(w16, x16, y, g, n, k, stream);
+        return launch_f16_grouped_t<128, 256, kGK, 2, 4>(w16, x16, y, g, n, k, stream);
     }
     if (t.columns == 192) {
-        return launch_f16_grouped_t<128, 192, 2, 4>(w16, x16, y, g, n, k, stream);
+        return launch_f16_grouped_t<128, 192, kGK, 2, 4>(w16, x16, y, g, n, k, stream);
     }
-    return launch_f16_grouped_t<64, 128, 2, 4>(w16, x16, y, g, n, k, stream);
+    if (t.columns == 128) {
+        return launch_f16_grouped_t<64, 128, kGK, 2, 4>(w16, x16, y, g, n, k, stream);
+    }
+    if (t.rows == 64) {
+        return launch_f16_grouped_t<64, 64, kDeepGK, 2, 4>(w16, x16, y, g, n, k, stream);
+    }
+    return launch_f16_grouped_t<32, 64, kDeepGK, 2, 4>(w16, x16, y, g, n, k, stream);
 }
 
 // ------------------------------------------------- allocation-free variant

@@ -184,7 +184,7 @@ constexpr int64_t kMaxGroupedK = (int64_t)1 << 24;   // 16 rows within 32-bit of
 // The fp16 mirror (q4k_f16.hip).
 hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
                                    int n, int k, hipStream_t stream);
-int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n);
+int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k);
 
 // Low-rank adapters (q4k_lora.hip).
 struct LoraArgs {

@@ -165,6 +165,22 @@ def test_grouped_sizes(kind, sizes, n, k):
     _check(kind, W, x, off, np.arange(rows), np.arange(rows), y0, got, n, k)
 
 
+@pytest.mark.parametrize("sizes,n,k", [
+    ([5, 0, 70], 130, 64), ([33, 64, 65, 1], 300, 320), ([400], 200, 256), ([1024], 520, 512),
+    ([31, 0, 33], 65, 2048), ([64, 129, 2], 1100, 768)])
+def test_grouped_f16_steps_of_k(sizes, n, k):
+    """Long and short steps along k, tiles of 32 and 64 rows, ragged ends."""
+    rng = np.random.default_rng(n + k)
+    groups, rows = len(sizes), sum(sizes)
+    W = Mirror(rng, groups, n, k)
+    x = _make_x(rng, "f16", rows, k)
+    off = _offsets(sizes)
+    y0 = np.full((rows, n), 123.25, np.float32)
+    print("grouped f16 steps sizes=%s n=%d k=%d" % (sizes, n, k), flush=True)
+    got = _gpu("f16", W.bytes, x, y0, off, n, k, groups, rows)
+    _check("f16", W, x, off, np.arange(rows), np.arange(rows), y0, got, n, k)
+
+
 def test_grouped_f16_wide_tiles():
     """Shapes that take the 128-row tiles (groups of about a tile or more and
     enough of them), ragged in rows and columns; of 256 columns (the third) and of
