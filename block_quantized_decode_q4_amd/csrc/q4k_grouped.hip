@@ -32,11 +32,13 @@
 // all waves of a workgroup, superblock by superblock with a barrier each, was
 // slower (one token 27 us, 48 tokens on eight wide experts 124 us).
 //
-// What bounds it: about 150 vector instructions a superblock and row tile
-// beside 17 matrix ones, three waves a SIMD, and the weights' bytes.  One
-// token, two of eight experts 14336 x 4096 (66 MB): 22 us with the x launch;
-// 264 MB (eight experts 4096 x 14336, 16 positions each) 83 us, 3.2 TB/s; 48
-// tokens of uneven experts (ten tiles where six experts are met) 110 us.
+// What bounds it: about 125 vector instructions a superblock and row tile
+// beside 17 matrix ones, and the weights' bytes.  One token, two of eight experts
+// 14336 x 4096 (66 MB): 21 us with the x launch; 264 MB (eight experts 4096 x
+// 14336, 16 positions each) 78 us, 3.4 TB/s; 48 tokens of uneven experts (ten
+// tiles where six experts are met) 99 us.  Measured without gain at 264 MB: two
+// row tiles worked on at once, four row tiles of weights in flight instead of two,
+// x of the next superblock asked for ahead (79 us each, and fewer waves a SIMD).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
