@@ -197,7 +197,7 @@ struct LoraArgs {
     const float* scales;               // null: 1
     const int* offsets;
     const int* order;                  // null: position i is row i
-    float* v;                          // rows x r (workspace)
+    float* v;                          // parts of k x rows x r up to 16s (workspace)
     int x_type, n, k, r, adapters, rows;
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
