@@ -93,20 +93,6 @@ __device__ __forceinline__ GroupSpan find_span(const int* offsets, int groups, i
     return r;
 }
 
-// Tile t itself; count = 0: it does not exist.
-template <int ROWS>
-__device__ __forceinline__ GroupTile find_tile(const int* offsets, int groups, int rows, int t)
-{
-    const GroupSpan s = find_span<ROWS>(offsets, groups, rows, t);
-    GroupTile r = {0, 0, 0};
-    if (s.tiles > 0) {
-        r.group = s.group;
-        r.begin = s.begin + (t - s.first) * ROWS;
-        r.count = min(ROWS, s.end - r.begin);
-    }
-    return r;
-}
-
 // The tile that holds position p (the first group's that has it); count = 0:
 // it is in no group.
 template <int ROWS>

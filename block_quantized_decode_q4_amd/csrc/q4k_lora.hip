@@ -27,11 +27,13 @@
 // lanes 16 apart) would take 64 clocks of the vector cache per load where
 // neighbouring lanes on neighbouring bytes take about 20, and that bound both
 // kernels.  2048 rows at rank 64, n = k = 4096, x binary16 (84 MB): down
-// 20 -> 9 us, up 27 -> 18 us; 24 rows of 16 adapters at rank 16: down 5.1 us,
-// up 4.8 us.  What bounds them now is the chain of loads that each workgroup
-// waits for (offsets, order, operands), about 1 us a link, so whatever can be
-// asked for before a wait is: two steps of operands, and up v, B and the base
-// together (base behind the products: 21 us).
+// 20 -> 7.4 us, up 27 -> 13.3 us; 24 rows of 16 adapters at rank 16: down 5.2 us,
+// up 4.0 us.  An adapter's tiles go to one XCD, whose L2 then reads A and B once
+// (over all XCDs: 2048 rows 30.9 us a call instead of 22.8, 8192 rows 98 instead of
+// 64).  What bounds them now is the chain of loads that each workgroup waits for
+// (offsets, order, operands), about 1 us a link, so whatever can be asked for
+// before a wait is: two steps of operands, and up v, B and the base together (base
+// behind the products: 3 us more).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -66,6 +68,15 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int adapter)
 __device__ __forceinline__ int order_at(const LoraArgs& a, int p)
 {
     return (a.order ? a.order : a.offsets)[a.order ? p : 0];
+}
+
+// This workgroup's tile.  gridDim.x is a multiple of eight, so XCD x takes the x-th
+// eighth of the tiles: an adapter's meet in one L2.
+template <int ROWS>
+__device__ __forceinline__ GroupTile adapter_tile(const LoraArgs& a)
+{
+    const GroupTiles tiles = count_tiles<ROWS>(a.offsets, a.adapters, a.rows, (int)gridDim.x);
+    return find_work<ROWS>(tiles, a.offsets, a.adapters, a.rows, 1, (int)blockIdx.x).tile;
 }
 
 // The place of 16-byte piece p of row r in LDS rows of 128 bytes (eight
@@ -241,7 +252,7 @@ lora_down_kernel(LoraArgs a)
     const int wave = threadIdx.x >> 6;
     const int j = lane & 15;
     const int g = lane >> 4;
-    const GroupTile t = find_tile<kTile>(a.offsets, a.adapters, a.rows, blockIdx.x);
+    const GroupTile t = adapter_tile<kTile>(a);
     if (t.count == 0) {
         return;
     }
@@ -325,7 +336,7 @@ lora_up_kernel(LoraArgs a)
     const int j = lane & 15;
     const int g = lane >> 4;
     const int col0 = (int)blockIdx.y * kUpCols;
-    const GroupTile t = find_tile<kUpTile>(a.offsets, a.adapters, a.rows, blockIdx.x);
+    const GroupTile t = adapter_tile<kUpTile>(a);
     if (t.count == 0) {
         return;
     }
@@ -572,11 +583,11 @@ void launch_up(const LoraArgs& a, dim3 up, hipStream_t stream)
 
 // Parts of k: enough workgroups for the chip.  (Sums of v are the caller's
 // workspace, so by the rows alone.)  Both products with 1 / 2 / 4 parts, rank 64,
-// n = k = 4096: 512 rows 17.7 / 15.4 / 14.5 us, 2048 rows 31.4 / 30.9 / 34.5 us,
-// 8192 rows 87 / 96 / 111 us.
+// n = k = 4096: 512 rows 16.5 / 13.7 / 12.2 us, 2048 rows 25.2 / 22.8 / 24.5 us,
+// 4096 rows 36.9 / 38.8 / 41.4 us.
 int down_parts(int64_t rows)
 {
-    return rows <= 512 ? 4 : rows <= 4096 ? 2 : 1;
+    return rows <= 512 ? 4 : rows < 4096 ? 2 : 1;
 }
 
 }  // namespace
@@ -589,18 +600,19 @@ size_t lora_ws_bytes(int64_t rows, int64_t r)
 // The grids: fewer than 2^32 threads, 65535 workgroups along y
 bool lora_fits(int64_t rows, int64_t adapters, int64_t n, int64_t r)
 {
-    const int64_t down = most_tiles(rows, adapters, kTile) *
+    const int64_t down = (most_tiles(rows, adapters, kTile) + 7) *
                          ((r + 16 * kRanks - 1) / (16 * kRanks)) * down_parts(rows);
     const int64_t up = (n + kUpCols - 1) / kUpCols;
     const int64_t most = (int64_t)1 << 32;
     return down * 64 * kDownWaves < most && up <= 65535 &&
-           most_tiles(rows, adapters, kUpTile) * up * 256 < most;
+           (most_tiles(rows, adapters, kUpTile) + 7) * up * 256 < most;
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream)
 {
     const int parts = down_parts(a.rows);
-    const dim3 down((unsigned)most_tiles(a.rows, a.adapters, kTile),
+    auto eights = [](int64_t tiles) { return (unsigned)((tiles + 7) / 8 * 8); };
+    const dim3 down(eights(most_tiles(a.rows, a.adapters, kTile)),
                     (unsigned)((a.r + 16 * kRanks - 1) / (16 * kRanks)), (unsigned)parts);
     const dim3 threads(64 * kDownWaves);
     if (a.x_type == kTypeF16) {
@@ -614,7 +626,7 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t stream)
     if (e != hipSuccess) {
         return e;
     }
-    const dim3 up((unsigned)most_tiles(a.rows, a.adapters, kUpTile),
+    const dim3 up(eights(most_tiles(a.rows, a.adapters, kUpTile)),
                   (unsigned)((a.n + kUpCols - 1) / kUpCols));
     switch (parts) {
     case 1: launch_up<1>(a, up, stream); break;
