@@ -18,7 +18,8 @@
 //
 // Two launches: grouped_x_kernel lays each position's x out once in the
 // caller's workspace (hi, lo and S in the order in which the lanes of the
-// product kernel read them); grouped_kernel multiplies.
+// product kernel read them); grouped_kernel multiplies.  A few rows (the tokens of
+// one decode step) take one: the products' waves lay x out themselves.
 //
 // grouped_kernel: a wave computes 16 weight rows x 16 positions of one group
 // (v_mfma_f32_16x16x32_f16, x as the rows, weights as the columns).  Lane
@@ -34,7 +35,7 @@
 //
 // What bounds it: about 125 vector instructions a superblock and row tile
 // beside 17 matrix ones, and the weights' bytes.  One token, two of eight experts
-// 14336 x 4096 (66 MB): 21 us with the x launch; 264 MB (eight experts 4096 x
+// 14336 x 4096 (66 MB): 20 us; 264 MB (eight experts 4096 x
 // 14336, 16 positions each) 78 us, 3.4 TB/s; 48 tokens of uneven experts (ten
 // tiles where six experts are met) 99 us.  Measured without gain at 264 MB: two
 // row tiles worked on at once, four row tiles of weights in flight instead of two,
@@ -129,6 +130,22 @@ __device__ __forceinline__ float piece_top(const float4& lo, const float4& hi, f
     return top;
 }
 
+// v of the lane that DPP control CTRL pairs with this one
+template <int CTRL>
+__device__ __forceinline__ float paired(float v)
+{
+    return __builtin_bit_cast(float, dpp_i<CTRL>(__builtin_bit_cast(int, v)));
+}
+
+// The largest of a row of 16 lanes (rotations by 8, 4, 2, 1), in all of them
+__device__ __forceinline__ float row_top(float v)
+{
+    v = fmaxf(v, paired<0x128>(v));
+    v = fmaxf(v, paired<0x124>(v));
+    v = fmaxf(v, paired<0x122>(v));
+    return fmaxf(v, paired<0x121>(v));
+}
+
 // The power of two that brings top into [2^14, 2^15): 15 - e for top in
 // [2^(e-1), 2^e), 0 where there is none (a zero, an infinity)
 __device__ __forceinline__ int scale_of(float top)
@@ -159,11 +176,13 @@ __device__ __forceinline__ void convert(const float4& lo4, const float4& hi4, in
     }
     float s0 = (t[0] + t[1]) + (t[2] + t[3]);
     float s1 = (t[4] + t[5]) + (t[6] + t[7]);
-#pragma unroll
-    for (int off = 1; off < 8; off <<= 1) {
-        s0 += __shfl_xor(s0, off, 64);
-        s1 += __shfl_xor(s1, off, 64);
-    }
+    // pairs and fours within a quad, then the mirrored lane of the eight
+    s0 += paired<0xB1>(s0);
+    s1 += paired<0xB1>(s1);
+    s0 += paired<0x4E>(s0);
+    s1 += paired<0x4E>(s1);
+    s0 += paired<0x141>(s0);
+    s1 += paired<0x141>(s1);
     _Float16 a0, b0, a1, b1;
     split(s0 * 0.015625f, a0, b0);
     split(s1 * 0.015625f, a1, b1);
@@ -220,10 +239,9 @@ grouped_x_kernel(GroupedArgs a)
         load_x<Q8>(a, row, v, lo, hi);
         top = piece_top(lo, hi, top);
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        top = fmaxf(top, __shfl_xor(top, off, 64));
-    }
+    top = row_top(top);
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
     if ((tid & 63) == 0) {
         part[tid >> 6] = top;
     }
@@ -349,11 +367,23 @@ constexpr int kWaves = 4;
 template <int T>
 constexpr int kWaveLds = T * 1024 > kWStage ? T * 1024 : kWStage;   // weights, then sums
 
+// Few positions in all (kFused<T> at most): no launch for x.  A wave lays out the x of
+// its superblock itself, in LDS: 32 lanes a position, eight elements a lane, scaled
+// by the superblock's largest |x|.  The sums are kept in the scale of the largest
+// so far (2^-E of a position; E falls, and the sums with it, when a larger one
+// comes), and the parts of k are joined in the smallest E.
+enum FusedX { kXLaidOut, kXF32, kXQ8 };
 template <int T>
+constexpr int kFused = T == 2 ? 16 : 8;            // so that two workgroups fit a CU's LDS
+constexpr int kNoScale = 1000;         // nothing but zeros so far
+template <int T, int FUSED>
+constexpr int kXLds = FUSED == kXLaidOut ? 0 : kFused<T> * kXsb;    // per wave
+
+template <int T, int FUSED>
 __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupTiles& tiles,
                                               int row_blocks, int kw_log2, unsigned char* smem)
 {
-    constexpr int kLds = kWaveLds<T>;
+    constexpr int kLds = kWaveLds<T> + kXLds<T, FUSED>;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     // wave-uniform, as are all addresses but the lanes' 32-bit offsets below
@@ -401,9 +431,7 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
     const uint32_t xoff = (uint32_t)((g * t.count + slot) * 16);
     u4_t xh[8], xl[8];
     uint2 xs;
-    auto load_x = [&](int slab) __attribute__((always_inline)) {
-        const char* const at =
-            xrows + (int64_t)min(slab * kw + wk, S - 1) * t.count * kXsb;
+    auto take_x = [&](const char* at) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             xh[u] = *reinterpret_cast<const u4_t*>(at + u * t.count * 64 + xoff);
@@ -411,6 +439,19 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
         }
         xs = *reinterpret_cast<const uint2*>(at + t.count * 1024 + xoff / 2);
     };
+    // fused: this lane's position is 2 pass + lane / 32; lane p < count also keeps
+    // what is known of position p
+    unsigned char* const xbuf = wbuf + kWaveLds<T>;
+    const int lane_row =
+        FUSED ? max(x_row_of(a.g, t.begin + min(lane & (kFused<T> - 1), t.count - 1)), 0) : 0;
+    int scale = kNoScale;                      // E
+    float4 raw[2];
+    auto fetch_x = [&](int slab, int pass) __attribute__((always_inline)) {
+        const int64_t row = __shfl(lane_row, min(2 * pass + (lane >> 5), t.count - 1), 64);
+        ::q4k::load_x<FUSED == kXQ8>(a, row, min(slab * kw + wk, S - 1) * 32 + (lane & 31), raw[0],
+                                     raw[1]);
+    };
+    float factor[4] = {1.f, 1.f, 1.f, 1.f};    // of positions 4 g + e in this superblock
     const uint32_t shift = 16 * (g >> 1);
     const uint32_t odd = g & 1 ? 0xFFFFFFFFu : 0u;
     const f4_t zero = {0.f, 0.f, 0.f, 0.f};
@@ -421,9 +462,61 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
     }
     load_w(0, 0, std::integral_constant<int, 0>());
     load_w(0, 1, std::integral_constant<int, 1>());
+    if constexpr (FUSED != kXLaidOut) {
+        fetch_x(0, 0);
+    }
     for (int slab = 0; slab < slabs; ++slab) {
-        load_x(slab);
         const bool in = slab * kw + wk < S;
+        if constexpr (FUSED == kXLaidOut) {
+            take_x(xrows + (int64_t)min(slab * kw + wk, S - 1) * t.count * kXsb);
+        } else if (in) {
+            int now = kNoScale;
+            wave_lds_order();
+            for (int pass = 0; 2 * pass < t.count; ++pass) {
+                if (pass > 0) {
+                    fetch_x(slab, pass);
+                }
+                float top = row_top(piece_top(raw[0], raw[1], 0.f));
+                top = fmaxf(top, __shfl_xor(top, 16, 64));
+                const int p = 2 * pass + (lane >> 5);
+                const int sc = scale_of(top);
+                h8_t h, l;
+                h4_t sums;
+                convert(raw[0], raw[1], sc, h, l, sums);
+                if (p < t.count) {
+                    const PieceAt at = piece_at(lane & 31);
+                    const int c = 4 * at.u + at.g;
+                    *reinterpret_cast<h8_t*>(xbuf + (c * t.count + p) * 16) = h;
+                    *reinterpret_cast<h8_t*>(xbuf + ((32 + c) * t.count + p) * 16) = l;
+                    if ((lane & 7) == 0) {
+                        *reinterpret_cast<h4_t*>(xbuf + t.count * 1024 +
+                                                 (at.sg * t.count + p) * 8) = sums;
+                    }
+                }
+                const int of = __shfl(top > 0.f ? sc : kNoScale, (lane & 1) * 32, 64);
+                now = lane >> 1 == pass ? of : now;
+            }
+            wave_lds_order();
+            const int next = min(scale, now);
+            if (__any(next < scale)) {                 // the sums so far, in the new scale
+                const int down = scale == kNoScale ? 0 : next - scale;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = __shfl(down, 4 * g + e, 64);
+#pragma unroll
+                    for (int i = 0; i < T; ++i) {
+                        total[i][e] = ldexpf(total[i][e], d);
+                    }
+                }
+                scale = next;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                factor[e] = ldexpf(1.f, __shfl(scale - now, 4 * g + e, 64));
+            }
+            take_x(reinterpret_cast<const char*>(xbuf));
+            fetch_x(min(slab + 1, slabs - 1), 0);
+        }
         auto tile = [&](int i, auto set) __attribute__((always_inline)) {
             // through the wave's own LDS
             wave_lds_order();
@@ -462,8 +555,13 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float v = __builtin_fmaf(al[e], 1.0f / 2048.0f, ah[e]);
-                total[i][e] = __builtin_fmaf(dh, v, total[i][e]);
-                total[i][e] = __builtin_fmaf(-dm, am[e], total[i][e]);
+                if constexpr (FUSED == kXLaidOut) {
+                    total[i][e] = __builtin_fmaf(dh, v, total[i][e]);
+                    total[i][e] = __builtin_fmaf(-dm, am[e], total[i][e]);
+                } else {
+                    const float both = __builtin_fmaf(-dm, am[e], dh * v);
+                    total[i][e] = __builtin_fmaf(factor[e], both, total[i][e]);
+                }
             }
         };
         static_assert(T % 2 == 0, "two sets in turn");
@@ -486,23 +584,48 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
         yr = a.g.y_rows ? a.g.y_rows[p] : p;
         yr = yr < a.g.y_count ? yr : -1;
     }
-    const int exps = ws.exps[p];
+    int exps = 0;
+    if constexpr (FUSED == kXLaidOut) {
+        exps = ws.exps[p];
+    } else if (lane < 16) {
+        reinterpret_cast<int*>(xbuf)[lane] = scale;
+    }
     __syncthreads();
     for (int q = wave; q < (kWaves >> kw_log2) * T; q += kWaves) {
         const int rg = q / T;
         const int i = q % T;
-        const unsigned char* const from = smem + (rg << kw_log2) * kLds + (i * 64 + lane) * 16;
-        f4_t sum = *reinterpret_cast<const f4_t*>(from);
-        for (int z = 1; z < kw; ++z) {
-            sum += *reinterpret_cast<const f4_t*>(from + z * kLds);
+        const unsigned char* const first = smem + (rg << kw_log2) * kLds;
+        const unsigned char* const from = first + (i * 64 + lane) * 16;
+        f4_t sum = zero;
+        int4 least = make_int4(kNoScale, kNoScale, kNoScale, kNoScale);
+        if constexpr (FUSED != kXLaidOut) {
+            for (int z = 0; z < kw; ++z) {
+                const int4 of =
+                    reinterpret_cast<const int4*>(first + z * kLds + kWaveLds<T>)[g];
+                least.x = min(least.x, of.x);
+                least.y = min(least.y, of.y);
+                least.z = min(least.z, of.z);
+                least.w = min(least.w, of.w);
+            }
         }
+        for (int z = 0; z < kw; ++z) {
+            f4_t one = *reinterpret_cast<const f4_t*>(from + z * kLds);
+            if constexpr (FUSED != kXLaidOut) {
+                const int4 of =
+                    reinterpret_cast<const int4*>(first + z * kLds + kWaveLds<T>)[g];
+                one = f4_t{ldexpf(one[0], least.x - of.x), ldexpf(one[1], least.y - of.y),
+                           ldexpf(one[2], least.z - of.z), ldexpf(one[3], least.w - of.w)};
+            }
+            sum = z == 0 ? one : sum + one;
+        }
+        const int scales[4] = {least.x, least.y, least.z, least.w};
         const int row =
             min((work.block * (kWaves >> kw_log2) + rg) * rows_per_group + 16 * i, last) + j;
         // D[4 g + e][j]: position 4 g + e, weight row j
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int yrow = __shfl(yr, 4 * g + e, 64);
-            const int exp = __shfl(exps, 4 * g + e, 64);
+            const int exp = FUSED == kXLaidOut ? __shfl(exps, 4 * g + e, 64) : scales[e];
             if (row < a.n && yrow >= 0) {
                 a.y[(int64_t)yrow * a.n + row] = ldexpf(sum[e], -exp);
             }
@@ -512,14 +635,14 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
 
 constexpr int kCus = 256;
 
-template <int T>
-__global__ void __launch_bounds__(64 * kWaves, 3)
+template <int T, int FUSED>
+__global__ void __launch_bounds__(64 * kWaves, FUSED == kXLaidOut ? 3 : 2)
 grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
 {
-    __shared__ __align__(16) unsigned char smem[kWaves * kWaveLds<T>];
+    __shared__ __align__(16) unsigned char smem[kWaves * (kWaveLds<T> + kXLds<T, FUSED>)];
     const GroupTiles t =
         count_tiles<kTile>(a.g.offsets, a.g.groups, a.g.rows, (int)gridDim.x / row_blocks);
-    grouped_tiles<T>(a, t, row_blocks, kw_log2, smem);
+    grouped_tiles<T, FUSED>(a, t, row_blocks, kw_log2, smem);
 }
 
 // T = 8 or, in fine_blocks, T = 4, by the number of tiles, which the host does not
@@ -536,9 +659,9 @@ grouped_either_kernel(GroupedArgs a, int row_blocks, int fine_blocks, int kw_log
     const int coarse = (t.tiles * row_blocks + kCus - 1) / kCus;
     const int fine = (t.tiles * fine_blocks + kCus - 1) / kCus;
     if (coarse * 2 * 8 <= fine * 9) {
-        grouped_tiles<8>(a, t, row_blocks, kw_log2, smem);
+        grouped_tiles<8, kXLaidOut>(a, t, row_blocks, kw_log2, smem);
     } else {
-        grouped_tiles<4>(a, t, fine_blocks, kw_log2, smem);
+        grouped_tiles<4, kXLaidOut>(a, t, fine_blocks, kw_log2, smem);
     }
 }
 
@@ -553,8 +676,15 @@ grouped_either_kernel(GroupedArgs a, int row_blocks, int fine_blocks, int kw_log
 //    than a fifth of the waves' steps would find no superblock (k = 1536, 64
 //    experts of 2048 rows with two positions each: kw 4 / 2 39.5 / 34.9 us); T = 2
 //    keeps 4, the shorter way.
+//  - x laid out by the products' own waves for a few rows, up to two a group and k
+//    to 8192.  A launch for x against none: one token, eight of 64 experts 1536 x
+//    2048 11.3 / 8.7 us, two of eight 14336 x 4096 21.6 / 20.0 us, 4096 x 14336 25.7 /
+//    25.8 us; 16 rows, two a group, 512 x 2048 9.2 / 6.7 us, eight a group 9.4 / 10.9
+//    us; eight rows of one group 4096 x 4096 15.3 / 21.6 us (every block of rows
+//    converts them again).  At T = 4, 16 rows would leave one workgroup a CU.
 struct GroupedCut {
     int T, kw_log2;
+    bool fused;                        // x laid out by the products' own waves
     int blocks, fine;                  // blocks of rows
     int64_t grid;
 };
@@ -565,6 +695,8 @@ GroupedCut grouped_cut(int64_t rows, int64_t groups, int64_t n, int64_t k)
     const int64_t S = k / kQK;
     GroupedCut c;
     c.T = tiles * ((n + 63) / 64) < 256 ? 2 : rows >= 8 * groups ? 8 : 4;
+    c.fused = c.T < 8 && rows <= (c.T == 2 ? kFused<2> : kFused<4>) && rows <= 2 * groups &&
+              k <= 8192;
     c.kw_log2 = 2;
     auto steps = [&](int log2) { return (((S - 1) >> log2) + 1) << log2; };  // of all parts
     while (c.T > 2 && c.kw_log2 > 0 && steps(c.kw_log2) * 4 > S * 5) {
@@ -595,6 +727,19 @@ int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k)
 
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream)
 {
+    const GroupedCut c = grouped_cut(a.g.rows, a.g.groups, a.n, a.k);
+    const dim3 grid((unsigned)c.grid), block(64 * kWaves);
+    if (c.fused) {                             // T is 2 or 4
+        auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+        };
+        if (c.T == 2) {
+            a.q ? launch(grouped_kernel<2, kXQ8>) : launch(grouped_kernel<2, kXF32>);
+        } else {
+            a.q ? launch(grouped_kernel<4, kXQ8>) : launch(grouped_kernel<4, kXF32>);
+        }
+        return hipGetLastError();
+    }
     // a piece of eight elements per thread and pass
     const int pieces = a.k / 8;
     const dim3 rows((unsigned)a.g.rows), threads(pieces < 1024 ? (pieces + 63) / 64 * 64 : 1024);
@@ -607,17 +752,18 @@ hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream)
     if (e != hipSuccess) {
         return e;
     }
-    const GroupedCut c = grouped_cut(a.g.rows, a.g.groups, a.n, a.k);
-    const dim3 grid((unsigned)c.grid), block(64 * kWaves);
     if (c.T == 2) {
-        hipLaunchKernelGGL(grouped_kernel<2>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+        hipLaunchKernelGGL((grouped_kernel<2, kXLaidOut>), grid, block, 0, stream, a, c.blocks,
+                           c.kw_log2);
     } else if (c.T == 4) {
-        hipLaunchKernelGGL(grouped_kernel<4>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+        hipLaunchKernelGGL((grouped_kernel<4, kXLaidOut>), grid, block, 0, stream, a, c.blocks,
+                           c.kw_log2);
     } else if (c.fine > 0) {
         hipLaunchKernelGGL(grouped_either_kernel, grid, block, 0, stream, a, c.blocks, c.fine,
                            c.kw_log2);
     } else {
-        hipLaunchKernelGGL(grouped_kernel<8>, grid, block, 0, stream, a, c.blocks, c.kw_log2);
+        hipLaunchKernelGGL((grouped_kernel<8, kXLaidOut>), grid, block, 0, stream, a, c.blocks,
+                           c.kw_log2);
     }
     return hipGetLastError();
 }

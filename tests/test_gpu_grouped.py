@@ -149,6 +149,10 @@ SIZES += [
 # the cut that the number of tiles decides: the coarse one, the fine one, and one
 # where fewer tiles are there than the sizes allow
 SIZES += [([40, 8], 20500, 256), ([40, 8], 4100, 512), ([0, 0, 70, 0, 0, 1], 5000, 1280)]
+# few rows, up to two a group on average: with two and with four row tiles a wave
+SIZES += [([1, 1], 9000, 512), ([3, 1, 0, 2], 5000, 768), ([1] * 8, 2100, 1280),
+          ([9, 4, 0, 1, 0, 0, 0, 0], 40, 1024), ([2], 70, 256), ([16] + [0] * 7, 100, 2048),
+          ([1, 1], 30, 8448)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "q8", "f16"])
@@ -274,6 +278,37 @@ def test_grouped_ranges_of_x():
     y1 = y0.copy()
     y1[[6, 7]] = got[[6, 7]]
     _check("f32", W, x, off, np.arange(rows), yr, y1, got, n, k, norm=False)
+
+
+@pytest.mark.parametrize("kind", ["f32", "q8"])
+@pytest.mark.parametrize("sizes,n", [([4, 1, 0, 2, 3], 40), ([2, 1, 0, 2, 3], 9000)])
+def test_grouped_few_rows_ranges_of_x(kind, sizes, n):
+    """Few rows, whose superblocks lie far apart, in either order: the largest
+    first, last, and zeros between; non-finite ones leave other rows alone."""
+    rng = np.random.default_rng(12)
+    k, groups, rows = 2304, len(sizes), sum(sizes)
+    W = Weights(rng, groups, n, k)
+    x = _make_x(rng, kind, rows, k)
+    scale = x if kind == "f32" else x[1]                 # what carries the range
+    per = scale.shape[1] // 9
+    up = np.array([-120, -60, -1000, -40, 0, 3, -1000, 40, 80], np.float64)
+    for i, e in enumerate((up, up[::-1], rng.permutation(up), np.full(9, -1000.0))):
+        scale[i] *= np.repeat(np.exp2(e), per).astype(np.float32)
+    scale[4, per + 1] = np.inf
+    scale[5, 8 * per + 3] = np.nan
+    if kind == "q8":
+        x[0][4, 256:512] = 5
+        x[0][5, 2048:] = 5
+    off = _offsets(sizes)
+    y0 = np.full((rows, n), 1.0, np.float32)
+    print("grouped few rows %s n=%d" % (kind, n), flush=True)
+    got = _gpu(kind, W.bytes, x, y0, off, n, k, groups, rows)
+    assert not np.isfinite(got[4]).any() and not np.isfinite(got[5]).any()
+    assert (got[3] == 0).all()
+    yr = np.where(np.isin(np.arange(rows), [4, 5]), -1, np.arange(rows))
+    y1 = y0.copy()
+    y1[[4, 5]] = got[[4, 5]]
+    _check(kind, W, x, off, np.arange(rows), yr, y1, got, n, k, norm=False)
 
 
 def test_grouped_weights_not_finite_stay_in_their_row():
