@@ -625,15 +625,17 @@ def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: 
 def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows: int, *,
                          x_rows=None, x_div: int = 1, x_count=None, y_rows=None, y_count=None,
                          stream=None) -> None:
-    """q4k_gemv_grouped on fp16 mirrors (groups * n x k halves, as f16 or
-    int16 tensors) and fp16 x, on the matrix cores; asynchronous on stream."""
+    """q4k_gemv_grouped on fp16 mirrors (groups * n x k halves) and fp16 x, each
+    an f16 tensor or its bits in an int16 or uint16 one, on the matrix cores;
+    asynchronous on stream."""
     dev = _device(w16, x16)
     i32 = _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
+    halves = (_torch.float16, _torch.int16, _torch.uint16)
     for t in (w16, x16):
-        if hasattr(t, "element_size") and t.element_size() != 2:
-            raise TypeError("expected 16-bit elements, got %s" % t.dtype)
+        if hasattr(t, "get_device") and t.dtype not in halves:
+            raise TypeError("expected f16 (or its bits as 16-bit integers), got %s" % t.dtype)
     _run(load_library().q4k_f16_gemm_grouped, "q4k_f16_gemm_grouped", dev, stream,
          _at(w16, None, groups * n * k, dev), _at(x16, None, x_count * k, dev),
          _at(y, _torch.float32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
