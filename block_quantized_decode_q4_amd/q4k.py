@@ -405,7 +405,8 @@ def q4k_f16_gemm_f32x_noalloc(w16, x, y, m: int, n: int, k: int, stream=None) ->
 # These run where their tensors live: the device of the first tensor, made
 # current for the call when it is not, on that device's current stream unless
 # one is given.  A tensor on another device, of another type than the call
-# takes, not dense or too short is refused before the call.
+# takes, not dense or too short is refused before the call, and so is any
+# object but a tensor or an integer address (an array in host memory).
 _torch = None
 _raw_stream = None          # device index -> address of its current stream
 _current_device = None
@@ -443,7 +444,9 @@ def _at(a, dtype, count, dev):
     if a is None or type(a) is int:
         return a
     if not hasattr(a, "get_device"):
-        return _addr(a)
+        if isinstance(a, int):
+            return int(a)
+        raise TypeError("expected a tensor on the GPU or its address, got %s" % type(a))
     if a.get_device() != dev:
         raise ValueError("tensors on more than one device: %s and cuda:%s" % (a.device, dev))
     if a.dtype is not dtype and dtype is not None:

@@ -1,6 +1,7 @@
 """The binding of the operators around a layer's projections on the CPU: which
 arguments reach the library.  Stand-ins take the place of GPU tensors and of
 the library, so nothing is launched: a call that is let through is recorded."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -65,3 +66,51 @@ def test_f16_grouped_takes_halves_only(calls):
     for w, x in ((half, half), (torch.int16, half), (half, torch.int16), (torch.uint16, half)):
         _f16_grouped(w, x)
     assert [name for name, _ in calls] == ["q4k_f16_gemm_grouped"] * 4
+
+
+def _every_call():
+    """Each call with every argument that is memory: (function, its memory
+    arguments by name, the rest)."""
+    f32, f16, i32, u8, i8 = (torch.float32, torch.float16, torch.int32, torch.uint8, torch.int8)
+    t = GpuTensor
+    ws = t(u8, 1 << 16)
+    rows = dict(y=t(f32, 5, 8), offsets=t(i32, 3), x_rows=t(i32, 5), y_rows=t(i32, 5))
+    q4 = dict(rows, w=t(u8, 2 * 8, 144), ws=ws)
+    sizes = dict(n=8, k=256, groups=2, rows=5)
+    return [
+        (q4k.q4k_rmsnorm, dict(x=t(f32, 2, 64), weight=t(f32, 64), residual=t(f32, 2, 64),
+                               sum_out=t(f32, 2, 64), y=t(f32, 2, 64), y16=t(f16, 2, 64),
+                               q=t(i8, 2, 64), d=t(f32, 2, 2)), dict(k=64, m=2)),
+        (q4k.q4k_moe_route, dict(logits=t(f32, 2, 8), ids=t(i32, 2, 2), weights=t(f32, 2, 2),
+                                 offsets=t(i32, 9), order=t(i32, 4), ws=ws),
+         dict(n_experts=8, topk=2, m=2)),
+        (q4k.q4k_moe_group, dict(ids=t(i32, 4), offsets=t(i32, 9), order=t(i32, 4), ws=ws),
+         dict(count=4, groups=8)),
+        (q4k.q4k_moe_combine, dict(y=t(f32, 4, 8), weights=t(f32, 2, 2), ids=t(i32, 2, 2),
+                                   out=t(f32, 2, 8), residual=t(f32, 2, 8)),
+         dict(n=8, topk=2, m=2)),
+        (q4k.q4k_gemv_grouped, dict(q4, x=t(f32, 5, 256)), sizes),
+        (q4k.q4k_gemv_grouped_q8, dict(q4, q=t(i8, 5, 256), d=t(f32, 5, 8)), sizes),
+        (q4k.q4k_f16_gemm_grouped, dict(rows, w16=t(f16, 16, 256), x16=t(f16, 5, 256)), sizes),
+        (q4k.q4k_lora, dict(x=t(f32, 5, 64), a=t(f16, 2, 4, 64), b=t(f16, 2, 8, 4), y=t(f32, 5, 8),
+                            offsets=t(i32, 3), order=t(i32, 5), base=t(f32, 5, 8), ranks=t(i32, 2),
+                            scales=t(f32, 2), ws=ws),
+         dict(n=8, k=64, r=4, adapters=2, rows=5)),
+    ]
+
+
+def _host_array(t):
+    kind = {torch.float32: np.float32, torch.float16: np.float16, torch.int32: np.int32,
+            torch.uint8: np.uint8, torch.int8: np.int8}[t.dtype]
+    return np.zeros(t.shape, kind)
+
+
+def test_host_arrays_are_refused(calls):
+    """A numpy array lies in host memory, which a kernel must not be given."""
+    for call, memory, rest in _every_call():
+        call(**memory, **rest)
+        assert calls.pop()[0] == call.__name__
+        for name, t in memory.items():
+            with pytest.raises(TypeError):
+                call(**dict(memory, **{name: _host_array(t)}), **rest)
+            assert calls == [], (call.__name__, name)
