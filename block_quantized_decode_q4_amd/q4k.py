@@ -531,7 +531,7 @@ def q4k_rmsnorm(x, weight, k: int, m: int = 1, *, eps: float = 1e-5, residual=No
     k: h to sum_out, y to any of y (f32), y16 (f16) and q, d (Q8 codes and
     scales); x f32, f16 or bf16, its rows x_stride elements apart (0: k);
     asynchronous on stream."""
-    dev = _device(x, weight)
+    dev = _device(x, weight, residual, sum_out, y, y16, q, d)
     mk = m * k
     f32, i8, f16 = _torch.float32, _torch.int8, _torch.float16
     _run(load_library().q4k_rmsnorm, "q4k_rmsnorm", dev, stream,
@@ -551,7 +551,7 @@ def q4k_moe_route(logits, ids, weights, n_experts: int, topk: int, m: int = 1, *
                   logits_stride: int = 0, stream=None) -> None:
     """The topk experts of m tokens (ids, softmax weights) and, with offsets
     and order, their slots grouped by expert; asynchronous on stream."""
-    dev = _device(logits, ids)
+    dev = _device(logits, ids, weights, offsets, order, ws)
     f32, i32 = _torch.float32, _torch.int32
     slots = m * topk
     _run(load_library().q4k_moe_route, "q4k_moe_route", dev, stream,
@@ -565,7 +565,7 @@ def q4k_moe_group(ids, offsets, order, count: int, groups: int, *, ws=None, ws_b
                   stream=None) -> None:
     """Slots grouped by id (order), and where each group begins (offsets);
     asynchronous on stream."""
-    dev = _device(ids, offsets)
+    dev = _device(ids, offsets, order, ws)
     i32 = _torch.int32
     _run(load_library().q4k_moe_group, "q4k_moe_group", dev, stream, _at(ids, i32, count, dev),
          _at(offsets, i32, groups + 1, dev), _at(order, i32, count, dev), int(count),
@@ -576,7 +576,7 @@ def q4k_moe_combine(y, weights, ids, out, n: int, topk: int, m: int = 1, *, resi
                     stream=None) -> None:
     """out[t] = residual[t] + sum_j weights[t][j] y[t * topk + j] over the
     choices with an id (ids None: all); asynchronous on stream."""
-    dev = _device(y, out)
+    dev = _device(y, weights, ids, out, residual)
     f32 = _torch.float32
     mt = m * topk
     _run(load_library().q4k_moe_combine, "q4k_moe_combine", dev, stream, _at(y, f32, mt * n, dev),
@@ -595,7 +595,7 @@ def q4k_gemv_grouped(w, x, y, offsets, n: int, k: int, groups: int, rows: int, *
                      ws_bytes=None, stream=None) -> None:
     """Position p of group g: y[y_rows[p]] = W_g x[x_rows[p] // x_div], W_g
     in Q4_K, x f32 (counts default to rows); asynchronous on stream."""
-    dev = _device(w, x)
+    dev = _device(w, x, y, offsets, x_rows, y_rows, ws)
     f32, i32 = _torch.float32, _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
@@ -612,7 +612,7 @@ def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: 
                         ws=None, ws_bytes=None, stream=None) -> None:
     """q4k_gemv_grouped with x in Q8: codes q (int8) and scales d (f32, one
     per 32); asynchronous on stream."""
-    dev = _device(w, q)
+    dev = _device(w, q, d, y, offsets, x_rows, y_rows, ws)
     f32, i32 = _torch.float32, _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
@@ -631,7 +631,7 @@ def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows
     """q4k_gemv_grouped on fp16 mirrors (groups * n x k halves) and fp16 x, each
     an f16 tensor or its bits in an int16 or uint16 one, on the matrix cores;
     asynchronous on stream."""
-    dev = _device(w16, x16)
+    dev = _device(w16, x16, y, offsets, x_rows, y_rows)
     i32 = _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
@@ -658,7 +658,7 @@ def q4k_lora(x, a, b, y, offsets, order, n: int, k: int, r: int, adapters: int, 
     adapter a (a: adapters x r x k, b: adapters x n x r, both f16; x f32, f16
     or bf16; offsets and order as q4k_moe_group gives them); asynchronous on
     stream."""
-    dev = _device(x, a)
+    dev = _device(x, a, b, y, offsets, order, base, ranks, scales, ws)
     f32, i32, f16 = _torch.float32, _torch.int32, _torch.float16
     _run(load_library().q4k_lora, "q4k_lora", dev, stream, _at(x, None, rows * k, dev),
          _act_type(x, x_type), _at(a, f16, adapters * r * k, dev),

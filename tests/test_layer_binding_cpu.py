@@ -114,3 +114,20 @@ def test_host_arrays_are_refused(calls):
             with pytest.raises(TypeError):
                 call(**dict(memory, **{name: _host_array(t)}), **rest)
             assert calls == [], (call.__name__, name)
+
+
+def test_one_tensor_among_addresses(calls):
+    """Addresses are taken wherever a tensor is; the one tensor left, whichever
+    it is, says which device the call runs on."""
+    for call, memory, rest in _every_call():
+        addresses = dict.fromkeys(memory, 0x100000)
+        if "ws" in memory:
+            rest = dict(rest, ws_bytes=memory["ws"].numel())
+        for name, t in memory.items():
+            call(**dict(addresses, **{name: t}), **rest)
+            assert [c[0] for c in calls] == [call.__name__], (call.__name__, name)
+            calls.clear()
+            t.get_device = lambda: -1              # a tensor on the host
+            with pytest.raises(ValueError):
+                call(**dict(addresses, **{name: t}), **rest)
+            assert calls == [], (call.__name__, name)
