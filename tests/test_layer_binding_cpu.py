@@ -127,7 +127,8 @@ def test_one_tensor_among_addresses(calls):
             call(**dict(addresses, **{name: t}), **rest)
             assert [c[0] for c in calls] == [call.__name__], (call.__name__, name)
             calls.clear()
-            t.get_device = lambda: -1              # a tensor on the host
+            host = GpuTensor(t.dtype, *t.shape)
+            host.get_device = lambda: -1
             with pytest.raises(ValueError):
-                call(**dict(addresses, **{name: t}), **rest)
+                call(**dict(addresses, **{name: host}), **rest)
             assert calls == [], (call.__name__, name)
