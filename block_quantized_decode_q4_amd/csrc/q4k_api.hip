@@ -1167,7 +1167,7 @@ size_t q4k_moe_group_ws(int64_t slots, int64_t groups, int64_t topk)
     if (check_group_shape(slots, groups, topk) != Q4K_OK) {
         return 0;
     }
-    return q4k::group_ws_bytes(slots, groups, topk, true);      // routing may need more
+    return q4k::group_ws_most(slots, groups, topk);
 }
 
 int q4k_moe_route(const float* logits, int64_t logits_stride, int32_t* ids, float* weights,
@@ -1352,7 +1352,7 @@ size_t q4k_lora_ws(int64_t rows, int64_t r)
     if (!in_range(rows, 1, kMaxRows) || !in_range(r, 1, 1024)) {
         return 0;
     }
-    return q4k::lora_ws_bytes(rows, r);
+    return q4k::lora_ws_most(rows, r);
 }
 
 int q4k_lora(const void* x, int x_type, const void* a, const void* b, const float* base,

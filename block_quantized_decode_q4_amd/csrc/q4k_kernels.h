@@ -141,6 +141,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 constexpr int kRowExperts = 256;       // experts that 16 lanes route
 bool group_in_one(int64_t slots, int64_t groups, int64_t topk, bool route);
 size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk, bool route);
+size_t group_ws_most(int64_t slots, int64_t groups, int64_t topk);       // or fewer slots
 
 struct CombineArgs {
     const float* y;
@@ -202,6 +203,7 @@ struct LoraArgs {
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
 size_t lora_ws_bytes(int64_t rows, int64_t r);
+size_t lora_ws_most(int64_t rows, int64_t r);          // or fewer rows
 bool lora_fits(int64_t rows, int64_t adapters, int64_t n, int64_t r);    // the launch limits
 
 }  // namespace q4k

@@ -38,6 +38,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "q4k_device.h"
@@ -585,9 +586,12 @@ void launch_up(const LoraArgs& a, dim3 up, hipStream_t stream)
 // workspace, so by the rows alone.)  Both products with 1 / 2 / 4 parts, rank 64,
 // n = k = 4096: 512 rows 16.5 / 13.7 / 12.2 us, 2048 rows 25.2 / 22.8 / 24.5 us,
 // 4096 rows 36.9 / 38.8 / 41.4 us.
+constexpr int64_t kRowsOf4 = 512;      // the most rows of four and of two parts
+constexpr int64_t kRowsOf2 = 4095;
+
 int down_parts(int64_t rows)
 {
-    return rows <= 512 ? 4 : rows < 4096 ? 2 : 1;
+    return rows <= kRowsOf4 ? 4 : rows <= kRowsOf2 ? 2 : 1;
 }
 
 }  // namespace
@@ -595,6 +599,19 @@ int down_parts(int64_t rows)
 size_t lora_ws_bytes(int64_t rows, int64_t r)
 {
     return (size_t)down_parts(rows) * (size_t)rows * (size_t)((r + 15) / 16 * 16) * sizeof(float);
+}
+
+// The most that `rows` rows or fewer take: 512 rows in four parts are 2048 rows of
+// v, and 513 in two are 1026.
+size_t lora_ws_most(int64_t rows, int64_t r)
+{
+    size_t most = lora_ws_bytes(rows, r);
+    for (const int64_t step : {kRowsOf4, kRowsOf2}) {
+        if (step < rows) {
+            most = std::max(most, lora_ws_bytes(step, r));
+        }
+    }
+    return most;
 }
 
 // The grids: fewer than 2^32 threads, 65535 workgroups along y

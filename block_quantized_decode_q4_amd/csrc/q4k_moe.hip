@@ -546,10 +546,13 @@ combine_kernel(CombineArgs a)
 // Slots per chunk: whole tokens, about 256 chunks (each placing workgroup
 // adds up all chunks' counts), and at least 64 slots.  8192 tokens of 128
 // experts, topk 8, with 128 / 256 / 512 chunks: 14.4 / 12.4 / 18.2 us.
+constexpr int64_t kChunks = 256;
+constexpr int64_t kChunkSlots = 64;
+
 int64_t chunk_slots(int64_t slots, int64_t topk)
 {
-    int64_t c = (slots + 255) / 256;
-    c = c < 64 ? 64 : c;
+    int64_t c = (slots + kChunks - 1) / kChunks;
+    c = c < kChunkSlots ? kChunkSlots : c;
     return (c + topk - 1) / topk * topk;
 }
 
@@ -603,6 +606,17 @@ size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk, bool route)
     }
     const int64_t chunk = chunk_slots(slots, topk);
     return sizeof(int) * (size_t)((slots + chunk - 1) / chunk) * (size_t)groups;
+}
+
+// The most that `slots` slots or fewer take: the chunks of the rule above, without
+// its rounding (16385 slots are 253 chunks of 65, 16384 are 256 of 64).
+size_t group_ws_most(int64_t slots, int64_t groups, int64_t topk)
+{
+    if (group_in_one(slots, groups, topk, true)) {
+        return 0;                          // routing takes more than grouping
+    }
+    const int64_t chunks = (slots + kChunkSlots - 1) / kChunkSlots;
+    return sizeof(int) * (size_t)(chunks < kChunks ? chunks : kChunks) * (size_t)groups;
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream)

@@ -390,7 +390,9 @@ int q4k_f16_gemm_f32x_noalloc(const void* w16, const float* x, float* y, int64_t
  *  - Every tensor is row-major and dense unless a stride is given; device
  *    pointers are 16-byte aligned (an optional one may be NULL).
  *  - A workspace is the caller's, `ws_bytes` long; the *_ws function of the
- *    call gives the bytes it needs (Q4K_ERR_SIZE when there are fewer).  Calls
+ *    call gives the bytes that it and every smaller call need (fewer rows or
+ *    slots, groups, r or k, the same topk), so one made for the largest call
+ *    serves them all (Q4K_ERR_SIZE when there are fewer bytes).  Calls
  *    that may run at the same time need workspaces of their own, captured
  *    graphs included.  Its contents mean nothing between calls.
  *  - Outputs and workspaces overlap neither inputs nor one another, unless the
