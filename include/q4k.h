@@ -399,6 +399,10 @@ int q4k_f16_gemm_f32x_noalloc(const void* w16, const float* x, float* y, int64_t
  *    call says so.
  *  - Rows and positions number fewer than 2^22 (Q4K_ERR_SHAPE beyond), and a
  *    launch fewer than 2^32 threads.
+ *  - The same call on the same data gives the same bits.  A row's last bits may
+ *    differ between calls of other numbers of rows, positions or groups, which
+ *    decide how its sums are cut (a token alone and in a batch); within one
+ *    such cut they do not depend on the other rows' data.
  * ------------------------------------------------------------------- */
 
 /* Types of activations. */

@@ -1,0 +1,118 @@
+"""Whose data a row's bits depend on, in the grouped products and the adapters:
+on no other row's, in calls of the same numbers of rows and groups; and how far
+calls of other numbers may lie from one another.
+
+Two forms of a Q4_K product each err by about 2^-20 of the results' 2-norm (280
+roundings of 2^-24 that add like a random walk), their difference by 2^-19.5:
+held to 2^-18.  A lost low half of x would leave 2^-13.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from block_quantized_decode_q4_amd import q4k, synth  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    q4k.load_library()
+    yield
+
+
+def _weights(kind, groups, n, k):
+    if kind == "f16":
+        g = torch.Generator("cuda").manual_seed(n + k)
+        return (torch.randn((groups * n, k), generator=g, device="cuda") * 0.05).half()
+    return torch.from_numpy(synth.pack(synth.draw_fields(np.random.default_rng(n + k), groups * n,
+                                                         k // 256))).cuda()
+
+
+def _x(kind, rows, k, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    x = torch.randn((rows, k), generator=g, device="cuda")
+    if kind == "q8":
+        d = x.view(rows, -1, 32).abs().amax(2) / 127
+        return [torch.round(x.view(rows, -1, 32) / d[..., None]).to(torch.int8).view(rows, k), d]
+    return [x.half() if kind == "f16" else x]
+
+
+def _product(kind, w, x, sizes, n, k):
+    rows, groups = sum(sizes), len(sizes)
+    off = torch.tensor(np.concatenate(([0], np.cumsum(sizes))), dtype=torch.int32).cuda()
+    y = torch.full((rows, n), float("nan"), device="cuda")
+    call = dict(f32=q4k.q4k_gemv_grouped, q8=q4k.q4k_gemv_grouped_q8, f16=q4k.q4k_f16_gemm_grouped)[kind]
+    ws = {} if kind == "f16" else dict(ws=torch.full((q4k.q4k_gemv_grouped_ws(k, rows),), 0xFF,
+                                                     dtype=torch.uint8, device="cuda"))
+    call(w, *x, y, off, n, k, groups, rows, **ws)
+    return y
+
+
+# the same rows in group 0 first, then others; the one-launch form (up to two rows
+# a group) with two and four row tiles a wave, and the two-launch form with two,
+# four and eight
+FORMS = [([4, 1, 1], [2, 3, 1], 40, 2304, 2), ([4, 1, 1], [1, 5, 0], 9000, 768, 1),
+         ([20, 0, 10], [5, 15, 10], 200, 1536, 5),
+         ([3, 1] + [2] * 38, [1, 9, 0, 0] + [2] * 35 + [0], 450, 768, 1),
+         ([40, 20], [18, 42], 5000, 512, 18)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "q8", "f16"])
+@pytest.mark.parametrize("sizes,others,n,k,same", FORMS)
+def test_grouped_bits_do_not_depend_on_other_rows(kind, sizes, others, n, k, same):
+    assert sum(sizes) == sum(others)
+    rows, groups = sum(sizes), len(sizes)
+    w = _weights(kind, groups, n, k)
+    x = _x(kind, rows, k, 1)
+    print("grouped bits %s %s n=%d k=%d" % (kind, sizes[:4], n, k), flush=True)
+    a = _product(kind, w, x, sizes, n, k)
+    assert bool(a.isfinite().all())
+    assert torch.equal(a, _product(kind, w, x, sizes, n, k))
+    x2 = _x(kind, rows, k, 2)
+    x2[-1][same:] *= 1000
+    x2[-1][rows - 1, 0] = float("nan")
+    x2[-1][same, 0] = float("inf")
+    for to, of in zip(x2, x):
+        to[:same] = of[:same]
+    for cut in (sizes, others):
+        assert torch.equal(_product(kind, w, x2, cut, n, k)[:same], a[:same])
+
+
+@pytest.mark.parametrize("kind", ["f32", "q8"])
+@pytest.mark.parametrize("n,k", [(200, 1536), (9000, 768)])
+def test_grouped_one_launch_against_two(kind, n, k):
+    """Five rows alone (one launch) and the same five of thirty (two)."""
+    w = _weights(kind, 3, n, k)
+    x = _x(kind, 30, k, 3)
+    many = _product(kind, w, x, [20, 0, 10], n, k)[:5]
+    few = _product(kind, w, [t[:5].contiguous() for t in x], [5, 0, 0], n, k)
+    assert float((many.double() - few.double()).norm() / many.double().norm()) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows", [6, 600, 4100])
+def test_lora_bits_do_not_depend_on_other_rows(kind, rows):
+    n, k, r, same = 300, 520, 70, 3
+    g = torch.Generator("cuda").manual_seed(rows)
+    a = torch.randn((2, r, k), generator=g, device="cuda").half()
+    b = torch.randn((2, n, r), generator=g, device="cuda").half()
+    x = torch.randn((rows, k), generator=g, device="cuda").to(kind)
+    x2 = (torch.randn((rows, k), generator=g, device="cuda") * 100).to(kind)
+    x2[rows - 1, 0] = float("nan")
+    x2[same, 0] = float("inf")
+    x2[:same] = x[:same]
+    ws = torch.full((q4k.q4k_lora_ws(rows, r),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = []
+    for v, first in ((x, rows - 2), (x, rows - 2), (x2, rows - 2), (x2, same)):
+        off = torch.tensor([0, first, rows], dtype=torch.int32, device="cuda")
+        y = torch.full((rows, n), float("nan"), device="cuda")
+        print("lora bits %s rows=%d first=%d" % (kind, rows, first), flush=True)
+        q4k.q4k_lora(v, a, b, y, off, None, n, k, r, 2, rows, ws=ws)
+        out.append(y)
+    assert bool(out[0].isfinite().all()) and torch.equal(out[0], out[1])
+    for y in out[2:]:
+        assert torch.equal(y[:same], out[0][:same])
