@@ -559,8 +559,9 @@ size_t q4k_lora_ws(int64_t rows, int64_t r);
  * to 2^-22 of their value or 2^-39 of their row's largest into B (A x), all
  * sums are f32: y is within (k + r + 4) 2^-23 * (|base| + |scale| sum_r |B|
  * sum_k |A| |x|) + 2^-38 |scale| sum_r |B| max_r |A x| of the exact value.  A
- * row of x with an infinity or NaN gives NaN or an infinity in its y row; other
- * rows are unaffected.  Asynchronous; allocates nothing. */
+ * row of x with an infinity or NaN gives NaN or an infinity in its y row (an
+ * adapter of rank 0 adds 0 to the base whatever x, its scale, a and b hold);
+ * other rows are unaffected.  Asynchronous; allocates nothing. */
 int q4k_lora(const void* x, int x_type, const void* a, const void* b, const float* base,
              float* y, const int32_t* ranks, const float* scales, const int32_t* offsets,
              const int32_t* order, int64_t n, int64_t k, int64_t r, int64_t adapters,

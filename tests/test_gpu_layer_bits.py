@@ -116,3 +116,29 @@ def test_lora_bits_do_not_depend_on_other_rows(kind, rows):
     assert bool(out[0].isfinite().all()) and torch.equal(out[0], out[1])
     for y in out[2:]:
         assert torch.equal(y[:same], out[0][:same])
+
+
+@pytest.mark.parametrize("rows", [4, 700, 4200])
+def test_lora_rank_0_adds_nothing(rows):
+    """Whatever x, the scale, a and b hold; the other adapter is as it is alone."""
+    n, k, r = 131, 72, 24
+    g = torch.Generator("cuda").manual_seed(rows)
+    x = torch.randn((rows, k), generator=g, device="cuda")
+    a = torch.randn((2, r, k), generator=g, device="cuda").half()
+    b = torch.randn((2, n, r), generator=g, device="cuda").half()
+    base = torch.randn((rows, n), generator=g, device="cuda")
+    none = rows // 2
+    off = torch.tensor([0, none, rows], dtype=torch.int32, device="cuda")
+    ranks = torch.tensor([0, r], dtype=torch.int32, device="cuda")
+    ws = torch.full((q4k.q4k_lora_ws(rows, r),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = []
+    for bad in (False, True):
+        scales = torch.tensor([float("inf") if bad else 1.0, 0.5], device="cuda")
+        if bad:
+            x[:none:2], x[1:none:2], a[0], b[0] = float("nan"), float("inf"), float("nan"), float("inf")
+        out.append(torch.full((rows, n), 7.0, device="cuda"))
+        print("lora rank 0 rows=%d bad=%s" % (rows, bad), flush=True)
+        q4k.q4k_lora(x, a, b, out[-1], off, None, n, k, r, 2, rows, base=base, ranks=ranks,
+                     scales=scales, ws=ws)
+        assert torch.equal(out[-1][:none], base[:none])
+    assert torch.equal(*out) and bool(out[0].isfinite().all())
