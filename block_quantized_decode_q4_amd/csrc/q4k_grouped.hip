@@ -33,11 +33,17 @@
 // all waves of a workgroup, superblock by superblock with a barrier each, was
 // slower (one token 27 us, 48 tokens on eight wide experts 124 us).
 //
-// What bounds it: about 125 vector instructions a superblock and row tile
-// beside 17 matrix ones, and the weights' bytes.  One token, two of eight experts
-// 14336 x 4096 (66 MB): 20 us; 264 MB (eight experts 4096 x
-// 14336, 16 positions each) 78 us, 3.4 TB/s; 48 tokens of uneven experts (ten
-// tiles where six experts are met) 99 us.  Measured without gain at 264 MB: two
+// What bounds it: by the counters neither pipe and not the bytes, but latency, with
+// too few waves to hide it.  A superblock and row tile takes about 135 vector and 17
+// matrix instructions.  48 tokens of uneven experts 4096 x 14336 (ten or eleven tiles
+// where six to eight experts are met): 89 us for the products, with 268 MB read (3
+// TB/s), the vector pipe busy 46 % of the time and the matrix pipe 21 %; two waves a
+// SIMD on average, which wait half of their time to issue an instruction and a sixth
+// of it for memory.  One token, two of eight experts 14336 x 4096 (66 MB): 20 us (3.3
+// TB/s), the pipes busy 50 and 17 %, 1.5 waves a SIMD, a third of their time waiting
+// for memory; the same bytes as 4096 x 14336, 256 workgroups, 26 us.  264 MB (eight
+// experts 4096 x 14336, 16 positions each: 256 workgroups, one wave a SIMD) 76-78 us,
+// 3.4 TB/s.  Measured without gain at 264 MB: two
 // row tiles worked on at once, four row tiles of weights in flight instead of two,
 // x of the next superblock asked for ahead (79 us each, and fewer waves a SIMD).
 
@@ -360,8 +366,8 @@ __device__ __forceinline__ h8_t operand(uint32_t D, h2_t sl, h2_t sh)
 // x of one superblock in registers, straight from the workspace, and goes
 // through its row tiles with it; the sums of all its tiles stay in registers
 // too, and the parts are added up once, at the end.  No barrier before that: a
-// wave waits for its own loads only.  Three waves a SIMD (x alone takes 66
-// registers).
+// wave waits for its own loads only.  Up to three waves a SIMD (x alone takes
+// 66 registers); few workgroups leave fewer.
 constexpr int kWaves = 4;
 
 template <int T>
@@ -676,12 +682,13 @@ grouped_either_kernel(GroupedArgs a, int row_blocks, int fine_blocks, int kw_log
 //    than a fifth of the waves' steps would find no superblock (k = 1536, 64
 //    experts of 2048 rows with two positions each: kw 4 / 2 39.5 / 34.9 us); T = 2
 //    keeps 4, the shorter way.
-//  - x laid out by the products' own waves for a few rows, up to two a group and k
-//    to 8192.  A launch for x against none: one token, eight of 64 experts 1536 x
-//    2048 11.3 / 8.7 us, two of eight 14336 x 4096 21.6 / 20.0 us, 4096 x 14336 25.7 /
-//    25.8 us; 16 rows, two a group, 512 x 2048 9.2 / 6.7 us, eight a group 9.4 / 10.9
-//    us; eight rows of one group 4096 x 4096 15.3 / 21.6 us (every block of rows
-//    converts them again).  At T = 4, 16 rows would leave one workgroup a CU.
+//  - x laid out by the products' own waves for a few rows, up to two a group on
+//    average (how they are spread is not known here) and k to 8192.  A launch for x
+//    against none: one token, eight of 64 experts 1536 x 2048 11.3 / 8.7 us, two of
+//    eight 14336 x 4096 21.6 / 20.0 us, 4096 x 14336 25.7 / 25.8 us; 16 rows, two a
+//    group, 512 x 2048 9.2 / 6.7 us, eight a group 9.4 / 10.9 us; eight rows of one
+//    group 4096 x 4096 15.3 / 21.6 us (every block of rows converts them again).  At
+//    T = 4, 16 rows would leave one workgroup a CU.
 struct GroupedCut {
     int T, kw_log2;
     bool fused;                        // x laid out by the products' own waves

@@ -9,8 +9,10 @@
 // rows of one adapter (q4k_groups.h).
 //
 // x in binary16 goes through v_mfma_f32_16x16x32_f16; f32 (and bfloat16)
-// x through v_mfma_f32_16x16x4_f32 with A widened to f32; no operand is
-// rounded.  For B v each row's v, scaled by the power of two that brings its
+// x through v_mfma_f32_16x16x4_f32 with A widened to f32, eight instructions
+// for one (2048 rows at rank 64, n = k = 4096, a call: binary16 23.7 us, bfloat16
+// 29.5, f32 43.3, of which 3.4 are x's further bytes); no operand of
+// A x is rounded.  For B v each row's v, scaled by the power of two that brings its
 // largest into [2^14, 2^15), is two binary16 numbers: hi and the rest, lo, which
 // leaves at most 2^-22 of the value or 2^-39 of the row's largest, and both go
 // through the f16 matrix cores into one f32 sum (an eighth of the f32
@@ -27,8 +29,8 @@
 // lanes 16 apart) would take 64 clocks of the vector cache per load where
 // neighbouring lanes on neighbouring bytes take about 20, and that bound both
 // kernels.  2048 rows at rank 64, n = k = 4096, x binary16 (84 MB): down
-// 20 -> 7.4 us, up 27 -> 13.3 us; 24 rows of 16 adapters at rank 16: down 5.2 us,
-// up 4.0 us.  An adapter's tiles go to one XCD, whose L2 then reads A and B once
+// 20 -> 8-10 us, up 27 -> 13-16 us; 24 rows of 16 adapters at rank 16: down 5.4 us,
+// up 4-5 us.  An adapter's tiles go to one XCD, whose L2 then reads A and B once
 // (over all XCDs: 2048 rows 30.9 us a call instead of 22.8, 8192 rows 98 instead of
 // 64).  What bounds them now is the chain of loads that each workgroup waits for
 // (offsets, order, operands), about 1 us a link, so whatever can be asked for
