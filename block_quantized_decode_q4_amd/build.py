@@ -21,10 +21,15 @@ SOURCES = [os.path.join(CSRC, "q4k_kernels.hip"), os.path.join(CSRC, "q4k_dpp.hi
            os.path.join(CSRC, "q4k_q6k.hip"), os.path.join(CSRC, "q4k_f16.hip"),
            os.path.join(CSRC, "q4k_norm.hip"), os.path.join(CSRC, "q4k_moe.hip"),
            os.path.join(CSRC, "q4k_grouped.hip"), os.path.join(CSRC, "q4k_lora.hip"),
+           os.path.join(CSRC, "q4k_act_kernels.hip"), os.path.join(CSRC, "q4k_act_dpp.hip"),
+           os.path.join(CSRC, "q4k_act_mfma.hip"), os.path.join(CSRC, "q4k_act_grouped.hip"),
+           os.path.join(CSRC, "q4k_f16_act.hip"),
            os.path.join(CSRC, "q4k_api.hip")]
 HEADERS = [os.path.join(CSRC, "q4k_kernels.h"), os.path.join(CSRC, "q4k_device.h"),
            os.path.join(CSRC, "q4k_lines.h"), os.path.join(CSRC, "q4k_xrep.h"),
            os.path.join(CSRC, "q4k_q8.h"), os.path.join(CSRC, "q4k_groups.h"),
+           os.path.join(CSRC, "q4k_out.h"), os.path.join(CSRC, "q4k_epilogue.h"),
+           os.path.join(CSRC, "q4k_f16_tile.h"),
            os.path.join(os.path.dirname(PKG), "include", "q4k.h")]
 ARCH = "gfx950"
 

@@ -465,13 +465,14 @@ int plan_checked(int64_t n, int64_t k, int64_t m, const q4k_launch* opts, bool w
     return Q4K_OK;
 }
 
-int gemv_checked(const void* w, const float* x, float* y, int64_t n, int64_t k, int64_t m,
-                 const q4k_launch* opts, void* stream)
+// The plan of q4k_gemv_ex for these pointers, every argument checked
+int gemv_plan(const void* w, const float* x, const float* y, int64_t n, int64_t k, int64_t m,
+              const q4k_launch* opts, GemvPlan* plan)
 {
     if (!w || !x || !y) {
         return Q4K_ERR_NULL;
     }
-    int rc = check_nk(n, k);
+    const int rc = check_nk(n, k);
     if (rc != Q4K_OK) {
         return rc;
     }
@@ -485,13 +486,50 @@ int gemv_checked(const void* w, const float* x, float* y, int64_t n, int64_t k, 
         return Q4K_ERR_ALIGN;
     }
     const bool w128 = (reinterpret_cast<uintptr_t>(w) & 127u) == 0;
+    return plan_checked(n, k, m, opts, w128, 0, plan);
+}
+
+int gemv_checked(const void* w, const float* x, float* y, int64_t n, int64_t k, int64_t m,
+                 const q4k_launch* opts, void* stream)
+{
     GemvPlan plan;
-    rc = plan_checked(n, k, m, opts, w128, 0, &plan);
+    const int rc = gemv_plan(w, x, y, n, k, m, opts, &plan);
     if (rc != Q4K_OK) {
         return rc;
     }
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return hip_status(q4k::launch_gemv(plan, w, x, y, s));
+}
+
+// An epilogue's pointers, types and alignment
+int check_epilogue(const q4k_epilogue* ep, q4k::EpArgs* out)
+{
+    if (!ep || (!ep->y && !ep->y16)) {
+        return Q4K_ERR_NULL;
+    }
+    if (ep->act < Q4K_ACT_NONE || ep->act > Q4K_ACT_SIGMOID ||
+        (ep->gate && ep->gate_type != Q4K_F32 && ep->gate_type != Q4K_F16)) {
+        return Q4K_ERR_UNSUPPORTED;
+    }
+    if (!aligned16(ep->bias) || !aligned16(ep->gate) || !aligned16(ep->residual) ||
+        !aligned16(ep->y) || !aligned16(ep->y16)) {
+        return Q4K_ERR_ALIGN;
+    }
+    out->bias = ep->bias;
+    out->gate = ep->gate;
+    out->residual = ep->residual;
+    out->y = ep->y;
+    out->y16 = ep->y16;
+    out->gate_type = ep->gate_type;
+    out->act = ep->act;
+    out->parked = 0;
+    return Q4K_OK;
+}
+
+// An address that the checks of a product without an epilogue take for its y
+const float* some_y(const q4k::EpArgs& e)
+{
+    return e.y ? e.y : static_cast<const float*>(e.y16);
 }
 
 // ------------------------------------------------------------------ Q6_K
@@ -675,6 +713,50 @@ int check_group_shape(int64_t slots, int64_t groups, int64_t topk)
     return Q4K_OK;
 }
 
+// The checks of the routing calls; fills what they share
+int check_route(const float* logits, int64_t logits_stride, int32_t* ids, float* weights,
+                int32_t* offsets, int32_t* order, int64_t n_experts, int64_t topk, int renorm,
+                int64_t m, void* ws, size_t ws_bytes, q4k::RouteArgs* a)
+{
+    if (!logits || !ids || !weights || (offsets == nullptr) != (order == nullptr)) {
+        return Q4K_ERR_NULL;
+    }
+    if (!in_range(m, 1, kMaxRows) || !in_range(topk, 1, q4k::kMaxTopk)) {
+        return Q4K_ERR_SHAPE;
+    }
+    const int rc = check_group_shape(m * topk, n_experts, topk);
+    const int64_t stride = logits_stride == 0 ? n_experts : logits_stride;
+    if (rc != Q4K_OK || stride < n_experts || stride > ((int64_t)1 << 40)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) ||
+        !aligned16(offsets) || !aligned16(order) || !aligned16(ws)) {
+        return Q4K_ERR_ALIGN;
+    }
+    if (offsets) {
+        const size_t need = q4k::group_ws_bytes(m * topk, n_experts, topk, true);
+        if (need && !ws) {
+            return Q4K_ERR_NULL;
+        }
+        if (need > ws_bytes) {
+            return Q4K_ERR_SIZE;
+        }
+    }
+    a->logits = logits;
+    a->ids = ids;
+    a->weights = weights;
+    a->offsets = offsets;
+    a->order = order;
+    a->counts = static_cast<int*>(ws);
+    a->stride = stride;
+    a->m = (int)m;
+    a->groups = (int)n_experts;
+    a->topk = (int)topk;
+    a->renorm = renorm != 0;
+    a->slots = (int)(m * topk);
+    return Q4K_OK;
+}
+
 // Grouped rows: pointers, counts and the index arrays' alignment (NULL, an
 // optional array that is not given, is aligned)
 int check_group_rows(const int32_t* offsets, const int32_t* x_rows, const int32_t* y_rows,
@@ -705,7 +787,7 @@ int check_group_rows(const int32_t* offsets, const int32_t* x_rows, const int32_
 
 int gemv_grouped_checked(const void* w, const float* x, const int8_t* q, const float* d, float* y,
                          q4k::GroupRows& g, int64_t n, int64_t k, void* ws, size_t ws_bytes,
-                         void* stream)
+                         void* stream, const q4k::EpArgs* ep = nullptr)
 {
     const int rc = check_nk(n, k);
     if (rc != Q4K_OK) {
@@ -721,7 +803,7 @@ int gemv_grouped_checked(const void* w, const float* x, const int8_t* q, const f
     if (ws_bytes < q4k::grouped_ws_bytes(k, g.rows)) {
         return Q4K_ERR_SIZE;
     }
-    q4k::GroupedArgs a;
+    q4k::GroupedActArgs a;
     a.w = w;
     a.x = x;
     a.q = q;
@@ -731,7 +813,30 @@ int gemv_grouped_checked(const void* w, const float* x, const int8_t* q, const f
     a.g = g;
     a.n = (int)n;
     a.k = (int)k;
-    return hip_status(q4k::launch_grouped(a, static_cast<hipStream_t>(stream)));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (ep) {
+        a.ep = *ep;
+        return hip_status(q4k::launch_grouped(a, s));
+    }
+    return hip_status(q4k::launch_grouped(static_cast<const q4k::GroupedArgs&>(a), s));
+}
+
+// The checks of the grouped products on fp16 mirrors
+int f16_grouped_checks(const void* w16, const void* x16, const void* y, int64_t k, int64_t grid)
+{
+    if (k < 1 || k > kInt32Max) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (k % 64 != 0) {
+        return Q4K_ERR_UNSUPPORTED;      // the k step of the tile
+    }
+    if (!fits_launch(grid, 512)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!aligned16(w16) || !aligned16(x16) || !aligned16(y)) {
+        return Q4K_ERR_ALIGN;
+    }
+    return Q4K_OK;
 }
 
 }  // namespace
@@ -1174,43 +1279,12 @@ int q4k_moe_route(const float* logits, int64_t logits_stride, int32_t* ids, floa
                   int32_t* offsets, int32_t* order, int64_t n_experts, int64_t topk, int renorm,
                   int64_t m, void* ws, size_t ws_bytes, void* stream)
 {
-    if (!logits || !ids || !weights || (offsets == nullptr) != (order == nullptr)) {
-        return Q4K_ERR_NULL;
-    }
-    if (!in_range(m, 1, kMaxRows) || !in_range(topk, 1, q4k::kMaxTopk)) {
-        return Q4K_ERR_SHAPE;
-    }
-    const int rc = check_group_shape(m * topk, n_experts, topk);
-    const int64_t stride = logits_stride == 0 ? n_experts : logits_stride;
-    if (rc != Q4K_OK || stride < n_experts || stride > ((int64_t)1 << 40)) {
-        return Q4K_ERR_SHAPE;
-    }
-    if (!aligned16(logits) || !aligned16(ids) || !aligned16(weights) ||
-        !aligned16(offsets) || !aligned16(order) || !aligned16(ws)) {
-        return Q4K_ERR_ALIGN;
-    }
-    if (offsets) {
-        const size_t need = q4k::group_ws_bytes(m * topk, n_experts, topk, true);
-        if (need && !ws) {
-            return Q4K_ERR_NULL;
-        }
-        if (need > ws_bytes) {
-            return Q4K_ERR_SIZE;
-        }
-    }
     q4k::RouteArgs a = {};
-    a.logits = logits;
-    a.ids = ids;
-    a.weights = weights;
-    a.offsets = offsets;
-    a.order = order;
-    a.counts = static_cast<int*>(ws);
-    a.stride = stride;
-    a.m = (int)m;
-    a.groups = (int)n_experts;
-    a.topk = (int)topk;
-    a.renorm = renorm != 0;
-    a.slots = (int)(m * topk);
+    const int rc = check_route(logits, logits_stride, ids, weights, offsets, order, n_experts,
+                               topk, renorm, m, ws, ws_bytes, &a);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
     return hip_status(q4k::launch_route(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -1326,22 +1400,14 @@ int q4k_f16_gemm_grouped(const void* w16, const void* x16, float* y, const int32
         return Q4K_ERR_NULL;
     }
     q4k::GroupRows g;
-    const int rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count,
+    int rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count,
                                     y_count, &g);
     if (rc != Q4K_OK) {
         return rc;
     }
-    if (k < 1 || k > kInt32Max) {
-        return Q4K_ERR_SHAPE;
-    }
-    if (k % 64 != 0) {
-        return Q4K_ERR_UNSUPPORTED;      // the k step of the tile
-    }
-    if (!fits_launch(q4k::f16_grouped_grid(rows, groups, n, k), 512)) {
-        return Q4K_ERR_SHAPE;
-    }
-    if (!aligned16(w16) || !aligned16(x16) || !aligned16(y)) {
-        return Q4K_ERR_ALIGN;
+    rc = f16_grouped_checks(w16, x16, y, k, q4k::f16_grouped_grid(rows, groups, n, k));
+    if (rc != Q4K_OK) {
+        return rc;
     }
     return hip_status(q4k::launch_f16_gemm_grouped(w16, x16, y, g, (int)n, (int)k,
                                                    static_cast<hipStream_t>(stream)));
@@ -1399,6 +1465,189 @@ int q4k_lora(const void* x, int x_type, const void* a, const void* b, const floa
     l.adapters = (int)adapters;
     l.rows = (int)rows;
     return hip_status(q4k::launch_lora(l, static_cast<hipStream_t>(stream)));
+}
+
+int q4k_gemv_act(const void* w, const float* x, const q4k_epilogue* epilogue, int64_t n, int64_t k,
+                 int64_t m, void* stream)
+{
+    q4k::EpArgs ep;
+    int rc = check_epilogue(epilogue, &ep);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    GemvPlan plan;
+    rc = gemv_plan(w, x, some_y(ep), n, k, m, nullptr, &plan);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    size_t lds_max = 0;
+    rc = device_lds_max(&lds_max);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    // the sums meet in LDS (in f64) before the epilogue; kernels that put them
+    // there to add up their parts have the room, others need it unless it does
+    // not fit
+    const bool whole = plan.kernel == 2   ? plan.nspans == 1
+                       : plan.kernel >= 3 ? (plan.S + 7) / 8 * 8 == plan.cols_per_task
+                                          : false;
+    const size_t sums = (size_t)plan.rows_per_block * plan.m * 8;
+    ep.parked = plan.kernel >= 2 && (!whole || plan.lds_bytes + sums <= lds_max);
+    if (whole && ep.parked) {
+        plan.lds_bytes += sums;
+    }
+    return hip_status(q4k::launch_gemv(plan, w, x, ep, static_cast<hipStream_t>(stream)));
+}
+
+int q4k_f16_gemm_act(const void* w16, const void* x16, const q4k_epilogue* epilogue, int64_t m,
+                     int64_t n, int64_t k, void* stream)
+{
+    q4k::EpArgs ep;
+    int rc = check_epilogue(epilogue, &ep);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    rc = f16_gemm_checks(w16, x16, some_y(ep), m, n, k);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    if (!fits_launch(q4k::f16_act_grid(m, n, k), 512)) {
+        return Q4K_ERR_SHAPE;
+    }
+    return hip_status(q4k::launch_f16_gemm_act(w16, x16, ep, (int)m, (int)n, (int)k,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int q4k_gemv_grouped_act(const void* w, const float* x, const q4k_epilogue* epilogue,
+                         const int32_t* offsets, const int32_t* x_rows, const int32_t* y_rows,
+                         int64_t n, int64_t k, int64_t groups, int64_t rows, int64_t x_div,
+                         int64_t x_count, int64_t y_count, void* ws, size_t ws_bytes,
+                         void* stream)
+{
+    if (!w || !x || !ws) {
+        return Q4K_ERR_NULL;
+    }
+    q4k::EpArgs ep;
+    int rc = check_epilogue(epilogue, &ep);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    q4k::GroupRows g;
+    rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count, y_count, &g);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    return gemv_grouped_checked(w, x, nullptr, nullptr, nullptr, g, n, k, ws, ws_bytes, stream,
+                                &ep);
+}
+
+int q4k_f16_gemm_grouped_act(const void* w16, const void* x16, const q4k_epilogue* epilogue,
+                             const int32_t* offsets, const int32_t* x_rows,
+                             const int32_t* y_rows, int64_t n, int64_t k, int64_t groups,
+                             int64_t rows, int64_t x_div, int64_t x_count, int64_t y_count,
+                             void* stream)
+{
+    if (!w16 || !x16) {
+        return Q4K_ERR_NULL;
+    }
+    q4k::EpArgs ep;
+    int rc = check_epilogue(epilogue, &ep);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    q4k::GroupRows g;
+    rc = check_group_rows(offsets, x_rows, y_rows, n, groups, rows, x_div, x_count, y_count, &g);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    rc = f16_grouped_checks(w16, x16, nullptr, k, q4k::f16_grouped_act_grid(rows, groups, n, k));
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    return hip_status(q4k::launch_f16_grouped_act(w16, x16, ep, g, (int)n, (int)k,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+int q4k_block_norm(const void* x, int x_type, int64_t x_stride, int kind,
+                   const float* post_weight, const float* post_bias, const float* gate,
+                   int64_t gate_stride, float scale, const float* residual, float* sum_out,
+                   const float* weight, const float* bias, float* y, void* y16, int8_t* q,
+                   float* d, int64_t k, int64_t m, float eps, void* stream)
+{
+    const bool normed = y || y16 || q;
+    if (!x || (!sum_out && !normed) || (normed && !weight) || (q == nullptr) != (d == nullptr)) {
+        return Q4K_ERR_NULL;
+    }
+    const int64_t stride = x_stride == 0 ? k : x_stride;
+    constexpr int64_t kMaxStride = (int64_t)1 << 40;
+    if (!in_range(m, 1, kMaxRows) || k < 1 || k > kInt32Max || stride < k || stride > kMaxStride ||
+        (gate && gate_stride != 0 && !in_range(gate_stride, k, kMaxStride)) ||
+        (q && k % 32 != 0) || !(eps >= 0.f) || !__builtin_isfinite(eps) ||
+        !__builtin_isfinite(scale) ||
+        !fits_launch(m, k > 8192 ? 1024 : (k / 8 + 64) / 64 * 64)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (!known_type(x_type) || (kind != Q4K_NORM_RMS && kind != Q4K_NORM_LAYER)) {
+        return Q4K_ERR_UNSUPPORTED;
+    }
+    if (!aligned16(x) || !aligned16(post_weight) || !aligned16(post_bias) || !aligned16(gate) ||
+        !aligned16(residual) || !aligned16(sum_out) || !aligned16(weight) || !aligned16(bias) ||
+        !aligned16(y) || !aligned16(y16) || !aligned16(q) || !aligned16(d)) {
+        return Q4K_ERR_ALIGN;
+    }
+    q4k::BlockNormArgs a;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.sum = sum_out;
+    a.y = y;
+    a.y16 = y16;
+    a.q = q;
+    a.d = d;
+    a.x_stride = stride;
+    a.x_type = x_type;
+    a.k = (int)k;
+    a.m = (int)m;
+    a.eps = eps;
+    a.bias = bias;
+    a.post_weight = post_weight;
+    a.post_bias = post_bias;
+    a.gate = gate;
+    a.gate_stride = gate_stride;
+    a.scale = scale;
+    a.layer = kind == Q4K_NORM_LAYER;
+    return hip_status(q4k::launch_block_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+int q4k_moe_route_biased(const float* logits, int64_t logits_stride, const float* bias, int score,
+                         int64_t expert_groups, int64_t topk_groups, int32_t* ids,
+                         float* weights, int32_t* offsets, int32_t* order, int64_t n_experts,
+                         int64_t topk, int renorm, float scale, int64_t m, void* ws,
+                         size_t ws_bytes, void* stream)
+{
+    q4k::BiasedRouteArgs a = {};
+    const int rc = check_route(logits, logits_stride, ids, weights, offsets, order, n_experts,
+                               topk, renorm, m, ws, ws_bytes, &a);
+    if (rc != Q4K_OK) {
+        return rc;
+    }
+    if (!in_range(expert_groups, 1, q4k::kMaxExpertGroups) ||
+        !in_range(topk_groups, 1, expert_groups) || n_experts % expert_groups != 0 ||
+        topk > n_experts / expert_groups * topk_groups || !__builtin_isfinite(scale)) {
+        return Q4K_ERR_SHAPE;
+    }
+    if (score != Q4K_SCORE_SOFTMAX && score != Q4K_SCORE_SIGMOID) {
+        return Q4K_ERR_UNSUPPORTED;
+    }
+    if (!aligned16(bias)) {
+        return Q4K_ERR_ALIGN;
+    }
+    a.bias = bias;
+    a.sigmoid = score == Q4K_SCORE_SIGMOID;
+    a.parts = (int)expert_groups;
+    a.keep = (int)topk_groups;
+    a.scale = scale;
+    return hip_status(q4k::launch_route(a, static_cast<hipStream_t>(stream)));
 }
 
 const char* q4k_status_string(int rc)

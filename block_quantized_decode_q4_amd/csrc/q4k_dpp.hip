@@ -48,6 +48,7 @@
 
 #include "q4k_device.h"
 #include "q4k_kernels.h"
+#include "q4k_out.h"
 #include "q4k_lines.h"
 #include "q4k_xrep.h"
 
@@ -136,7 +137,7 @@ __device__ __forceinline__ void convert_group_dot(const float4 (&v)[4], int G, b
 template <int NW, int P, int XC, bool ANY, bool ONEBODY = false>
 __global__ void __launch_bounds__(NW * 64)
 gemv_dot4_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
-                       float* __restrict__ y, int n, int S, int rows_per_block, int slabs_per_task)
+                       Out y, int n, int S, int rows_per_block, int slabs_per_task)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x;
@@ -247,8 +248,8 @@ gemv_dot4_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
         v += __shfl_xor(v, 16, 64);
         v += __shfl_xor(v, 32, 64);
         if (g == 0 && r < rows_here) {
-            if (ncg == 1) {
-                y[row0 + r] = (float)v;
+            if (ncg == 1 && !parked(y)) {
+                put_y(y, row0 + r, row0 + r, v);
             } else {
                 ypart[(task % ncg) * rows_per_block + r] = v;
             }
@@ -295,20 +296,20 @@ gemv_dot4_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
             slab_flag);
     }
 
-    if (ncg > 1) {
+    if (ncg > 1 || parked(y)) {
         __syncthreads();
         for (int i = tid; i < rows_here; i += NW * 64) {
             double a = 0.0;
             for (int cg = 0; cg < ncg; ++cg) {
                 a += ypart[cg * rows_per_block + i];
             }
-            y[row0 + i] = (float)a;
+            put_y(y, row0 + i, row0 + i, a);
         }
     }
 }
 
 template <int NW, int P, int XC>
-static hipError_t launch_dot4_x(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_dot4_x(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                 hipStream_t stream)
 {
     if constexpr (P == 3) {
@@ -339,7 +340,7 @@ static hipError_t launch_dot4_x(const GemvPlan& p, const uint8_t* w, const float
 // XC: groups of 16 x values each thread converts, the power of two covering
 // S * 16 / (64 NW), at most 4 (k <= 16384 per 64 NW lanes)
 template <int NW, int P>
-static hipError_t launch_dot4_p(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_dot4_p(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                 hipStream_t stream)
 {
     const int per = (p.S * 16 + NW * 64 - 1) / (NW * 64);
@@ -350,27 +351,30 @@ static hipError_t launch_dot4_p(const GemvPlan& p, const uint8_t* w, const float
 }
 
 template <int NW>
-static hipError_t launch_dot4_w(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_dot4_w(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                 hipStream_t stream)
 {
-    if (p.ring_depth == 9) return launch_dot4_p<NW, 9>(p, w, x, y, stream);
+    if constexpr (!kEpilogue) {        // asked for only, as are four waves below
+        if (p.ring_depth == 9) return launch_dot4_p<NW, 9>(p, w, x, y, stream);
+    }
     return launch_dot4_p<NW, 3>(p, w, x, y, stream);
 }
 
-hipError_t launch_gemv_dot4(const GemvPlan& p, const void* w, const float* x, float* y,
+hipError_t launch_gemv_dot4(const GemvPlan& p, const void* w, const float* x, Out y,
                             hipStream_t stream)
 {
     const uint8_t* wb = static_cast<const uint8_t*>(w);
-    switch (p.waves_per_block) {
-    case 4: return launch_dot4_w<4>(p, wb, x, y, stream);
-    case 8: return launch_dot4_w<8>(p, wb, x, y, stream);
-    default: return hipErrorInvalidValue;
+    if constexpr (!kEpilogue) {
+        if (p.waves_per_block == 4) return launch_dot4_w<4>(p, wb, x, y, stream);
     }
+    return p.waves_per_block == 8 ? launch_dot4_w<8>(p, wb, x, y, stream) : hipErrorInvalidValue;
 }
 
+#ifndef Q4K_EPILOGUE
 size_t dot4_lds_bytes(int S, int waves)
 {
     return (size_t)S * kDotCol + (size_t)waves * (S % 8 != 0 ? kRing4Wave : kRingWave);
 }
+#endif  // Q4K_EPILOGUE
 
 }  // namespace q4k

@@ -1,0 +1,83 @@
+// q4k_epilogue.h -- what a product's sum z (its bias added) goes through:
+//   y = act(z) gate + residual
+// in f32, each step rounded once (the last two may be one fused step), y16 the
+// nearest binary16 of that y.  Internal.
+//
+// The activations, each without cancellation for negative z:
+//   silu        z / (1 + e^-z)
+//   gelu        z/2 erfc(-z / sqrt 2)
+//   gelu, tanh  z/2 (1 + tanh u) = z / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3)
+//   sigmoid     1 / (1 + e^-z)
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q4k_kernels.h"
+
+namespace q4k {
+
+// enum q4k_act of include/q4k.h
+constexpr int kActNone = 0;
+constexpr int kActRelu = 1;
+constexpr int kActSilu = 2;
+constexpr int kActGelu = 3;
+constexpr int kActGeluTanh = 4;
+constexpr int kActSigmoid = 5;
+
+template <int ACT>
+__device__ __forceinline__ float activated(float z)
+{
+    if constexpr (ACT == kActRelu) {
+        return z < 0.f ? 0.f : z;              // a NaN stays one
+    } else if constexpr (ACT == kActSilu) {
+        return z / (1.f + expf(-z));
+    } else if constexpr (ACT == kActGelu) {
+        return 0.5f * z * erfcf(z * -0.707106781f);
+    } else if constexpr (ACT == kActGeluTanh) {
+        const float u2 = 1.59576912f * (z + 0.044715f * z * z * z);
+        return z / (1.f + expf(-u2));
+    } else if constexpr (ACT == kActSigmoid) {
+        return 1.f / (1.f + expf(-z));
+    } else {
+        return z;
+    }
+}
+
+__device__ __forceinline__ float activated(int act, float z)
+{
+    switch (act) {                             // the same for the whole launch
+    case kActRelu: return activated<kActRelu>(z);
+    case kActSilu: return activated<kActSilu>(z);
+    case kActGelu: return activated<kActGelu>(z);
+    case kActGeluTanh: return activated<kActGeluTanh>(z);
+    case kActSigmoid: return activated<kActSigmoid>(z);
+    default: return z;
+    }
+}
+
+// y of element `at` from its z
+__device__ __forceinline__ float ep_value(const EpArgs& e, int64_t at, float z)
+{
+    float v = activated(e.act, z);
+    if (e.gate != nullptr) {
+        v *= e.gate_type == kTypeF16 ? (float)static_cast<const _Float16*>(e.gate)[at]
+                                     : static_cast<const float*>(e.gate)[at];
+    }
+    if (e.residual != nullptr) {
+        v += e.residual[at];
+    }
+    return v;
+}
+
+__device__ __forceinline__ void ep_store(const EpArgs& e, int64_t at, float v)
+{
+    if (e.y != nullptr) {
+        e.y[at] = v;
+    }
+    if (e.y16 != nullptr) {
+        static_cast<_Float16*>(e.y16)[at] = (_Float16)v;
+    }
+}
+
+}  // namespace q4k

@@ -55,6 +55,7 @@
 #include "q4k_device.h"
 #include "q4k_groups.h"
 #include "q4k_kernels.h"
+#include "q4k_out.h"
 
 namespace q4k {
 
@@ -386,7 +387,7 @@ template <int T, int FUSED>
 constexpr int kXLds = FUSED == kXLaidOut ? 0 : kFused<T> * kXsb;    // per wave
 
 template <int T, int FUSED>
-__device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupTiles& tiles,
+__device__ __forceinline__ void grouped_tiles(const GroupedOut& a, const GroupTiles& tiles,
                                               int row_blocks, int kw_log2, unsigned char* smem)
 {
     constexpr int kLds = kWaveLds<T> + kXLds<T, FUSED>;
@@ -625,15 +626,16 @@ __device__ __forceinline__ void grouped_tiles(const GroupedArgs& a, const GroupT
             sum = z == 0 ? one : sum + one;
         }
         const int scales[4] = {least.x, least.y, least.z, least.w};
-        const int row =
-            min((work.block * (kWaves >> kw_log2) + rg) * rows_per_group + 16 * i, last) + j;
+        const int tile_row = (work.block * (kWaves >> kw_log2) + rg) * rows_per_group + 16 * i;
+        const int row = min(tile_row, last) + j;
         // D[4 g + e][j]: position 4 g + e, weight row j
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int yrow = __shfl(yr, 4 * g + e, 64);
             const int exp = FUSED == kXLaidOut ? __shfl(exps, 4 * g + e, 64) : scales[e];
-            if (row < a.n && yrow >= 0) {
-                a.y[(int64_t)yrow * a.n + row] = ldexpf(sum[e], -exp);
+            // with an epilogue once: y may be its residual or gate
+            if (row < a.n && yrow >= 0 && (!kEpilogue || row >= tile_row)) {
+                put_grouped(a, work.tile.group, yrow, row, ldexpf(sum[e], -exp));
             }
         }
     }
@@ -643,7 +645,7 @@ constexpr int kCus = 256;
 
 template <int T, int FUSED>
 __global__ void __launch_bounds__(64 * kWaves, FUSED == kXLaidOut ? 3 : 2)
-grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
+grouped_kernel(GroupedOut a, int row_blocks, int kw_log2)
 {
     __shared__ __align__(16) unsigned char smem[kWaves * (kWaveLds<T> + kXLds<T, FUSED>)];
     const GroupTiles t =
@@ -657,7 +659,7 @@ grouped_kernel(GroupedArgs a, int row_blocks, int kw_log2)
 // leaves much of its last round empty: ten tiles of 4096 x 14336, 320 workgroups
 // at T = 8, 105 us against 96 us; eight tiles, 256 workgroups, 78 us against 87 us.
 __global__ void __launch_bounds__(64 * kWaves, 3)
-grouped_either_kernel(GroupedArgs a, int row_blocks, int fine_blocks, int kw_log2)
+grouped_either_kernel(GroupedOut a, int row_blocks, int fine_blocks, int kw_log2)
 {
     __shared__ __align__(16) unsigned char smem[kWaves * kWaveLds<8>];
     const GroupTiles t =
@@ -721,6 +723,7 @@ GroupedCut grouped_cut(int64_t rows, int64_t groups, int64_t n, int64_t k)
 
 }  // namespace
 
+#ifndef Q4K_EPILOGUE
 size_t grouped_ws_bytes(int64_t k, int64_t rows)
 {
     return (size_t)rows * (size_t)(k / kQK) * kXsb + (size_t)rows * sizeof(int);
@@ -731,8 +734,9 @@ int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k)
 {
     return grouped_cut(rows, groups, n, k).grid;
 }
+#endif  // Q4K_EPILOGUE
 
-hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream)
+hipError_t launch_grouped(const GroupedOut& a, hipStream_t stream)
 {
     const GroupedCut c = grouped_cut(a.g.rows, a.g.groups, a.n, a.k);
     const dim3 grid((unsigned)c.grid), block(64 * kWaves);

@@ -40,8 +40,30 @@ struct GemvPlan {
     int cols_per_task;     // line-streamed kernels: superblock columns per task
 };
 
+// What a product's sums go through on their way out (q4k_epilogue of
+// include/q4k.h): y = act(sum + bias) gate + residual; any pointer but one of y
+// and y16 may be null.
+struct EpArgs {
+    const float* bias;     // by weight row (grouped: by matrix and row)
+    const void* gate;      // where y is, of gate_type
+    const float* residual;
+    float* y;
+    void* y16;
+    int gate_type;         // kTypeF32 or kTypeF16
+    int act;               // enum q4k_act
+    int parked;            // GEMV: a workgroup's sums meet in LDS before they go out
+};
+
+// The launches with an EpArgs in y's place are the same kernels, compiled with the
+// epilogue (q4k_out.h).
 hipError_t launch_gemv(const GemvPlan& p, const void* w, const float* x, float* y,
                        hipStream_t stream);
+hipError_t launch_gemv(const GemvPlan& p, const void* w, const float* x, EpArgs y,
+                       hipStream_t stream);
+hipError_t launch_gemv_mfma(const GemvPlan& p, const void* w, const float* x, EpArgs y,
+                            hipStream_t stream);
+hipError_t launch_gemv_dot4(const GemvPlan& p, const void* w, const float* x, EpArgs y,
+                            hipStream_t stream);
 hipError_t launch_gemv_mfma(const GemvPlan& p, const void* w, const float* x, float* y,
                             hipStream_t stream);
 size_t lines_lds_bytes(int S, int m, int waves);
@@ -120,6 +142,19 @@ struct NormArgs {
 };
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
 
+// The norms on both sides of a residual's addition; any output may be null, and
+// weight where there is no output but sum.
+struct BlockNormArgs : NormArgs {
+    const float* bias;
+    const float* post_weight;          // null: no norm of x
+    const float* post_bias;
+    const float* gate;
+    int64_t gate_stride;               // 0: one row of gate for all
+    float scale;
+    int layer;                         // layer norms, else root-mean-square
+};
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
+
 // Routing and grouping (q4k_moe.hip).  logits null: the ids are given.
 constexpr int kFewSlots = 192;         // slots that one workgroup groups in one launch
 constexpr int kMaxGroups = 1024;       // experts (ids) that routing and grouping take
@@ -138,6 +173,14 @@ struct RouteArgs {
     int slots;                         // m * topk
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+constexpr int kMaxExpertGroups = 64;
+struct BiasedRouteArgs : RouteArgs {
+    const float* bias;                 // may be null
+    int sigmoid;                       // scores: sigmoid, else softmax
+    int parts, keep;                   // groups of experts, and how many stay
+    float scale;
+};
+hipError_t launch_route(const BiasedRouteArgs& a, hipStream_t stream);
 constexpr int kRowExperts = 256;       // experts that 16 lanes route
 bool group_in_one(int64_t slots, int64_t groups, int64_t topk, bool route);
 size_t group_ws_bytes(int64_t slots, int64_t groups, int64_t topk, bool route);
@@ -178,6 +221,10 @@ struct GroupedArgs {
     int n, k;
 };
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
+struct GroupedActArgs : GroupedArgs {  // y is not used
+    EpArgs ep;
+};
+hipError_t launch_grouped(const GroupedActArgs& a, hipStream_t stream);
 size_t grouped_ws_bytes(int64_t k, int64_t rows);
 int64_t grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k);
 constexpr int64_t kMaxGroupedK = (int64_t)1 << 24;   // 16 rows within 32-bit offsets
@@ -186,6 +233,14 @@ constexpr int64_t kMaxGroupedK = (int64_t)1 << 24;   // 16 rows within 32-bit of
 hipError_t launch_f16_gemm_grouped(const void* w16, const void* x16, float* y, const GroupRows& g,
                                    int n, int k, hipStream_t stream);
 int64_t f16_grouped_grid(int64_t rows, int64_t groups, int64_t n, int64_t k);
+
+// Products on the fp16 mirror with an epilogue (q4k_f16_act.hip).
+hipError_t launch_f16_gemm_act(const void* w16, const void* x16, const EpArgs& ep, int m, int n,
+                               int k, hipStream_t stream);
+int64_t f16_act_grid(int64_t m, int64_t n, int64_t k);
+hipError_t launch_f16_grouped_act(const void* w16, const void* x16, const EpArgs& ep,
+                                  const GroupRows& g, int n, int k, hipStream_t stream);
+int64_t f16_grouped_act_grid(int64_t rows, int64_t groups, int64_t n, int64_t k);
 
 // Low-rank adapters (q4k_lora.hip).
 struct LoraArgs {

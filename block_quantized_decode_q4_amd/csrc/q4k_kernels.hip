@@ -46,6 +46,7 @@
 
 #include "q4k_device.h"
 #include "q4k_kernels.h"
+#include "q4k_out.h"
 
 namespace q4k {
 
@@ -94,7 +95,7 @@ __device__ __forceinline__ void stage_x(const float* __restrict__ x, int k, int 
 // ---------------------------------------------------------------- GEMV
 template <int M, int R, int NW, bool XREG>
 __global__ void __launch_bounds__(NW * 64)
-gemv_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x, float* __restrict__ y,
+gemv_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x, Out y,
             int n, int k, int S, int rows_per_block, int spans_per_chunk)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -217,7 +218,7 @@ gemv_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x, float* _
                         const double v = wave_sum(acc[i][b]);
                         const int rl = g * R + i;
                         if (lane == 0 && rl < rows_here) {
-                            y[(size_t)b * n + row0 + rl] = (float)v;
+                            put_y(y, (size_t)b * n + row0 + rl, row0 + rl, v);
                         }
                     }
                 }
@@ -356,7 +357,7 @@ __device__ __forceinline__ double row_partial(const RowData& q, const X4D* xr,
 template <int NW, int P>
 __global__ void __launch_bounds__(NW * 64)
 gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
-                   float* __restrict__ y, int n, int k, int S, int rows_per_block,
+                   Out y, int n, int k, int S, int rows_per_block,
                    int rows_per_task, int spans_per_chunk)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -428,9 +429,9 @@ gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             // y (global) or the per-span row sums (LDS): two typed pointers, so
             // that neither store becomes a flat access, which would make the
             // compiler drain the prefetched loads at every row
-            float* yout = y + row0 + rb;
+            float* yout = direct_y(y) + row0 + rb;
             double* pout = ypart + span * rows_per_block + rb;
-            const bool direct = nspans == 1;
+            const bool direct = nspans == 1 && !parked(y);
             int t = 0;
             for (; t + P <= T; t += P) {
 #pragma unroll
@@ -462,18 +463,19 @@ gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             }
         }
     }
-    if (nspans > 1) {
+    if (nspans > 1 || parked(y)) {
         __syncthreads();
         for (int r = tid; r < rows_here; r += NW * 64) {
             double acc = 0.0;
             for (int sp = 0; sp < nspans; ++sp) {
                 acc += ypart[sp * rows_per_block + r];
             }
-            y[row0 + r] = (float)acc;
+            put_y(y, row0 + r, row0 + r, acc);
         }
     }
 }
 
+#ifndef Q4K_EPILOGUE
 // ------------------------------------------------------------- dequant
 // One thread per (superblock, chunk c, dword u): decodes 8 weights and
 // writes them as two groups of four (f32, or the fp16 mirror: the f32
@@ -575,9 +577,11 @@ read_kernel(const u32x4_t* __restrict__ buf, size_t n16, float* __restrict__ out
     }
 }
 
+#endif  // Q4K_EPILOGUE
+
 // -------------------------------------------------------------- launch
 template <int M, int R, int NW, bool XREG>
-static hipError_t launch_one(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_one(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                              hipStream_t stream)
 {
     hipLaunchKernelGGL((gemv_kernel<M, R, NW, XREG>), dim3(p.grid), dim3(NW * 64), p.lds_bytes,
@@ -586,7 +590,7 @@ static hipError_t launch_one(const GemvPlan& p, const uint8_t* w, const float* x
 }
 
 template <int M>
-static hipError_t launch_m(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_m(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                            hipStream_t stream)
 {
     if constexpr (M == 1) {
@@ -619,7 +623,7 @@ static hipError_t launch_m(const GemvPlan& p, const uint8_t* w, const float* x, 
 }
 
 template <int NW, int P>
-static hipError_t launch_stream(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_stream(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                 hipStream_t stream)
 {
     hipLaunchKernelGGL((gemv_stream_kernel<NW, P>), dim3(p.grid), dim3(NW * 64), p.lds_bytes,
@@ -629,7 +633,7 @@ static hipError_t launch_stream(const GemvPlan& p, const uint8_t* w, const float
 }
 
 template <int NW>
-static hipError_t launch_stream_nw(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_stream_nw(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                    hipStream_t stream)
 {
     if (p.ring_depth == 1) return launch_stream<NW, 1>(p, w, x, y, stream);
@@ -638,7 +642,7 @@ static hipError_t launch_stream_nw(const GemvPlan& p, const uint8_t* w, const fl
     return launch_stream<NW, 4>(p, w, x, y, stream);
 }
 
-hipError_t launch_gemv(const GemvPlan& p, const void* w, const float* x, float* y,
+hipError_t launch_gemv(const GemvPlan& p, const void* w, const float* x, Out y,
                        hipStream_t stream)
 {
     const uint8_t* wb = static_cast<const uint8_t*>(w);
@@ -665,6 +669,7 @@ hipError_t launch_gemv(const GemvPlan& p, const void* w, const float* x, float* 
     }
 }
 
+#ifndef Q4K_EPILOGUE
 hipError_t launch_dequant(const void* w, float* out, int64_t nsb, hipStream_t stream)
 {
     const int64_t threads = nsb * 32;
@@ -689,5 +694,6 @@ hipError_t launch_read(const void* buf, size_t n16, float* out, hipStream_t stre
                        static_cast<const u32x4_t*>(buf), n16, out);
     return hipGetLastError();
 }
+#endif  // Q4K_EPILOGUE
 
 }  // namespace q4k

@@ -23,6 +23,7 @@
 
 #include "q4k_device.h"
 #include "q4k_kernels.h"
+#include "q4k_out.h"
 #include "q4k_lines.h"
 #include "q4k_xrep.h"
 
@@ -127,7 +128,7 @@ __device__ __forceinline__ void load_x_quarter(const float* __restrict__ x, int 
 template <int NW, int P, int XC, int M>
 __global__ void __launch_bounds__(NW * 64)
 gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
-                     float* __restrict__ y, int n, int S, int rows_per_block, int slabs_per_task)
+                     Out y, int n, int S, int rows_per_block, int slabs_per_task)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x;
@@ -243,8 +244,8 @@ gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             v += __shfl_xor(v, 16, 64);
             v += __shfl_xor(v, 32, 64);
             if (g == 0 && r < rows_here) {
-                if (ncg == 1) {
-                    y[(size_t)b * n + row0 + r] = (float)v;
+                if (ncg == 1 && !parked(y)) {
+                    put_y(y, (size_t)b * n + row0 + r, row0 + r, v);
                 } else {
                     ypart[(b * ncg + task % ncg) * rows_per_block + r] = v;
                 }
@@ -255,7 +256,7 @@ gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
     line_stream<NW, P>(w, x, n, S, rows_per_block, slabs_per_task, ring, issue_x, convert_x, step,
                        task_end, slab_flag);
 
-    if (ncg > 1) {
+    if (ncg > 1 || parked(y)) {
         __syncthreads();
         for (int i = tid; i < rows_here * M; i += NW * 64) {
             const int b = i / rows_here;
@@ -264,7 +265,7 @@ gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             for (int cg = 0; cg < ncg; ++cg) {
                 a += ypart[(b * ncg + cg) * rows_per_block + r];
             }
-            y[(size_t)b * n + row0 + r] = (float)a;
+            put_y(y, (size_t)b * n + row0 + r, row0 + r, a);
         }
     }
 }
@@ -549,7 +550,7 @@ constexpr int kWinAhead = 2;
 template <int NW, int XC, int NQ, int MODE, bool ANY>
 __global__ void __launch_bounds__(NW * 64)
 gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
-                   float* __restrict__ y, int n, int S, int m, int rows_per_block,
+                   Out y, int n, int S, int m, int rows_per_block,
                    int slabs_per_task)
 {
     static_assert(MODE != kModeWindow || !ANY, "the window needs whole slabs");
@@ -908,8 +909,8 @@ gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             }
             const int b = b4 + g;
             if (b < m && r < rows_here) {
-                if (ncg == 1) {
-                    y[(size_t)b * n + row0 + r] = (float)acc.at<q>();
+                if (ncg == 1 && !parked(y)) {
+                    put_y(y, (size_t)b * n + row0 + r, row0 + r, acc.at<q>());
                 } else {
                     ypart[(b * ncg + task % ncg) * rows_per_block + r] = acc.at<q>();
                 }
@@ -947,7 +948,7 @@ gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
                            step, task_end, slab_flag);
     }
 
-    if (ncg > 1) {
+    if (ncg > 1 || parked(y)) {
         __syncthreads();
         for (int i = tid; i < rows_here * m; i += NW * 64) {
             const int b = i / rows_here;
@@ -956,13 +957,13 @@ gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             for (int cg = 0; cg < ncg; ++cg) {
                 a += ypart[(b * ncg + cg) * rows_per_block + r];
             }
-            y[(size_t)b * n + row0 + r] = (float)a;
+            put_y(y, (size_t)b * n + row0 + r, row0 + r, a);
         }
     }
 }
 
 template <int XC, int NQ, int MODE = kModeStaged, int NW = 8>
-static hipError_t launch_sub_x(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_sub_x(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                hipStream_t stream)
 {
     if (p.waves_per_block != NW) {
@@ -995,7 +996,7 @@ static hipError_t launch_sub_x(const GemvPlan& p, const uint8_t* w, const float*
 // (column, quad) groups each of the eight waves converts before the first
 // barrier: the power of two covering S * NQ / 8, at most 4
 template <int NQ>
-static hipError_t launch_sub(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_sub(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                              hipStream_t stream)
 {
     const int per = (p.S * NQ + 7) / 8;
@@ -1005,7 +1006,7 @@ static hipError_t launch_sub(const GemvPlan& p, const uint8_t* w, const float* x
 }
 
 template <int NW, int P, int XC, int M>
-static hipError_t launch_lines_x(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_lines_x(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                  hipStream_t stream)
 {
     hipLaunchKernelGGL((gemv_i8_lines_kernel<NW, P, XC, M>), dim3(p.grid), dim3(NW * 64),
@@ -1018,7 +1019,7 @@ static hipError_t launch_lines_x(const GemvPlan& p, const uint8_t* w, const floa
 // first barrier: the power of two covering S * m / (4 NW), at most 4 (the
 // rest follow in a loop)
 template <int NW, int P>
-static hipError_t launch_lines_p(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_lines_p(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                  hipStream_t stream)
 {
     const int per = (p.S + 4 * NW - 1) / (4 * NW);
@@ -1028,7 +1029,7 @@ static hipError_t launch_lines_p(const GemvPlan& p, const uint8_t* w, const floa
 }
 
 template <int NW>
-static hipError_t launch_lines(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_lines(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                hipStream_t stream)
 {
     if (p.ring_depth == 9) return launch_lines_p<NW, 9>(p, w, x, y, stream);
@@ -1037,7 +1038,7 @@ static hipError_t launch_lines(const GemvPlan& p, const uint8_t* w, const float*
 
 // several vectors: eight waves, three lines in flight
 template <int M>
-static hipError_t launch_lines_m(const GemvPlan& p, const uint8_t* w, const float* x, float* y,
+static hipError_t launch_lines_m(const GemvPlan& p, const uint8_t* w, const float* x, Out y,
                                  hipStream_t stream)
 {
     const int per = (p.S * M + 31) / 32;
@@ -1052,7 +1053,7 @@ static int sub_quads(int m)
     return m > kMaxMStaged ? 8 : m > 8 ? 4 : m > 4 ? 2 : 1;
 }
 
-hipError_t launch_gemv_mfma(const GemvPlan& p, const void* w, const float* x, float* y,
+hipError_t launch_gemv_mfma(const GemvPlan& p, const void* w, const float* x, Out y,
                             hipStream_t stream)
 {
     const uint8_t* wb = static_cast<const uint8_t*>(w);
@@ -1085,10 +1086,15 @@ hipError_t launch_gemv_mfma(const GemvPlan& p, const void* w, const float* x, fl
     if (p.m != 1) {
         return hipErrorInvalidValue;   // one MFMA group per vector: one or two vectors
     }
-    if (p.waves_per_block == 8) return launch_lines<8>(p, wb, x, y, stream);
-    return launch_lines<4>(p, wb, x, y, stream);
+    if constexpr (kEpilogue) {
+        return hipErrorInvalidValue;   // one vector: never the automatic choice
+    } else {
+        if (p.waves_per_block == 8) return launch_lines<8>(p, wb, x, y, stream);
+        return launch_lines<4>(p, wb, x, y, stream);
+    }
 }
 
+#ifndef Q4K_EPILOGUE
 size_t sub_lds_bytes(int S, int m)
 {
     const int nq = sub_quads(m);
@@ -1117,5 +1123,6 @@ size_t lines_lds_bytes(int S, int m, int waves)
 {
     return (size_t)(S * m + 1) * kK4Pair + (size_t)waves * kRingWave;
 }
+#endif  // Q4K_EPILOGUE
 
 }  // namespace q4k

@@ -151,7 +151,8 @@ template <int LANES>
 constexpr int kChoices = LANES < kMaxTopk ? kMaxTopk / LANES : 1;
 
 template <int LANES, int NL>
-__device__ __forceinline__ void route_tokens(const RouteArgs& a, float* l, int* id, float* weight)
+__device__ __forceinline__ void route_tokens(const RouteArgs& a, int64_t, float* l, int* id,
+                                             float* weight)
 {
     constexpr int C = kChoices<LANES>;
     const int i0 = threadIdx.x & (LANES - 1);
@@ -224,11 +225,197 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, float* l, int* 
     }
 }
 
+// ------------------------------------------------------ choice by biased scores
+// s = softmax(l) or sigmoid(l), c = s + bias.  With groups of experts (`parts`
+// consecutive ones of the same size) a group's value is the sum of its two largest
+// c, and the experts of the `keep` largest groups stay.  The topk largest c are
+// chosen, their weights are scale s, or scale s / sum of the chosen s.  Scores,
+// sums and comparisons in f64, so that what is chosen does not hang on how an exp
+// was rounded to f32.
+constexpr double kNoValue = -__builtin_inf();
+
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(b >> 32));
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+template <int LANES, typename F>
+__device__ __forceinline__ double lanes_reduce(double v, F f)
+{
+    if constexpr (LANES == 16) {
+        v = f(v, dpp64<0x128>(v));
+        v = f(v, dpp64<0x124>(v));
+        v = f(v, dpp64<0x122>(v));
+        v = f(v, dpp64<0x121>(v));
+    } else {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            v = f(v, __shfl_xor(v, off, 64));
+        }
+    }
+    return v;
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_max(double v)     // no NaN
+{
+    return lanes_reduce<LANES>(v, [](double a, double b) { return a > b ? a : b; });
+}
+
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double v)
+{
+    return lanes_reduce<LANES>(v, [](double a, double b) { return a + b; });
+}
+
+// The value of a softmax whose largest logit is top: e^(l - top), 0 for a masked
+// one; where the largest are infinite they count 1 and the others 0
+__device__ __forceinline__ double softmax_part(float l, float top)
+{
+    return l == kNone ? 0.0 : l == top ? 1.0 : exp((double)l - (double)top);
+}
+
+template <int LANES, int NL>
+__device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t token, float* l,
+                                             int* id, float* weight)
+{
+    constexpr int C = kChoices<LANES>;
+    const int i0 = threadIdx.x & (LANES - 1);
+    float top = kNone;
+    double all = 1.0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        l[i] = l[i] == l[i] ? l[i] : kNone;
+    }
+    if (!a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            top = fmaxf(top, l[i]);
+        }
+        top = lanes_max<LANES>(top);
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            sum += softmax_part(l[i], top);
+        }
+        all = lanes_sum<LANES>(sum);
+    }
+    auto score = [&](float v) {
+        return a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : softmax_part(v, top) / all;
+    };
+    double c[NL];
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const int e = i * LANES + i0;
+        const float b = a.bias != nullptr && e < a.groups ? a.bias[e] : 0.f;
+        c[i] = l[i] == kNone || b != b || b == kNone ? kNoValue : score(l[i]) + (double)b;
+    }
+    if (a.keep < a.parts) {
+        const int each = a.groups / a.parts;
+        // group p's value in lane p % LANES, at p / LANES
+        constexpr int V = kMaxExpertGroups / LANES;
+        double value[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            value[v] = kNoValue;
+        }
+        for (int p = 0; p < a.parts; ++p) {
+            double first = kNoValue, second = kNoValue;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int e = i * LANES + i0;
+                const double x = e >= p * each && e < (p + 1) * each ? c[i] : kNoValue;
+                second = x > first ? first : x > second ? x : second;
+                first = x > first ? x : first;
+            }
+            const double best = lanes_max<LANES>(first);
+            const int holder = lanes_min<LANES>(first == best ? i0 : LANES);
+            const double next = lanes_max<LANES>(i0 == holder ? second : first);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (p == v * LANES + i0) {
+                    value[v] = next == kNoValue ? best : best + next;
+                }
+            }
+        }
+        uint64_t kept = 0;
+        for (int j = 0; j < a.keep; ++j) {
+            double best = kNoValue;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                best = value[v] > best ? value[v] : best;
+            }
+            best = lanes_max<LANES>(best);
+            int mine = 0x7fffffff;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) {
+                mine = value[v] == best && best != kNoValue ? v * LANES + i0 : mine;
+            }
+            const int chosen = lanes_min<LANES>(mine);
+            kept |= chosen < kMaxExpertGroups ? 1ull << chosen : 0ull;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                value[v] = chosen == v * LANES + i0 ? kNoValue : value[v];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = i * LANES + i0;
+            c[i] = e < a.groups && (kept >> (e / each) & 1) ? c[i] : kNoValue;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < C; ++v) {
+        id[v] = -1;
+    }
+    for (int j = 0; j < a.topk; ++j) {
+        double best = c[0];
+#pragma unroll
+        for (int i = 1; i < NL; ++i) {
+            best = c[i] > best ? c[i] : best;
+        }
+        best = lanes_max<LANES>(best);
+        if (__all(best == kNoValue)) {
+            break;                             // nothing left in any token
+        }
+        int mine = 0x7fffffff;
+#pragma unroll
+        for (int i = NL - 1; i >= 0; --i) {
+            mine = c[i] == best ? i * LANES + i0 : mine;
+        }
+        const int chosen = lanes_min<LANES>(mine);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            c[i] = i * LANES + i0 == chosen ? kNoValue : c[i];
+        }
+#pragma unroll
+        for (int v = 0; v < C; ++v) {
+            id[v] = j == v * LANES + i0 && best != kNoValue ? chosen : id[v];
+        }
+    }
+    // each lane scores its own choices again
+    double s[C], sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < C; ++v) {
+        s[v] = id[v] < 0 ? 0.0 : score(a.logits[token * a.stride + id[v]]);
+        sum += s[v];
+    }
+    sum = a.renorm ? lanes_sum<LANES>(sum) : 1.0;
+#pragma unroll
+    for (int v = 0; v < C; ++v) {
+        weight[v] = sum == 0.0 ? 0.f : (float)(s[v] / sum * (double)a.scale);
+    }
+}
+
 // Few slots: routing and grouping in one workgroup.  NL 0: the ids are given.
 // slots <= kFewSlots.
-template <int LANES, int NL>
+template <int LANES, int NL, typename Args>
 __global__ void __launch_bounds__(kPlaceThreads)
-group_few_kernel(RouteArgs a)
+group_few_kernel(Args a)
 {
     __shared__ __align__(16) int ids[kFewSlots];
     const int tid = threadIdx.x;
@@ -243,7 +430,7 @@ group_few_kernel(RouteArgs a)
             int id[kChoices<LANES>];
             float weight[kChoices<LANES>], l[NL];
             load_logits<LANES, NL>(a, t0, a.m, l);
-            route_tokens<LANES, NL>(a, l, id, weight);
+            route_tokens<LANES, NL>(a, t0 + lane / LANES, l, id, weight);
             const int t = t0 + lane / LANES;
 #pragma unroll
             for (int c = 0; c < kChoices<LANES>; ++c) {
@@ -291,9 +478,9 @@ group_few_kernel(RouteArgs a)
 
 // More slots: chunk c counts its slots per group into counts[c][0..groups).
 // With NL > 0 it routes the chunk's tokens first.
-template <int LANES, int NL>
+template <int LANES, int NL, typename Args>
 __global__ void __launch_bounds__(kCountThreads)
-group_count_kernel(RouteArgs a)
+group_count_kernel(Args a)
 {
     extern __shared__ int hist[];
     const int tid = threadIdx.x;
@@ -319,7 +506,7 @@ group_count_kernel(RouteArgs a)
                 l[i] = next[i];
             }
             load_logits<LANES, NL>(a, t0 + kPass, last, next);     // on the way
-            route_tokens<LANES, NL>(a, l, id, weight);
+            route_tokens<LANES, NL>(a, t0 + lane / LANES, l, id, weight);
             const int64_t t = t0 + lane / LANES;
 #pragma unroll
             for (int c = 0; c < kChoices<LANES>; ++c) {
@@ -561,12 +748,12 @@ size_t place_lds(int groups)
     return sizeof(int) * ((size_t)(kPlaceWaves + 1) * groups + 1 + 2 * kPlaceThreads);
 }
 
-template <int LANES, int NL>
-hipError_t launch_route_t(RouteArgs a, hipStream_t stream)
+template <int LANES, int NL, typename Args>
+hipError_t launch_route_t(Args a, hipStream_t stream)
 {
     if (group_in_one(a.slots, a.groups, a.topk, NL > 0)) {
-        hipLaunchKernelGGL((group_few_kernel<LANES, NL>), dim3(1), dim3(kPlaceThreads), 0, stream,
-                           a);
+        hipLaunchKernelGGL((group_few_kernel<LANES, NL, Args>), dim3(1), dim3(kPlaceThreads), 0,
+                           stream, a);
         return hipGetLastError();
     }
     a.chunk = chunk_slots(a.slots, a.topk);
@@ -574,7 +761,7 @@ hipError_t launch_route_t(RouteArgs a, hipStream_t stream)
     if (a.offsets == nullptr) {
         a.counts = nullptr;
     }
-    hipLaunchKernelGGL((group_count_kernel<LANES, NL>), dim3(a.chunks), dim3(kCountThreads),
+    hipLaunchKernelGGL((group_count_kernel<LANES, NL, Args>), dim3(a.chunks), dim3(kCountThreads),
                        sizeof(int) * a.groups, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.offsets == nullptr) {
@@ -619,11 +806,9 @@ size_t group_ws_most(int64_t slots, int64_t groups, int64_t topk)
     return sizeof(int) * (size_t)(chunks < kChunks ? chunks : kChunks) * (size_t)groups;
 }
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream)
+template <typename Args>
+static hipError_t launch_logits(const Args& a, hipStream_t stream)
 {
-    if (a.logits == nullptr) {
-        return launch_route_t<64, 0>(a, stream);
-    }
     if (a.groups <= 32) {
         return launch_route_t<16, 2>(a, stream);
     }
@@ -640,6 +825,16 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream)
         return launch_route_t<64, 8>(a, stream);
     }
     return launch_route_t<64, 16>(a, stream);
+}
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream)
+{
+    return a.logits == nullptr ? launch_route_t<64, 0>(a, stream) : launch_logits(a, stream);
+}
+
+hipError_t launch_route(const BiasedRouteArgs& a, hipStream_t stream)
+{
+    return launch_logits(a, stream);
 }
 
 hipError_t launch_combine(CombineArgs a, hipStream_t stream)

@@ -134,25 +134,26 @@ __device__ __forceinline__ void put_f32(const NormArgs& a, float* base, int64_t 
     }
 }
 
-// The outputs of one group from its h (and the row's factor r)
+// Eight f32 of base from `from` + c on (c the group's column); zeros beyond the row
 template <bool TAIL>
-__device__ __forceinline__ void put_y(const NormArgs& a, int64_t row, int c, const float* h,
-                                      double r)
+__device__ __forceinline__ void load_f32(const NormArgs& a, const float* base, int64_t from, int c,
+                                         float* e)
 {
-    float w[8], y[8];
     if (!TAIL || a.k >= 8) {
-        load8<kTypeF32>(a.weight, read_at<TAIL>(a, c), w);
+        load8<kTypeF32>(base, from + read_at<TAIL>(a, c), e);
     }
     if (TAIL && a.k - c < 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[i] = c + i < a.k ? a.weight[c + i] : 0.f;
+            e[i] = c + i < a.k ? base[from + c + i] : 0.f;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        y[i] = (float)((double)h[i] * r * (double)w[i]);
-    }
+}
+
+// The outputs of one group from its y
+template <bool TAIL>
+__device__ __forceinline__ void put_outputs(const NormArgs& a, int64_t row, int c, const float* y)
+{
     const int64_t at = row * a.k + c;
     if (a.y != nullptr) {
         put_f32<TAIL>(a, a.y, row, c, y);
@@ -201,6 +202,20 @@ __device__ __forceinline__ void put_y(const NormArgs& a, int64_t row, int c, con
             }
         }
     }
+}
+
+// The outputs of one group from its h (and the row's factor r)
+template <bool TAIL>
+__device__ __forceinline__ void put_y(const NormArgs& a, int64_t row, int c, const float* h,
+                                      double r)
+{
+    float w[8], y[8];
+    load_f32<TAIL>(a, a.weight, 0, c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = (float)((double)h[i] * r * (double)w[i]);
+    }
+    put_outputs<TAIL>(a, row, c, y);
 }
 
 // P: groups of eight elements that a thread keeps in registers; the groups
@@ -315,7 +330,253 @@ hipError_t launch_t(const NormArgs& a, hipStream_t stream)
     return launch_p<TYPE, 4>(a, threads < 1024 ? threads : 1024, stream);
 }
 
+// ------------------------------------------------ norms on both sides of a block
+//   p = N(x; post_weight, post_bias)      (x itself without post_weight)
+//   h = residual + scale gate p           (f32, one rounding)
+//   y = N(h; weight, bias)
+// N divides by sqrt(mean v^2 + eps), the layer norm after taking the mean off
+// (its squares are summed in a second step: a row far from zero loses nothing).
+// All sums and products in f64, as above; the same split: a workgroup per row,
+// groups of eight elements in registers from the loads to the outputs.
+struct RowNorm {
+    double mean, r;
+};
+
+// The workgroup's sum of v (each thread's); `part` is this sum's own
+__device__ __forceinline__ double block_sum(double v, double* part, int waves)
+{
+    v = wave_sum(v);
+    if (waves > 1) {
+        if ((threadIdx.x & 63) == 0) {
+            part[threadIdx.x >> 6] = v;
+        }
+        __syncthreads();
+        v = part[0];
+        for (int i = 1; i < waves; ++i) {      // in wave order, the same in every thread
+            v += part[i];
+        }
+    }
+    return v;
+}
+
+// h of the group at column c from its x
+template <bool TAIL>
+__device__ __forceinline__ void block_h(const BlockNormArgs& a, int64_t row, int c, const float* x,
+                                        const RowNorm& n, float* h)
+{
+    double p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i] = (double)x[i];
+    }
+    float t[8];
+    if (a.post_weight != nullptr) {
+        load_f32<TAIL>(a, a.post_weight, 0, c, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] = (p[i] - n.mean) * n.r * (double)t[i];
+        }
+        if (a.post_bias != nullptr) {
+            load_f32<TAIL>(a, a.post_bias, 0, c, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[i] += (double)t[i];
+            }
+        }
+    }
+    if (a.gate != nullptr) {
+        load_f32<TAIL>(a, a.gate, row * a.gate_stride, c, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            p[i] *= (double)t[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        t[i] = 0.f;
+    }
+    if (a.residual != nullptr) {
+        load_f32<TAIL>(a, a.residual, row * a.k, c, t);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        h[i] = (float)__builtin_fma(p[i], (double)a.scale, (double)t[i]);
+        if (TAIL && c + i >= a.k) {
+            h[i] = 0.f;
+        }
+    }
+}
+
+template <bool TAIL>
+__device__ __forceinline__ void block_y(const BlockNormArgs& a, int64_t row, int c, const float* h,
+                                        const RowNorm& n)
+{
+    float w[8], b[8], y[8];
+    load_f32<TAIL>(a, a.weight, 0, c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        b[i] = 0.f;
+    }
+    if (a.bias != nullptr) {
+        load_f32<TAIL>(a, a.bias, 0, c, b);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[i] = (float)__builtin_fma(((double)h[i] - n.mean) * n.r, (double)w[i], (double)b[i]);
+    }
+    put_outputs<TAIL>(a, row, c, y);
+}
+
+template <int TYPE, int P, bool TAIL>
+__global__ void __launch_bounds__(1024)
+block_norm_kernel(BlockNormArgs a)
+{
+    __shared__ double part[4][16];
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
+    const int threads = blockDim.x;
+    const int waves = threads >> 6;
+    const int groups = (a.k - 1) / 8 + 1;
+    auto load_x = [&](int c, float* v) {
+        if (!TAIL || a.k >= 8) {
+            load8<TYPE>(a.x, row * a.x_stride + read_at<TAIL>(a, c), v);
+        }
+        if (TAIL && a.k - c < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = c + i < a.k ? element<TYPE>(a.x, row * a.x_stride + c + i) : 0.f;
+            }
+        }
+    };
+    // sum over the row's elements v of f(v); `more` gives those of a group beyond
+    // the registers
+    auto row_sum = [&](const float (&v)[P][8], auto more, double* place, auto f) {
+        double sum = 0.0;
+        auto add = [&](const float* e, int c) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum += !TAIL || c + i < a.k ? f((double)e[i]) : 0.0;
+            }
+        };
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int gi = p * threads + tid;
+            if (gi < groups) {
+                add(v[p], gi * 8);
+            }
+        }
+        for (int gi = P * threads + tid; gi < groups; gi += threads) {
+            float e[8];
+            more(gi * 8, e);
+            add(e, gi * 8);
+        }
+        return block_sum(sum, place, waves);
+    };
+    auto row_norm = [&](const float (&v)[P][8], auto more, int which) {
+        RowNorm n = {0.0, 0.0};
+        if (a.layer) {
+            n.mean = row_sum(v, more, part[2 * which], [](double e) { return e; }) / (double)a.k;
+        }
+        const double mean = n.mean;
+        const double squares = row_sum(v, more, part[2 * which + 1],
+                                       [mean](double e) { return (e - mean) * (e - mean); });
+        n.r = 1.0 / __builtin_sqrt(squares / (double)a.k + (double)a.eps);
+        return n;
+    };
+
+    float v[P][8];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int gi = p * threads + tid;
+        if (gi < groups) {
+            load_x(gi * 8, v[p]);
+        }
+    }
+    RowNorm n = {0.0, 0.0};
+    if (a.post_weight != nullptr) {
+        n = row_norm(v, load_x, 0);
+    }
+    const RowNorm post = n;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int gi = p * threads + tid;
+        if (gi < groups) {
+            block_h<TAIL>(a, row, gi * 8, v[p], post, v[p]);
+            if (a.sum != nullptr) {
+                put_f32<TAIL>(a, a.sum, row, gi * 8, v[p]);
+            }
+        }
+    }
+    // h of a group beyond the registers: from sum where it is kept (this thread's
+    // own stores; x and residual may have been there), else once more
+    auto load_sum = [&](int c, float* h) {
+        if (a.sum != nullptr) {
+            load_f32<TAIL>(a, a.sum, row * a.k, c, h);
+        } else {
+            float x[8];
+            load_x(c, x);
+            block_h<TAIL>(a, row, c, x, post, h);
+        }
+    };
+    if (a.sum != nullptr) {
+        for (int gi = P * threads + tid; gi < groups; gi += threads) {
+            float x[8];
+            load_x(gi * 8, x);
+            block_h<TAIL>(a, row, gi * 8, x, post, x);
+            put_f32<TAIL>(a, a.sum, row, gi * 8, x);
+        }
+    }
+    if (a.y == nullptr && a.y16 == nullptr && a.q == nullptr) {
+        return;
+    }
+    n = row_norm(v, load_sum, 1);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int gi = p * threads + tid;
+        if (gi < groups) {
+            block_y<TAIL>(a, row, gi * 8, v[p], n);
+        }
+    }
+    for (int gi = P * threads + tid; gi < groups; gi += threads) {
+        float h[8];
+        load_sum(gi * 8, h);
+        block_y<TAIL>(a, row, gi * 8, h, n);
+    }
+}
+
+template <int TYPE, int P>
+hipError_t launch_block_p(const BlockNormArgs& a, int threads, hipStream_t stream)
+{
+    const dim3 grid((unsigned)a.m), block(threads);
+    if (a.k % 8 != 0) {
+        hipLaunchKernelGGL((block_norm_kernel<TYPE, P, true>), grid, block, 0, stream, a);
+    } else {
+        hipLaunchKernelGGL((block_norm_kernel<TYPE, P, false>), grid, block, 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+template <int TYPE>
+hipError_t launch_block_t(const BlockNormArgs& a, hipStream_t stream)
+{
+    const int groups = (a.k - 1) / 8 + 1;
+    if (groups <= 1024) {
+        return launch_block_p<TYPE, 1>(a, (groups + 63) / 64 * 64, stream);
+    }
+    const int threads = a.m < 1024 ? 1024 : ((groups + 3) / 4 + 63) / 64 * 64;
+    return launch_block_p<TYPE, 4>(a, threads < 1024 ? threads : 1024, stream);
+}
+
 }  // namespace
+
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream)
+{
+    switch (a.x_type) {
+    case kTypeF16: return launch_block_t<kTypeF16>(a, stream);
+    case kTypeBF16: return launch_block_t<kTypeBF16>(a, stream);
+    default: return launch_block_t<kTypeF32>(a, stream);
+    }
+}
 
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream)
 {

@@ -27,6 +27,19 @@ Q4K_F32 = 0
 Q4K_F16 = 1
 Q4K_BF16 = 2
 
+Q4K_ACT_NONE = 0
+Q4K_ACT_RELU = 1
+Q4K_ACT_SILU = 2
+Q4K_ACT_GELU = 3
+Q4K_ACT_GELU_TANH = 4
+Q4K_ACT_SIGMOID = 5
+
+Q4K_NORM_RMS = 0
+Q4K_NORM_LAYER = 1
+
+Q4K_SCORE_SOFTMAX = 0
+Q4K_SCORE_SIGMOID = 1
+
 # every symbol include/q4k.h declares
 EXPORTED = (
     "q4k_row_bytes",
@@ -63,6 +76,12 @@ EXPORTED = (
     "q4k_f16_gemm_grouped",
     "q4k_lora_ws",
     "q4k_lora",
+    "q4k_gemv_act",
+    "q4k_f16_gemm_act",
+    "q4k_gemv_grouped_act",
+    "q4k_f16_gemm_grouped_act",
+    "q4k_block_norm",
+    "q4k_moe_route_biased",
 )
 
 
@@ -119,6 +138,18 @@ class q6k_plan_info(ctypes.Structure):
         ("rows_per_block", ctypes.c_int32),
         ("grid", ctypes.c_int32),
         ("lds_bytes", ctypes.c_int32),
+    ]
+
+
+class q4k_epilogue(ctypes.Structure):
+    _fields_ = [
+        ("bias", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("y16", ctypes.c_void_p),
+        ("gate_type", ctypes.c_int32),
+        ("act", ctypes.c_int32),
     ]
 
 
@@ -194,6 +225,7 @@ def load_library():
         lib.q4k_plan.restype = ctypes.c_int
         ci = ctypes.c_int
         sz = ctypes.c_size_t
+        cf = ctypes.c_float
         grouped = [vp, vp, vp, i64, i64, i64, i64, i64, i64, i64]   # offsets .. y_count
         for name, args, res in (
                 ("q4k_rmsnorm", [vp, ci, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64,
@@ -206,6 +238,14 @@ def load_library():
                 ("q4k_gemv_grouped", [vp, vp, vp] + grouped + [vp, sz, vp], ci),
                 ("q4k_gemv_grouped_q8", [vp, vp, vp, vp] + grouped + [vp, sz, vp], ci),
                 ("q4k_f16_gemm_grouped", [vp, vp, vp] + grouped + [vp], ci),
+                ("q4k_gemv_act", [vp, vp, vp, i64, i64, i64, vp], ci),
+                ("q4k_f16_gemm_act", [vp, vp, vp, i64, i64, i64, vp], ci),
+                ("q4k_gemv_grouped_act", [vp, vp, vp] + grouped + [vp, sz, vp], ci),
+                ("q4k_f16_gemm_grouped_act", [vp, vp, vp] + grouped + [vp], ci),
+                ("q4k_block_norm", [vp, ci, i64, ci, vp, vp, vp, i64, cf, vp, vp, vp, vp, vp, vp,
+                                    vp, vp, i64, i64, cf, vp], ci),
+                ("q4k_moe_route_biased", [vp, i64, vp, ci, i64, i64, vp, vp, vp, vp, i64, i64, ci,
+                                          cf, i64, vp, sz, vp], ci),
                 ("q4k_lora_ws", [i64, i64], sz),
                 ("q4k_lora", [vp, ci, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp,
                               sz, vp], ci)):
@@ -625,6 +665,14 @@ def q4k_gemv_grouped_q8(w, q, d, y, offsets, n: int, k: int, groups: int, rows: 
          _ws_bytes(ws, ws_bytes))
 
 
+def _check_halves(*tensors):
+    """Refuses tensors that do not hold binary16 numbers."""
+    halves = (_torch.float16, _torch.int16, _torch.uint16)
+    for t in tensors:
+        if hasattr(t, "get_device") and t.dtype not in halves:
+            raise TypeError("expected f16 (or its bits as 16-bit integers), got %s" % t.dtype)
+
+
 def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows: int, *,
                          x_rows=None, x_div: int = 1, x_count=None, y_rows=None, y_count=None,
                          stream=None) -> None:
@@ -635,10 +683,7 @@ def q4k_f16_gemm_grouped(w16, x16, y, offsets, n: int, k: int, groups: int, rows
     i32 = _torch.int32
     x_count = rows if x_count is None else x_count
     y_count = rows if y_count is None else y_count
-    halves = (_torch.float16, _torch.int16, _torch.uint16)
-    for t in (w16, x16):
-        if hasattr(t, "get_device") and t.dtype not in halves:
-            raise TypeError("expected f16 (or its bits as 16-bit integers), got %s" % t.dtype)
+    _check_halves(w16, x16)
     _run(load_library().q4k_f16_gemm_grouped, "q4k_f16_gemm_grouped", dev, stream,
          _at(w16, None, groups * n * k, dev), _at(x16, None, x_count * k, dev),
          _at(y, _torch.float32, y_count * n, dev), _at(offsets, i32, groups + 1, dev),
@@ -667,6 +712,129 @@ def q4k_lora(x, a, b, y, offsets, order, n: int, k: int, r: int, adapters: int, 
          _at(scales, f32, adapters, dev), _at(offsets, i32, adapters + 1, dev),
          _at(order, i32, rows, dev), int(n), int(k), int(r), int(adapters), int(rows),
          _at(ws, None, 0, dev), _ws_bytes(ws, ws_bytes))
+
+
+# ------------------------------------------------- the ends of a layer's blocks
+def _epilogue(dev, y, y16, act, bias, gate, residual, gate_type, biases: int, count: int):
+    """The q4k_epilogue of a product of `count` outputs and `biases` biases."""
+    f32, f16 = _torch.float32, _torch.float16
+    if gate is None:
+        kind = Q4K_F32
+    elif not hasattr(gate, "get_device"):
+        kind = Q4K_F32 if gate_type is None else int(gate_type)
+    else:
+        kind = _act_type(gate, gate_type)
+    gate = _at(gate, None, count, dev)
+    return q4k_epilogue(_at(bias, f32, biases, dev), gate, _at(residual, f32, count, dev),
+                        _at(y, f32, count, dev), _at(y16, f16, count, dev), kind, int(act))
+
+
+def q4k_gemv_act(w, x, y, n: int, k: int, m: int = 1, *, act: int = Q4K_ACT_NONE, bias=None,
+                 gate=None, residual=None, y16=None, gate_type=None, stream=None) -> None:
+    """y = act(W x + bias) * gate + residual for the m vectors of x, W in Q4_K
+    (bias: n; gate, f32 or f16, and residual, f32: m x n); y f32 (None: not
+    wanted) and y16 f16; asynchronous on stream."""
+    dev = _device(w, x, y, y16, bias, gate, residual)
+    ep = _epilogue(dev, y, y16, act, bias, gate, residual, gate_type, n, m * n)
+    _run(load_library().q4k_gemv_act, "q4k_gemv_act", dev, stream,
+         _at(w, _torch.uint8, n * (k // 256) * 144, dev), _at(x, _torch.float32, m * k, dev),
+         ctypes.addressof(ep), int(n), int(k), int(m))
+
+
+def q4k_f16_gemm_act(w16, x16, y, m: int, n: int, k: int, *, act: int = Q4K_ACT_NONE, bias=None,
+                     gate=None, residual=None, y16=None, gate_type=None, stream=None) -> None:
+    """q4k_gemv_act on an fp16 mirror (n x k halves) and fp16 x (m x k), each an
+    f16 tensor or its bits in an int16 or uint16 one, on the matrix cores;
+    asynchronous on stream."""
+    dev = _device(w16, x16, y, y16, bias, gate, residual)
+    _check_halves(w16, x16)
+    ep = _epilogue(dev, y, y16, act, bias, gate, residual, gate_type, n, m * n)
+    _run(load_library().q4k_f16_gemm_act, "q4k_f16_gemm_act", dev, stream,
+         _at(w16, None, n * k, dev), _at(x16, None, m * k, dev), ctypes.addressof(ep), int(m),
+         int(n), int(k))
+
+
+def q4k_gemv_grouped_act(w, x, y, offsets, n: int, k: int, groups: int, rows: int, *,
+                         act: int = Q4K_ACT_NONE, bias=None, gate=None, residual=None, y16=None,
+                         gate_type=None, x_rows=None, x_div: int = 1, x_count=None, y_rows=None,
+                         y_count=None, ws=None, ws_bytes=None, stream=None) -> None:
+    """q4k_gemv_grouped with the epilogue of q4k_gemv_act (bias: groups x n; gate
+    and residual where y's rows are); asynchronous on stream."""
+    dev = _device(w, x, y, y16, offsets, x_rows, y_rows, ws, bias, gate, residual)
+    f32, i32 = _torch.float32, _torch.int32
+    x_count = rows if x_count is None else x_count
+    y_count = rows if y_count is None else y_count
+    ep = _epilogue(dev, y, y16, act, bias, gate, residual, gate_type, groups * n, y_count * n)
+    _run(load_library().q4k_gemv_grouped_act, "q4k_gemv_grouped_act", dev, stream,
+         _at(w, _torch.uint8, groups * n * (k // 256) * 144, dev), _at(x, f32, x_count * k, dev),
+         ctypes.addressof(ep), _at(offsets, i32, groups + 1, dev),
+         _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
+         int(rows), int(x_div), int(x_count), int(y_count), _at(ws, None, 0, dev),
+         _ws_bytes(ws, ws_bytes))
+
+
+def q4k_f16_gemm_grouped_act(w16, x16, y, offsets, n: int, k: int, groups: int, rows: int, *,
+                             act: int = Q4K_ACT_NONE, bias=None, gate=None, residual=None,
+                             y16=None, gate_type=None, x_rows=None, x_div: int = 1, x_count=None,
+                             y_rows=None, y_count=None, stream=None) -> None:
+    """q4k_f16_gemm_grouped with the epilogue of q4k_gemv_grouped_act;
+    asynchronous on stream."""
+    dev = _device(w16, x16, y, y16, offsets, x_rows, y_rows, bias, gate, residual)
+    i32 = _torch.int32
+    x_count = rows if x_count is None else x_count
+    y_count = rows if y_count is None else y_count
+    _check_halves(w16, x16)
+    ep = _epilogue(dev, y, y16, act, bias, gate, residual, gate_type, groups * n, y_count * n)
+    _run(load_library().q4k_f16_gemm_grouped_act, "q4k_f16_gemm_grouped_act", dev, stream,
+         _at(w16, None, groups * n * k, dev), _at(x16, None, x_count * k, dev),
+         ctypes.addressof(ep), _at(offsets, i32, groups + 1, dev),
+         _at(x_rows, i32, rows, dev), _at(y_rows, i32, rows, dev), int(n), int(k), int(groups),
+         int(rows), int(x_div), int(x_count), int(y_count))
+
+
+def q4k_block_norm(x, weight, k: int, m: int = 1, *, kind: int = Q4K_NORM_RMS, bias=None,
+                   post_weight=None, post_bias=None, gate=None, gate_stride: int = 0,
+                   scale: float = 1.0, residual=None, sum_out=None, y=None, y16=None, q=None,
+                   d=None, eps: float = 1e-5, x_stride: int = 0, x_type=None,
+                   stream=None) -> None:
+    """h = residual + scale * gate * N(x; post_weight, post_bias) (x itself
+    without post_weight), y = N(h; weight, bias) for m rows of k, N the rms or the
+    layer norm: h to sum_out, y to any of y (f32), y16 (f16) and q, d (Q8 codes and
+    scales); gate f32, one row of k for all (gate_stride 0) or m rows gate_stride
+    apart; x f32, f16 or bf16, its rows x_stride apart (0: k); asynchronous on
+    stream."""
+    dev = _device(x, weight, residual, sum_out, y, y16, q, d, post_weight, post_bias, gate, bias)
+    mk = m * k
+    f32, i8, f16 = _torch.float32, _torch.int8, _torch.float16
+    rows = m if gate_stride else 1
+    _run(load_library().q4k_block_norm, "q4k_block_norm", dev, stream,
+         _rows_at(x, None, m, k, x_stride, dev), _act_type(x, x_type), int(x_stride), int(kind),
+         _at(post_weight, f32, k, dev), _at(post_bias, f32, k, dev),
+         _rows_at(gate, f32, rows, k, gate_stride, dev), int(gate_stride), float(scale),
+         _at(residual, f32, mk, dev), _at(sum_out, f32, mk, dev), _at(weight, f32, k, dev),
+         _at(bias, f32, k, dev), _at(y, f32, mk, dev), _at(y16, f16, mk, dev),
+         _at(q, i8, mk, dev), _at(d, f32, mk // 32, dev), int(k), int(m), float(eps))
+
+
+def q4k_moe_route_biased(logits, ids, weights, n_experts: int, topk: int, m: int = 1, *,
+                         bias=None, score: int = Q4K_SCORE_SOFTMAX, groups: int = 1,
+                         topk_groups: int = 1, renorm: bool = True, scale: float = 1.0,
+                         offsets=None, order=None, ws=None, ws_bytes=None,
+                         logits_stride: int = 0, stream=None) -> None:
+    """The topk experts of m tokens by score + bias (bias: n_experts), within the
+    topk_groups best of `groups` groups of experts; ids, their scores times scale
+    as weights (renorm: shares of their sum) and, with offsets and order, the slots
+    grouped by expert; asynchronous on stream."""
+    dev = _device(logits, ids, weights, offsets, order, ws, bias)
+    f32, i32 = _torch.float32, _torch.int32
+    slots = m * topk
+    _run(load_library().q4k_moe_route_biased, "q4k_moe_route_biased", dev, stream,
+         _rows_at(logits, f32, m, n_experts, logits_stride, dev), int(logits_stride),
+         _at(bias, f32, n_experts, dev), int(score), int(groups), int(topk_groups),
+         _at(ids, i32, slots, dev), _at(weights, f32, slots, dev),
+         _at(offsets, i32, n_experts + 1, dev), _at(order, i32, slots, dev), int(n_experts),
+         int(topk), 1 if renorm else 0, float(scale), int(m), _at(ws, None, 0, dev),
+         _ws_bytes(ws, ws_bytes))
 
 
 def q4k_read_calibrate_blocks() -> int:

@@ -567,6 +567,154 @@ int q4k_lora(const void* x, int x_type, const void* a, const void* b, const floa
              const int32_t* order, int64_t n, int64_t k, int64_t r, int64_t adapters,
              int64_t rows, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------
+ * The ends of a layer's blocks: products with an epilogue, the norms on both
+ * sides of a residual's addition, and routing by biased scores.  The conventions
+ * of the calls around the projections hold.
+ * ------------------------------------------------------------------- */
+
+/* Activations, z in f32:
+ *   silu z / (1 + e^-z), gelu z/2 erfc(-z/sqrt 2), gelu in its tanh form
+ *   z / (1 + e^-2u) with u = sqrt(2/pi) (z + 0.044715 z^3), sigmoid 1 / (1 + e^-z).
+ * For finite z, act(z) is within (32 + 4 z^2 + |z|^3) 2^-24 |act(z)| + 2^-100 of the
+ * exact value at z; relu and none are exact.  A NaN gives a NaN, and so does
+ * z = -infinity with silu and both gelu (their formulas' infinity times 0). */
+enum q4k_act {
+    Q4K_ACT_NONE = 0,
+    Q4K_ACT_RELU = 1,
+    Q4K_ACT_SILU = 2,
+    Q4K_ACT_GELU = 3,
+    Q4K_ACT_GELU_TANH = 4,
+    Q4K_ACT_SIGMOID = 5
+};
+
+/* What a product's sums go through instead of being written:
+ *   z = sum + bias,  y = act(z) * gate + residual
+ * in f32 (z rounded once from the product's own sums and their accuracy; then
+ * the activation, the product with gate and the sum with residual each within
+ * a rounding).  Every pointer is a device pointer, 16-byte aligned.
+ *  bias     : f32, one per weight row (n; grouped products groups x n, by
+ *             group), NULL = 0
+ *  gate     : elements of gate_type (Q4K_F32 or Q4K_F16) where y's are (m x n;
+ *             grouped products y_count x n), NULL = 1: the other product of a
+ *             gated block.  Q4K_BF16: Q4K_ERR_UNSUPPORTED
+ *  residual : f32 where y's elements are, NULL = 0
+ *  y, y16   : f32 / binary16 (nearest even of the f32 y) outputs, at least one;
+ *             y may be residual, and y or y16 may be gate where the types are
+ *             the same: each element is read before it is written.  No other
+ *             overlap
+ * The struct is the caller's and read during the call only. */
+typedef struct q4k_epilogue {
+    const float* bias;
+    const void* gate;
+    const float* residual;
+    float* y;
+    void* y16;
+    int32_t gate_type;
+    int32_t act;              /* enum q4k_act */
+} q4k_epilogue;
+
+/* q4k_gemv with an epilogue: the same shapes, kernels, refusals and sums (z is
+ * within 1e-5 * sum|w||x| of the exact sum plus bias, and 2^-24 |z| more).
+ * Asynchronous on `stream`; allocates nothing. */
+int q4k_gemv_act(const void* w, const float* x, const q4k_epilogue* ep, int64_t n, int64_t k,
+                 int64_t m, void* stream);
+
+/* q4k_f16_gemm with an epilogue: the same operands and refusals, z's sum within
+ * k * 2^-23 * sum|w16||x16|. */
+int q4k_f16_gemm_act(const void* w16, const void* x16, const q4k_epilogue* ep, int64_t m,
+                     int64_t n, int64_t k, void* stream);
+
+/* q4k_gemv_grouped with an epilogue: the same operands, workspace, refusals and
+ * sums.  Rows of y, and of gate and residual, are those of y_rows; rows that no
+ * position names are not touched. */
+int q4k_gemv_grouped_act(const void* w, const float* x, const q4k_epilogue* ep,
+                         const int32_t* offsets, const int32_t* x_rows, const int32_t* y_rows,
+                         int64_t n, int64_t k, int64_t groups, int64_t rows, int64_t x_div,
+                         int64_t x_count, int64_t y_count, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* q4k_f16_gemm_grouped with an epilogue, likewise. */
+int q4k_f16_gemm_grouped_act(const void* w16, const void* x16, const q4k_epilogue* ep,
+                             const int32_t* offsets, const int32_t* x_rows,
+                             const int32_t* y_rows, int64_t n, int64_t k, int64_t groups,
+                             int64_t rows, int64_t x_div, int64_t x_count, int64_t y_count,
+                             void* stream);
+
+/* Norms over a row v of k elements:
+ *   rms   v / sqrt(sum v^2 / k + eps) * weight + bias
+ *   layer (v - mean) / sqrt(sum (v - mean)^2 / k + eps) * weight + bias */
+enum q4k_norm {
+    Q4K_NORM_RMS = 0,
+    Q4K_NORM_LAYER = 1
+};
+
+/* The norms on both sides of a residual's addition, in one call:
+ *   p = N(x; post_weight, post_bias)          (x where post_weight is NULL)
+ *   h = residual + scale * gate * p           (f32, rounded once)
+ *   y = N(h; weight, bias)                    per row of k elements
+ *  x         : device, m rows of k elements of x_type, x_stride elements from
+ *              row to row (0 = k; at least k otherwise): the block's output
+ *  kind      : enum q4k_norm, of both norms (Q4K_ERR_UNSUPPORTED otherwise)
+ *  post_weight, post_bias, weight, bias : device, k f32; a bias may be NULL (0)
+ *              and is not read without its weight; weight may be NULL where
+ *              only h is wanted
+ *  gate      : device, f32: k, for every row (gate_stride 0), or m rows of k,
+ *              gate_stride floats apart (at least k); NULL = 1
+ *  scale     : finite (Q4K_ERR_SHAPE)
+ *  residual  : device, m x k f32; NULL = 0
+ *  sum_out   : device, m x k f32, gets h; NULL = not kept.  May be residual
+ *              itself, or x when x is f32 and dense; no other overlap
+ *  y, y16, q, d : as for q4k_rmsnorm, of the f32 y
+ * At least one output.  m, k >= 1, eps >= 0 and finite.  All sums and products
+ * in f64, h and y rounded once to f32: h is within 2^-23 (|residual| + |scale
+ * gate p|) of the exact value, y within 2^-23 (|y| + |bias|) of the exact value
+ * for the h that was rounded (2^-23 + 2^-40 k of it where a layer norm's mean is
+ * 2^10 times its deviation).  A row of h with a NaN, or with an infinity in a
+ * layer norm, gives NaN; with an infinity in an rms norm NaN there and its bias
+ * (or 0) elsewhere; x likewise gives p.  Asynchronous on `stream`; allocates
+ * nothing. */
+int q4k_block_norm(const void* x, int x_type, int64_t x_stride, int kind,
+                   const float* post_weight, const float* post_bias, const float* gate,
+                   int64_t gate_stride, float scale, const float* residual, float* sum_out,
+                   const float* weight, const float* bias, float* y, void* y16, int8_t* q,
+                   float* d, int64_t k, int64_t m, float eps, void* stream);
+
+/* Scores of experts from their logits l. */
+enum q4k_score {
+    Q4K_SCORE_SOFTMAX = 0,     /* exp(l - max) / sum exp(l - max) */
+    Q4K_SCORE_SIGMOID = 1      /* 1 / (1 + exp(-l)) */
+};
+
+/* The experts of m tokens, chosen by biased scores:
+ *   s = score(l),  c = s + bias;
+ *   expert_groups > 1: the experts are so many groups of consecutive ones; a
+ *   group's value is the sum of its two largest c (of its one where there is
+ *   one), and the topk_groups groups of the largest values stay;
+ *   the topk largest c of those that stay are chosen, the largest first;
+ *   weights = scale * s, with renorm nonzero scale * s / sum of the chosen s (0
+ *   where that sum is 0).
+ * Scores, sums and comparisons in f64 (values that differ by a few 2^-52 may be
+ * taken either way; equal ones in the order of the experts, of the groups).
+ *  logits, logits_stride, ids, offsets, order, ws : as for q4k_moe_route
+ *  bias   : device, n_experts f32, NULL = 0
+ *  score  : enum q4k_score (Q4K_ERR_UNSUPPORTED otherwise)
+ *  weights: device, m x topk f32, rounded once
+ *  A logit that is NaN or -infinity masks its expert as in q4k_moe_route; a bias
+ *  that is NaN or -infinity keeps its expert from being chosen (it still counts
+ *  in a softmax's sum), one of +infinity puts it first.  Choices that are not
+ *  there get id -1 and weight 0.
+ * 1 <= topk <= 32, n_experts <= 1024, 1 <= topk_groups <= expert_groups <= 64,
+ * n_experts % expert_groups == 0, topk <= n_experts / expert_groups *
+ * topk_groups, scale finite (Q4K_ERR_SHAPE).  Workspace: q4k_moe_group_ws(m *
+ * topk, n_experts, topk), none without offsets.  Asynchronous; allocates
+ * nothing. */
+int q4k_moe_route_biased(const float* logits, int64_t logits_stride, const float* bias, int score,
+                         int64_t expert_groups, int64_t topk_groups, int32_t* ids,
+                         float* weights, int32_t* offsets, int32_t* order, int64_t n_experts,
+                         int64_t topk, int renorm, float scale, int64_t m, void* ws,
+                         size_t ws_bytes, void* stream);
+
 /* Read `bytes` (a multiple of 16) of device memory at `buf` (16-byte
  * aligned) with coalesced 16-byte loads and write a checksum per workgroup
  * to `out` (device, q4k_read_calibrate_blocks() floats).  Benchmark
