@@ -29,7 +29,7 @@ HEADERS = [os.path.join(CSRC, "q4k_kernels.h"), os.path.join(CSRC, "q4k_device.h
            os.path.join(CSRC, "q4k_lines.h"), os.path.join(CSRC, "q4k_xrep.h"),
            os.path.join(CSRC, "q4k_q8.h"), os.path.join(CSRC, "q4k_groups.h"),
            os.path.join(CSRC, "q4k_out.h"), os.path.join(CSRC, "q4k_epilogue.h"),
-           os.path.join(CSRC, "q4k_f16_tile.h"),
+           os.path.join(CSRC, "q4k_f16_tile.h"), os.path.join(CSRC, "q4k_f16_dma.h"),
            os.path.join(os.path.dirname(PKG), "include", "q4k.h")]
 ARCH = "gfx950"
 

@@ -1560,7 +1560,8 @@ int q4k_f16_gemm_grouped_act(const void* w16, const void* x16, const q4k_epilogu
     if (rc != Q4K_OK) {
         return rc;
     }
-    rc = f16_grouped_checks(w16, x16, nullptr, k, q4k::f16_grouped_act_grid(rows, groups, n, k));
+    rc = f16_grouped_checks(w16, x16, nullptr, k,
+                            k < 1 ? 1 : q4k::f16_grouped_act_grid(rows, groups, x_count, n, k));
     if (rc != Q4K_OK) {
         return rc;
     }

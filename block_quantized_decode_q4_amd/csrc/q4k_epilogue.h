@@ -25,20 +25,27 @@ constexpr int kActGelu = 3;
 constexpr int kActGeluTanh = 4;
 constexpr int kActSigmoid = 5;
 
+// e^x by the hardware's 2^x: the product's rounding is x 2^-24 of it, the rest a few
+// steps; above 2^128 infinity, below 2^-126 0
+__device__ __forceinline__ float fast_exp(float x)
+{
+    return __builtin_amdgcn_exp2f(x * 1.44269504f);
+}
+
 template <int ACT>
 __device__ __forceinline__ float activated(float z)
 {
     if constexpr (ACT == kActRelu) {
         return z < 0.f ? 0.f : z;              // a NaN stays one
     } else if constexpr (ACT == kActSilu) {
-        return z / (1.f + expf(-z));
+        return z * __builtin_amdgcn_rcpf(1.f + fast_exp(-z));
     } else if constexpr (ACT == kActGelu) {
         return 0.5f * z * erfcf(z * -0.707106781f);
     } else if constexpr (ACT == kActGeluTanh) {
         const float u2 = 1.59576912f * (z + 0.044715f * z * z * z);
-        return z / (1.f + expf(-u2));
+        return z * __builtin_amdgcn_rcpf(1.f + fast_exp(-u2));
     } else if constexpr (ACT == kActSigmoid) {
-        return 1.f / (1.f + expf(-z));
+        return __builtin_amdgcn_rcpf(1.f + fast_exp(-z));
     } else {
         return z;
     }

@@ -240,7 +240,7 @@ hipError_t launch_f16_gemm_act(const void* w16, const void* x16, const EpArgs& e
 int64_t f16_act_grid(int64_t m, int64_t n, int64_t k);
 hipError_t launch_f16_grouped_act(const void* w16, const void* x16, const EpArgs& ep,
                                   const GroupRows& g, int n, int k, hipStream_t stream);
-int64_t f16_grouped_act_grid(int64_t rows, int64_t groups, int64_t n, int64_t k);
+int64_t f16_grouped_act_grid(int64_t rows, int64_t groups, int64_t x_count, int64_t n, int64_t k);
 
 // Low-rank adapters (q4k_lora.hip).
 struct LoraArgs {

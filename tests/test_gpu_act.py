@@ -131,7 +131,9 @@ def test_gemv_whose_sums_do_not_fit_the_lds():
 # -------------------------------------------------------------- fp16 mirrors
 GEMMS = [(1, 1, 64), (1, 64, 64), (2, 300, 256), (7, 33, 128), (16, 1000, 512), (63, 127, 192),
          (64, 128, 64), (65, 129, 320), (130, 257, 1024), (257, 513, 128), (509, 1000, 448),
-         (300, 4096, 256), (1025, 2050, 64), (2000, 1024, 576), (33, 5000, 64), (700, 72, 2048)]
+         (300, 4096, 256), (1025, 2050, 64), (2000, 1024, 576), (33, 5000, 64), (700, 72, 2048),
+         (1000, 7000, 192), (2048, 14336, 128), (1100, 9000, 320), (257, 4100, 1536), (40, 1003, 768),
+         (120, 200, 64), (520, 4096, 2048)]
 
 
 @pytest.mark.parametrize("m,n,k", GEMMS)
@@ -153,7 +155,8 @@ def test_gemm(m, n, k, which):
 # (rows per group, n, k, x_div): positions in a mixed order, some left out
 GROUPS = [([1], 16, 256, 1), ([0, 3, 0, 1], 40, 512, 2), ([2, 1, 0, 4, 1], 1001, 256, 1),
           ([16, 17, 0, 33], 100, 768, 2), ([1] * 9, 70, 1024, 4), ([5, 0, 140], 200, 512, 1),
-          ([200, 90, 1, 300], 130, 256, 2), ([0, 0], 33, 256, 1), ([3, 3], 5, 256, 1)]
+          ([200, 90, 1, 300], 130, 256, 2), ([0, 0], 33, 256, 1), ([3, 3], 5, 256, 1),
+          ([700, 0, 900, 3], 3000, 256, 1), ([260, 129, 600], 5001, 256, 1)]
 
 
 def _grouped(g, kind, sizes, n, k, x_div, ep):
@@ -314,6 +317,42 @@ def test_activations_over_their_range(act):
     small = z64.abs() > 64                     # there act is z, 0 or 1 to a step
     err = torch.where(small, 2.0 ** -22 * ref.abs() + 2.0 ** -80, err)
     B.assert_within(y, ref, err, "act %d" % act)
+
+
+def test_gemm_of_rows_past_4_mi():
+    """Rows so long that an operand's offsets within a tile pass 32 bits."""
+    m, n, k = 2, 3, (1 << 22) + 64
+    g = _gen(12)
+    w, x = (_rand(g, n, k) * 2.0 ** -10).half(), _rand(g, m, k).half()
+    for which in (2, 5):
+        o, y = _operands(g, EPILOGUES[which], (n,), (m, n))
+        q4k.q4k_f16_gemm_act(w, x, y, m, n, k, **o)
+        z = x.double() @ w.double().T + o["bias"].double()
+        _check(y, o, z, k * 2.0 ** -23 * (x.double().abs() @ w.double().abs().T), "long rows")
+
+
+def test_grouped_x_of_4_gib():
+    """x rows whose offsets pass 32 bits."""
+    n, k, groups, rows = 96, 4096, 2, 130
+    x_count = (1 << 31) // k + 3
+    g = _gen(13)
+    w = (_rand(g, groups * n, k) * 0.03).half()
+    x = torch.zeros((x_count, k), device="cuda", dtype=F16)
+    x[:8], x[-8:] = _rand(g, 8, k).half(), _rand(g, 8, k).half()
+    x_rows = np.concatenate([np.arange(8), x_count - 1 - np.arange(8)])[np.arange(rows) % 16]
+    off = [0, 50, rows]
+    o, y = _operands(g, EPILOGUES[2], (groups, n), (rows, n))
+    q4k.q4k_f16_gemm_grouped_act(w, x, y, _i32(off), n, k, groups, rows, x_rows=_i32(x_rows),
+                                 x_count=x_count, **o)
+    z = torch.empty((rows, n), device="cuda", dtype=torch.float64)
+    dz = torch.empty_like(z)
+    xs = x[torch.from_numpy(x_rows).cuda()].double()
+    for e in range(groups):
+        at = slice(off[e], off[e + 1])
+        w64 = w[e * n: (e + 1) * n].double()
+        z[at] = xs[at] @ w64.T + o["bias"][e].double()
+        dz[at] = k * 2.0 ** -23 * (xs[at].abs() @ w64.abs().T)
+    _check(y, o, z, dz, "grouped")
 
 
 def test_gemm_past_32_bit_offsets():
