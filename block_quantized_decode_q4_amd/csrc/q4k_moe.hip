@@ -34,6 +34,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "q4k_epilogue.h"
 #include "q4k_groups.h"
 #include "q4k_kernels.h"
 
@@ -229,9 +230,10 @@ __device__ __forceinline__ void route_tokens(const RouteArgs& a, int64_t, float*
 // s = softmax(l) or sigmoid(l), c = s + bias.  With groups of experts (`parts`
 // consecutive ones of the same size) a group's value is the sum of its two largest
 // c, and the experts of the `keep` largest groups stay.  The topk largest c are
-// chosen, their weights are scale s, or scale s / sum of the chosen s.  Scores,
-// sums and comparisons in f64, so that what is chosen does not hang on how an exp
-// was rounded to f32.
+// chosen, their weights are scale s, or scale s / sum of the chosen s.  What is
+// chosen does not hang on how an exp was rounded: f32 finds the largest, and where
+// others come nearer to it than their errors can be, these few are scored in f64
+// (equal logits are among them).  Weights are f64 until their one rounding.
 constexpr double kNoValue = -__builtin_inf();
 
 template <int CTRL>
@@ -279,6 +281,301 @@ __device__ __forceinline__ double softmax_part(float l, float top)
     return l == kNone ? 0.0 : l == top ? 1.0 : exp((double)l - (double)top);
 }
 
+// The larger and the second of the two largest over a token's lanes: each step joins
+// two sets of lanes that have none in common
+__device__ __forceinline__ void join_two(float& first, float& second, float f, float s)
+{
+    second = fmaxf(fminf(first, f), fmaxf(second, s));
+    first = fmaxf(first, f);
+}
+
+template <int LANES>
+__device__ __forceinline__ void lanes_two(float& first, float& second)
+{
+    if constexpr (LANES == 16) {
+        join_two(first, second, as_float(dpp<0x128>(as_int(first))),
+                 as_float(dpp<0x128>(as_int(second))));
+        join_two(first, second, as_float(dpp<0x124>(as_int(first))),
+                 as_float(dpp<0x124>(as_int(second))));
+        join_two(first, second, as_float(dpp<0x122>(as_int(first))),
+                 as_float(dpp<0x122>(as_int(second))));
+        join_two(first, second, as_float(dpp<0x121>(as_int(first))),
+                 as_float(dpp<0x121>(as_int(second))));
+    } else {
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            join_two(first, second, __shfl_xor(first, off, 64), __shfl_xor(second, off, 64));
+        }
+    }
+}
+
+// A token's choice (its 16 or 64 lanes).  c: the values in f32, off by less than tol /
+// 2, experts i LANES + lane; exact(e): expert e's in f64.
+template <int LANES, int NL, typename Exact>
+struct Choice {
+    const BiasedRouteArgs& a;
+    float (&c)[NL];
+    float tol;
+    Exact exact;
+    int i0;
+
+    // This lane's experts among `some` (bits): the best in f64, ties to the lowest, or
+    // with second its two best
+    __device__ __forceinline__ void best_of(uint32_t some, double& first, double& second, int& at)
+    {
+        first = second = kNoValue;
+        at = 0x7fffffff;
+        while (__any(some != 0)) {
+            if (some != 0) {
+                const int e = __builtin_ctz(some) * LANES + i0;
+                some &= some - 1;
+                const double v = exact(e);
+                second = v > first ? first : v > second ? v : second;
+                at = v > first ? e : at;
+                first = v > first ? v : first;
+            }
+        }
+    }
+
+    // Group p's two largest values in f32
+    __device__ __forceinline__ void group_two(int p, int each, float& first, float& second)
+    {
+        first = second = kNone;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int e = i * LANES + i0;
+            join_two(first, second, e >= p * each && e < (p + 1) * each ? c[i] : kNone, kNone);
+        }
+        lanes_two<LANES>(first, second);
+    }
+
+    // Leaves the experts of the best groups
+    __device__ __forceinline__ void keep_groups()
+    {
+        const int each = a.groups / a.parts;
+        // group p's value in lane p % LANES, at p / LANES
+        constexpr int V = kMaxExpertGroups / LANES;
+        float value[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            value[v] = kNone;
+        }
+        auto put = [&](int p, float first, float second) __attribute__((always_inline)) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (p == v * LANES + i0) {
+                    value[v] = second == kNone ? first : first + second;
+                }
+            }
+        };
+        const bool rows = each % LANES == 0;   // a group's experts are whole rows of lanes
+        if (rows) {
+            float first = kNone, second = kNone;
+            int p = 0, left = each / LANES;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                join_two(first, second, c[i], kNone);
+                if (--left == 0) {
+                    lanes_two<LANES>(first, second);
+                    put(p++, first, second);
+                    first = second = kNone;
+                    left = each / LANES;
+                }
+            }
+        } else {
+            for (int p = 0; p < a.parts; ++p) {
+                float first, second;
+                group_two(p, each, first, second);
+                put(p, first, second);
+            }
+        }
+        // the keep-th largest value: as many steps of the largest that is left
+        float left[V], least = kNone, most = kNone;
+        uint64_t kept = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            left[v] = value[v];
+        }
+        for (int j = 0; j < a.keep; ++j) {
+            float best = kNone;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                best = fmaxf(best, left[v]);
+            }
+            best = lanes_max<LANES>(best);
+            int mine = 0x7fffffff;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v) {
+                mine = left[v] == best && best != kNone ? v * LANES + i0 : mine;
+            }
+            const int chosen = lanes_min<LANES>(mine);
+            kept |= chosen < kMaxExpertGroups ? 1ull << chosen : 0ull;
+            least = chosen < kMaxExpertGroups ? best : least;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                left[v] = chosen == v * LANES + i0 ? kNone : left[v];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            most = fmaxf(most, left[v]);
+        }
+        most = lanes_max<LANES>(most);         // of those that do not stay
+        const bool close = most != kNone && !(least - most > 2.f * tol);
+        if (__any(close)) {
+            // groups whose sums f32 does not tell from the last one that stays: in f64
+            double near[V];
+            int sure = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                near[v] = kNoValue;
+            }
+            for (int p = 0; p < a.parts; ++p) {
+                float mine = kNone;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    mine = p == v * LANES + i0 ? value[v] : mine;
+                }
+                mine = lanes_max<LANES>(mine);
+                const bool above = mine != kNone && mine > least + 2.f * tol;
+                const bool in = close && mine != kNone && !above && !(mine < least - 2.f * tol);
+                sure += above ? 1 : 0;
+                if (__any(in)) {
+                    float first, second;
+                    group_two(p, each, first, second);
+                    uint32_t some = 0;
+#pragma unroll
+                    for (int i = 0; i < NL; ++i) {
+                        const int e = i * LANES + i0;
+                        const bool has = in && e >= p * each && e < (p + 1) * each &&
+                                         c[i] != kNone && !(c[i] < second - tol);
+                        some |= has ? 1u << i : 0u;
+                    }
+                    double f, s;
+                    int at;
+                    best_of(some, f, s, at);
+                    const double best = lanes_max<LANES>(f);
+                    const int holder = lanes_min<LANES>(f == best ? i0 : LANES);
+                    const double next = lanes_max<LANES>(i0 == holder ? s : f);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (p == v * LANES + i0 && in) {
+                            near[v] = next == kNoValue ? best : best + next;
+                        }
+                    }
+                }
+            }
+            // those above stay, and the largest of the close ones, ties to the lowest
+            if (close) {
+                kept = 0;
+            }
+            for (int p = 0; p < a.parts; ++p) {
+                float mine = kNone;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    mine = p == v * LANES + i0 ? value[v] : mine;
+                }
+                mine = lanes_max<LANES>(mine);
+                kept |= close && mine != kNone && mine > least + 2.f * tol ? 1ull << p : 0ull;
+            }
+            for (int j = 0; j < a.keep; ++j) {
+                double best = kNoValue;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    best = near[v] > best ? near[v] : best;
+                }
+                best = lanes_max<LANES>(best);
+                int mine = 0x7fffffff;
+#pragma unroll
+                for (int v = V - 1; v >= 0; --v) {
+                    mine = near[v] == best && best != kNoValue ? v * LANES + i0 : mine;
+                }
+                const int chosen = lanes_min<LANES>(mine);
+                const bool take = close && sure + j < a.keep && chosen < kMaxExpertGroups;
+                kept |= take ? 1ull << chosen : 0ull;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    near[v] = chosen == v * LANES + i0 ? kNoValue : near[v];
+                }
+            }
+        }
+        if (rows) {
+            int p = 0, rest = each / LANES;
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                c[i] = kept >> p & 1 ? c[i] : kNone;
+                if (--rest == 0) {
+                    p = min(p + 1, kMaxExpertGroups - 1);
+                    rest = each / LANES;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int e = i * LANES + i0;
+                c[i] = e < a.groups && (kept >> (e / each) & 1) ? c[i] : kNone;
+            }
+        }
+    }
+
+    // The topk experts, lane i's choices i, i + LANES, ... to id
+    __device__ __forceinline__ void take(int* id)
+    {
+        constexpr int C = kChoices<LANES>;
+#pragma unroll
+        for (int v = 0; v < C; ++v) {
+            id[v] = -1;
+        }
+        for (int j = 0; j < a.topk; ++j) {
+            float best = c[0];
+#pragma unroll
+            for (int i = 1; i < NL; ++i) {
+                best = fmaxf(best, c[i]);
+            }
+            best = lanes_max<LANES>(best);
+            if (__all(best == kNone)) {
+                break;                         // nothing left in any token
+            }
+            // the lowest expert with it, and whether others come near
+            const float edge = best - tol;
+            int mine = 0x7fffffff;
+            int many = 0;
+#pragma unroll
+            for (int i = NL - 1; i >= 0; --i) {
+                mine = c[i] == best ? i * LANES + i0 : mine;
+                many += c[i] < edge ? 0 : 1;   // an edge that is NaN: all
+            }
+            int chosen = lanes_min<LANES>(mine);
+            // a lane with one, if it is the chosen, stands alone
+            const bool others = best != kNone && many > (chosen % LANES == i0 ? 1 : 0);
+            if (__any(others)) {
+                const uint64_t who = __ballot(others);
+                const int lane = threadIdx.x & 63;
+                const bool unsure = LANES == 64 ? who != 0 : (who >> (lane & 48) & 0xFFFF) != 0;
+                uint32_t some = 0;
+#pragma unroll
+                for (int i = 0; i < NL; ++i) {
+                    some |= unsure && c[i] != kNone && !(c[i] < edge) ? 1u << i : 0u;
+                }
+                double f, s;
+                int at;
+                best_of(some, f, s, at);
+                const double top = lanes_max<LANES>(f);
+                const int exactly = lanes_min<LANES>(f == top ? at : 0x7fffffff);
+                chosen = unsure ? exactly : chosen;
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                c[i] = i * LANES + i0 == chosen ? kNone : c[i];
+            }
+#pragma unroll
+            for (int v = 0; v < C; ++v) {
+                id[v] = j == v * LANES + i0 && best != kNone ? chosen : id[v];
+            }
+        }
+    }
+};
+
 template <int LANES, int NL>
 __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t token, float* l,
                                              int* id, float* weight)
@@ -286,128 +583,83 @@ __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t t
     constexpr int C = kChoices<LANES>;
     const int i0 = threadIdx.x & (LANES - 1);
     float top = kNone;
-    double all = 1.0;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        l[i] = l[i] == l[i] ? l[i] : kNone;
-    }
-    if (!a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            top = fmaxf(top, l[i]);
-        }
-        top = lanes_max<LANES>(top);
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            sum += softmax_part(l[i], top);
-        }
-        all = lanes_sum<LANES>(sum);
-    }
-    auto score = [&](float v) {
-        return a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : softmax_part(v, top) / all;
-    };
-    double c[NL];
+    float b[NL];
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         const int e = i * LANES + i0;
-        const float b = a.bias != nullptr && e < a.groups ? a.bias[e] : 0.f;
-        c[i] = l[i] == kNone || b != b || b == kNone ? kNoValue : score(l[i]) + (double)b;
+        b[i] = a.bias != nullptr && e < a.groups ? a.bias[e] : 0.f;
+        l[i] = l[i] == l[i] ? l[i] : kNone;
+        top = fmaxf(top, l[i]);
     }
+    // Scores in f32.  The exp is off by (1.5 |x| + 2) steps of 2^-24, so a sigmoid by
+    // less than 4 of them; a softmax's score by less than (NL + 8) steps of the largest
+    // score (its sum's roundings; x e^-x < 1).  half: no less than that; tol: twice that
+    // and more than the roundings of the bias's addition.
+    float c[NL], half = 0x1p-22f;
+    double all = 1.0;
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            c[i] = __builtin_amdgcn_rcpf(1.f + fast_exp(-l[i]));
+        }
+    } else {
+        top = lanes_max<LANES>(top);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            // equal infinities would leave inf - inf: the largest counts 1
+            c[i] = l[i] == kNone ? 0.f : l[i] == top ? 1.f : fast_exp(l[i] - top);
+            sum += c[i];
+        }
+        const float share = 1.f / lanes_sum<LANES>(sum);
+        half = share * 0x1p-19f;
+        // where weights are shares of all experts' scores, and where f64 decides
+        double sum64 = 0.0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            sum64 += softmax_part(l[i], top);
+            c[i] *= share;
+        }
+        all = lanes_sum<LANES>(sum64);
+    }
+    float largest = 0.f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const bool in = l[i] != kNone && b[i] == b[i] && b[i] != kNone;
+        c[i] = in ? c[i] + b[i] : kNone;
+        largest = in ? fmaxf(largest, fabsf(c[i])) : largest;
+    }
+    largest = lanes_max<LANES>(largest);
+    const float tol = 2.f * half + largest * 0x1p-21f;
+    const float* const row = a.logits + token * a.stride;
+    auto score = [&](float v) {
+        return a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : softmax_part(v, top) / all;
+    };
+    auto exact = [&](int e) {
+        return score(row[e]) + (a.bias != nullptr ? (double)a.bias[e] : 0.0);
+    };
+    Choice<LANES, NL, decltype(exact)> choice = {a, c, tol, exact, i0};
     if (a.keep < a.parts) {
-        const int each = a.groups / a.parts;
-        // group p's value in lane p % LANES, at p / LANES
-        constexpr int V = kMaxExpertGroups / LANES;
-        double value[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            value[v] = kNoValue;
-        }
-        for (int p = 0; p < a.parts; ++p) {
-            double first = kNoValue, second = kNoValue;
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                const int e = i * LANES + i0;
-                const double x = e >= p * each && e < (p + 1) * each ? c[i] : kNoValue;
-                second = x > first ? first : x > second ? x : second;
-                first = x > first ? x : first;
-            }
-            const double best = lanes_max<LANES>(first);
-            const int holder = lanes_min<LANES>(first == best ? i0 : LANES);
-            const double next = lanes_max<LANES>(i0 == holder ? second : first);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (p == v * LANES + i0) {
-                    value[v] = next == kNoValue ? best : best + next;
-                }
-            }
-        }
-        uint64_t kept = 0;
-        for (int j = 0; j < a.keep; ++j) {
-            double best = kNoValue;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                best = value[v] > best ? value[v] : best;
-            }
-            best = lanes_max<LANES>(best);
-            int mine = 0x7fffffff;
-#pragma unroll
-            for (int v = V - 1; v >= 0; --v) {
-                mine = value[v] == best && best != kNoValue ? v * LANES + i0 : mine;
-            }
-            const int chosen = lanes_min<LANES>(mine);
-            kept |= chosen < kMaxExpertGroups ? 1ull << chosen : 0ull;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                value[v] = chosen == v * LANES + i0 ? kNoValue : value[v];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int e = i * LANES + i0;
-            c[i] = e < a.groups && (kept >> (e / each) & 1) ? c[i] : kNoValue;
-        }
+        choice.keep_groups();
     }
-#pragma unroll
-    for (int v = 0; v < C; ++v) {
-        id[v] = -1;
-    }
-    for (int j = 0; j < a.topk; ++j) {
-        double best = c[0];
-#pragma unroll
-        for (int i = 1; i < NL; ++i) {
-            best = c[i] > best ? c[i] : best;
-        }
-        best = lanes_max<LANES>(best);
-        if (__all(best == kNoValue)) {
-            break;                             // nothing left in any token
-        }
-        int mine = 0x7fffffff;
-#pragma unroll
-        for (int i = NL - 1; i >= 0; --i) {
-            mine = c[i] == best ? i * LANES + i0 : mine;
-        }
-        const int chosen = lanes_min<LANES>(mine);
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            c[i] = i * LANES + i0 == chosen ? kNoValue : c[i];
-        }
-#pragma unroll
-        for (int v = 0; v < C; ++v) {
-            id[v] = j == v * LANES + i0 && best != kNoValue ? chosen : id[v];
-        }
-    }
-    // each lane scores its own choices again
+    choice.take(id);
+    // each lane scores its own choices, in f64
     double s[C], sum = 0.0;
 #pragma unroll
     for (int v = 0; v < C; ++v) {
-        s[v] = id[v] < 0 ? 0.0 : score(a.logits[token * a.stride + id[v]]);
+        s[v] = 0.0;
+        if (v * LANES < a.topk && id[v] >= 0) {
+            s[v] = score(row[id[v]]);
+        }
         sum += s[v];
     }
     sum = a.renorm ? lanes_sum<LANES>(sum) : 1.0;
 #pragma unroll
     for (int v = 0; v < C; ++v) {
-        weight[v] = sum == 0.0 ? 0.f : (float)(s[v] / sum * (double)a.scale);
+        weight[v] = 0.f;
+        if (v * LANES < a.topk && sum != 0.0) {
+            weight[v] = (float)(s[v] / sum * (double)a.scale);
+        }
     }
 }
 

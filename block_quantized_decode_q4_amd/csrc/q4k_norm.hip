@@ -336,11 +336,37 @@ hipError_t launch_t(const NormArgs& a, hipStream_t stream)
 //   y = N(h; weight, bias)
 // N divides by sqrt(mean v^2 + eps), the layer norm after taking the mean off
 // (its squares are summed in a second step: a row far from zero loses nothing).
-// All sums and products in f64, as above; the same split: a workgroup per row,
-// groups of eight elements in registers from the loads to the outputs.
+// The same split as above: a workgroup per row, groups of eight elements in registers
+// from the loads to the outputs.  The sums are f64; the elements are f32, a power of
+// two s = about 1 / sqrt(..) taken out first, so that nothing overflows or vanishes:
+//   N = ((v s - mean s) r) weight + bias,   r sqrt(..) s = 1, mean s in two f32,
+// (v s is exact, its difference from the mean is rounded at its own size).
+//
+// What bounds it: the bytes.  4096 rows of 8192, binary16 in, residual in and out, binary16
+// out (402 MB): 87 us, 4.6 TB/s; a copy on this card runs at 5.1.  One row of 4096: 4.3 us,
+// two loads, two sums across waves and a store, one after the other.
 struct RowNorm {
-    double mean, r;
+    float s, high, low, r;
 };
+
+__device__ __forceinline__ RowNorm row_factors(double mean, double squares, const BlockNormArgs& a)
+{
+    const double r = 1.0 / __builtin_sqrt(squares / (double)a.k + (double)a.eps);
+    int power = 0;                             // of a zero, an infinity or NaN: any
+    (void)frexp(r, &power);
+    power = min(max(power, -126), 127);
+    RowNorm n;
+    n.s = __builtin_bit_cast(float, (uint32_t)max(power + 127, 1) << 23);
+    n.r = (float)ldexp(r, -power);
+    n.high = (float)(mean * (double)n.s);
+    n.low = (float)(mean * (double)n.s - (double)n.high);
+    return n;
+}
+
+__device__ __forceinline__ float normed(float v, const RowNorm& n)
+{
+    return (__builtin_fmaf(v, n.s, -n.high) - n.low) * n.r;
+}
 
 // The workgroup's sum of v (each thread's); `part` is this sum's own
 __device__ __forceinline__ double block_sum(double v, double* part, int waves)
@@ -359,28 +385,41 @@ __device__ __forceinline__ double block_sum(double v, double* part, int waves)
     return v;
 }
 
-// h of the group at column c from its x
+// The residual of the group at column c, zeros where there is none
 template <bool TAIL>
-__device__ __forceinline__ void block_h(const BlockNormArgs& a, int64_t row, int c, const float* x,
-                                        const RowNorm& n, float* h)
+__device__ __forceinline__ void block_residual(const BlockNormArgs& a, int64_t row, int c,
+                                               float* r)
 {
-    double p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        p[i] = (double)x[i];
+        r[i] = 0.f;
     }
-    float t[8];
+    if (a.residual != nullptr) {
+        load_f32<TAIL>(a, a.residual, row * a.k, c, r);
+    }
+}
+
+// h of the group at column c from its x and residual
+template <bool TAIL>
+__device__ __forceinline__ void block_h(const BlockNormArgs& a, int64_t row, int c, const float* x,
+                                        const float* r, const RowNorm& n, float* h)
+{
+    float p[8], t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i] = x[i];
+    }
     if (a.post_weight != nullptr) {
         load_f32<TAIL>(a, a.post_weight, 0, c, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            p[i] = (p[i] - n.mean) * n.r * (double)t[i];
+            p[i] = normed(p[i], n) * t[i];
         }
         if (a.post_bias != nullptr) {
             load_f32<TAIL>(a, a.post_bias, 0, c, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[i] += (double)t[i];
+                p[i] += t[i];
             }
         }
     }
@@ -388,19 +427,12 @@ __device__ __forceinline__ void block_h(const BlockNormArgs& a, int64_t row, int
         load_f32<TAIL>(a, a.gate, row * a.gate_stride, c, t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            p[i] *= (double)t[i];
+            p[i] *= t[i];
         }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        t[i] = 0.f;
-    }
-    if (a.residual != nullptr) {
-        load_f32<TAIL>(a, a.residual, row * a.k, c, t);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        h[i] = (float)__builtin_fma(p[i], (double)a.scale, (double)t[i]);
+        h[i] = __builtin_fmaf(p[i], a.scale, r[i]);
         if (TAIL && c + i >= a.k) {
             h[i] = 0.f;
         }
@@ -422,13 +454,14 @@ __device__ __forceinline__ void block_y(const BlockNormArgs& a, int64_t row, int
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        y[i] = (float)__builtin_fma(((double)h[i] - n.mean) * n.r, (double)w[i], (double)b[i]);
+        y[i] = __builtin_fmaf(normed(h[i], n), w[i], b[i]);
     }
     put_outputs<TAIL>(a, row, c, y);
 }
 
+// The residual is asked for with x.
 template <int TYPE, int P, bool TAIL>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, P == 1 ? 8 : 4)
 block_norm_kernel(BlockNormArgs a)
 {
     __shared__ double part[4][16];
@@ -473,26 +506,25 @@ block_norm_kernel(BlockNormArgs a)
         return block_sum(sum, place, waves);
     };
     auto row_norm = [&](const float (&v)[P][8], auto more, int which) {
-        RowNorm n = {0.0, 0.0};
+        double mean = 0.0;
         if (a.layer) {
-            n.mean = row_sum(v, more, part[2 * which], [](double e) { return e; }) / (double)a.k;
+            mean = row_sum(v, more, part[2 * which], [](double e) { return e; }) / (double)a.k;
         }
-        const double mean = n.mean;
         const double squares = row_sum(v, more, part[2 * which + 1],
                                        [mean](double e) { return (e - mean) * (e - mean); });
-        n.r = 1.0 / __builtin_sqrt(squares / (double)a.k + (double)a.eps);
-        return n;
+        return row_factors(mean, squares, a);
     };
 
-    float v[P][8];
+    float v[P][8], res[P][8];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int gi = p * threads + tid;
         if (gi < groups) {
             load_x(gi * 8, v[p]);
+            block_residual<TAIL>(a, row, gi * 8, res[p]);
         }
     }
-    RowNorm n = {0.0, 0.0};
+    RowNorm n = {1.f, 0.f, 0.f, 1.f};
     if (a.post_weight != nullptr) {
         n = row_norm(v, load_x, 0);
     }
@@ -501,7 +533,7 @@ block_norm_kernel(BlockNormArgs a)
     for (int p = 0; p < P; ++p) {
         const int gi = p * threads + tid;
         if (gi < groups) {
-            block_h<TAIL>(a, row, gi * 8, v[p], post, v[p]);
+            block_h<TAIL>(a, row, gi * 8, v[p], res[p], post, v[p]);
             if (a.sum != nullptr) {
                 put_f32<TAIL>(a, a.sum, row, gi * 8, v[p]);
             }
@@ -513,16 +545,18 @@ block_norm_kernel(BlockNormArgs a)
         if (a.sum != nullptr) {
             load_f32<TAIL>(a, a.sum, row * a.k, c, h);
         } else {
-            float x[8];
+            float x[8], r[8];
             load_x(c, x);
-            block_h<TAIL>(a, row, c, x, post, h);
+            block_residual<TAIL>(a, row, c, r);
+            block_h<TAIL>(a, row, c, x, r, post, h);
         }
     };
     if (a.sum != nullptr) {
         for (int gi = P * threads + tid; gi < groups; gi += threads) {
-            float x[8];
+            float x[8], r[8];
             load_x(gi * 8, x);
-            block_h<TAIL>(a, row, gi * 8, x, post, x);
+            block_residual<TAIL>(a, row, gi * 8, r);
+            block_h<TAIL>(a, row, gi * 8, x, r, post, x);
             put_f32<TAIL>(a, a.sum, row, gi * 8, x);
         }
     }
@@ -556,15 +590,29 @@ hipError_t launch_block_p(const BlockNormArgs& a, int threads, hipStream_t strea
     return hipGetLastError();
 }
 
+// Groups of eight per thread, by what was measured (us with one / two / four):
+//  - one for few rows (one row of 4096 4.3 / 4.6 / 5.8) and short ones (1000 rows of 2049
+//    15.7 / 16.0 / 17.4, 4096 of 2048 25.2 / 26.4 / 26.1);
+//  - two for many rows from 4096 elements on, whose workgroups, half as large, are in
+//    different phases of theirs (4096 rows of 8192 100 / 87 / 92, 4096 of 4095 65 / 56 /
+//    65, 2048 of 5120 34 / 31 / 34, 256 of 8192 9.6 / 9.1 / 10.2);
+//  - beyond 8192 elements two, or four for many rows (256 rows of 14336 - / 12.5 / 13.0,
+//    1024 rows - / 47 / 44); from 16384 on four.
 template <int TYPE>
 hipError_t launch_block_t(const BlockNormArgs& a, hipStream_t stream)
 {
     const int groups = (a.k - 1) / 8 + 1;
-    if (groups <= 1024) {
-        return launch_block_p<TYPE, 1>(a, (groups + 63) / 64 * 64, stream);
+    const auto threads = [&](int each) {
+        const int64_t t = ((int64_t)(groups - 1) / each + 1 + 63) / 64 * 64;
+        return (int)(t < 1024 ? t : 1024);
+    };
+    if (groups > 2048 || (groups > 1024 && a.m >= 1024)) {
+        return launch_block_p<TYPE, 4>(a, threads(4), stream);
     }
-    const int threads = a.m < 1024 ? 1024 : ((groups + 3) / 4 + 63) / 64 * 64;
-    return launch_block_p<TYPE, 4>(a, threads < 1024 ? threads : 1024, stream);
+    if (groups > 1024 || (groups >= 512 && a.m >= 256)) {
+        return launch_block_p<TYPE, 2>(a, threads(2), stream);
+    }
+    return launch_block_p<TYPE, 1>(a, threads(1), stream);
 }
 
 }  // namespace

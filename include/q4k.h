@@ -666,14 +666,14 @@ enum q4k_norm {
  *  sum_out   : device, m x k f32, gets h; NULL = not kept.  May be residual
  *              itself, or x when x is f32 and dense; no other overlap
  *  y, y16, q, d : as for q4k_rmsnorm, of the f32 y
- * At least one output.  m, k >= 1, eps >= 0 and finite.  All sums and products
- * in f64, h and y rounded once to f32: h is within 2^-23 (|residual| + |scale
- * gate p|) of the exact value, y within 2^-23 (|y| + |bias|) of the exact value
- * for the h that was rounded (2^-23 + 2^-40 k of it where a layer norm's mean is
- * 2^10 times its deviation).  A row of h with a NaN, or with an infinity in a
- * layer norm, gives NaN; with an infinity in an rms norm NaN there and its bias
- * (or 0) elsewhere; x likewise gives p.  Asynchronous on `stream`; allocates
- * nothing. */
+ * At least one output.  m, k >= 1, eps >= 0 and finite.  Sums in f64, elements in
+ * f32: h is within 2^-21 |scale gate| (|p - post_bias| + |post_bias|) + 2^-24
+ * |residual| of the exact value, y within 6 2^-24 (|y - bias| + |bias|) of the exact
+ * norm of the h that came out (a layer norm whose mean is m times its deviation
+ * 2^-48 m |weight| more).  A row of h with a NaN, or with an infinity in a layer
+ * norm, gives NaN; with an infinity in an rms norm NaN there and its bias (or 0)
+ * elsewhere; x likewise gives p; an all-zero row with eps = 0 gives NaN.
+ * Asynchronous on `stream`; allocates nothing. */
 int q4k_block_norm(const void* x, int x_type, int64_t x_stride, int kind,
                    const float* post_weight, const float* post_bias, const float* gate,
                    int64_t gate_stride, float scale, const float* residual, float* sum_out,
