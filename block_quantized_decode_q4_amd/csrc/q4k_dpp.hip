@@ -150,6 +150,8 @@ gemv_dot4_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
     const int ncg = ((S + 7) >> 3) / slabs_per_task;
     constexpr int kWaveRing = ANY ? kRing4Wave : kRingWave;
 
+    const auto early = fetch_y(y, tid < rows_here, row0 + tid, row0 + tid);
+
     // LDS: staged x (S columns), the line rings, row sums of slab groups
     const size_t xbytes = (size_t)S * kDotCol;
     unsigned char* ring = smem + xbytes + wave * kWaveRing;
@@ -249,7 +251,7 @@ gemv_dot4_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
         v += __shfl_xor(v, 32, 64);
         if (g == 0 && r < rows_here) {
             if (ncg == 1 && !parked(y)) {
-                put_y(y, row0 + r, row0 + r, v);
+                put_y(y, row0 + r, fetch_y(y, true, row0 + r, row0 + r), v);
             } else {
                 ypart[(task % ncg) * rows_per_block + r] = v;
             }
@@ -303,7 +305,8 @@ gemv_dot4_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ 
             for (int cg = 0; cg < ncg; ++cg) {
                 a += ypart[cg * rows_per_block + i];
             }
-            put_y(y, row0 + i, row0 + i, a);
+            const auto ops = i == tid ? early : fetch_y(y, true, row0 + i, row0 + i);
+            put_y(y, row0 + i, ops, a);
         }
     }
 }

@@ -63,18 +63,34 @@ __device__ __forceinline__ float activated(int act, float z)
     }
 }
 
-// y of element `at` from its z
-__device__ __forceinline__ float ep_value(const EpArgs& e, int64_t at, float z)
+// What an element's epilogue reads, asked for together
+struct EpOperands {
+    float bias, gate, residual;
+};
+
+// of element `at` of y and weight row `row` (both within their tensors)
+__device__ __forceinline__ EpOperands ep_fetch(const EpArgs& e, int64_t at, int64_t row)
 {
-    float v = activated(e.act, z);
+    EpOperands o = {0.f, 1.f, 0.f};
+    if (e.bias != nullptr) {
+        o.bias = e.bias[row];
+    }
     if (e.gate != nullptr) {
-        v *= e.gate_type == kTypeF16 ? (float)static_cast<const _Float16*>(e.gate)[at]
-                                     : static_cast<const float*>(e.gate)[at];
+        o.gate = e.gate_type == kTypeF16 ? (float)static_cast<const _Float16*>(e.gate)[at]
+                                         : static_cast<const float*>(e.gate)[at];
     }
     if (e.residual != nullptr) {
-        v += e.residual[at];
+        o.residual = e.residual[at];
     }
-    return v;
+    return o;
+}
+
+// y from its z (the bias added)
+__device__ __forceinline__ float ep_value(const EpArgs& e, const EpOperands& o, float z)
+{
+    float v = activated(e.act, z);
+    v = e.gate != nullptr ? v * o.gate : v;
+    return e.residual != nullptr ? v + o.residual : v;
 }
 
 __device__ __forceinline__ void ep_store(const EpArgs& e, int64_t at, float v)

@@ -118,13 +118,13 @@ f16_act_far_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict_
         return;
     }
     const auto xrow = [&](int i) { return x16 + (int64_t)max(x_row_of(rows, t, i), 0) * k; };
-    const float* const bias = ep.bias != nullptr ? ep.bias + (int64_t)t.group * n : nullptr;
     const auto put = [&](int i, auto each) {
         const int row = y_row_of(rows, t, i);
         if (row >= 0) {
             each([&](int c, float v) {
-                const float z = v + (bias != nullptr ? bias[c] : 0.f);
-                ep_store(ep, (int64_t)row * n + c, ep_value(ep, (int64_t)row * n + c, z));
+                const int64_t at = (int64_t)row * n + c;
+                const EpOperands o = ep_fetch(ep, at, (int64_t)t.group * n + c);
+                ep_store(ep, at, ep_value(ep, o, v + o.bias));
             });
         }
     };

@@ -203,8 +203,9 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
                     const float v = *reinterpret_cast<const float*>(
                         rows + at / (16 * T::FB) * T::kPitch + 4 * c);
                     const int64_t to = (int64_t)row * n + col0 + c;
+                    const EpOperands o = ep_fetch(ep, to, 0);
                     const float z = v + (bias != nullptr ? bias[col0 + c] : 0.f);
-                    ep_store(ep, to, ep_value(ep, to, z));
+                    ep_store(ep, to, ep_value(ep, o, z));
                 }
             }
             continue;

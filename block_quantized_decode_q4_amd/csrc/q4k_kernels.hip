@@ -218,7 +218,8 @@ gemv_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x, Out y,
                         const double v = wave_sum(acc[i][b]);
                         const int rl = g * R + i;
                         if (lane == 0 && rl < rows_here) {
-                            put_y(y, (size_t)b * n + row0 + rl, row0 + rl, v);
+                            const size_t at = (size_t)b * n + row0 + rl;
+                            put_y(y, at, fetch_y(y, true, at, row0 + rl), v);
                         }
                     }
                 }
@@ -380,6 +381,7 @@ gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
 
     float4* xs = reinterpret_cast<float4*>(smem);
     double* ypart = reinterpret_cast<double*>(xs + chunk_spans * 1024);
+    const auto early = fetch_y(y, tid < rows_here, row0 + tid, row0 + tid);
 
     for (int ch = 0; ch < nchunks; ++ch) {
         const int span0 = ch * chunk_spans;
@@ -470,7 +472,8 @@ gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             for (int sp = 0; sp < nspans; ++sp) {
                 acc += ypart[sp * rows_per_block + r];
             }
-            put_y(y, row0 + r, row0 + r, acc);
+            const auto ops = r == tid ? early : fetch_y(y, true, row0 + r, row0 + r);
+            put_y(y, row0 + r, ops, acc);
         }
     }
 }

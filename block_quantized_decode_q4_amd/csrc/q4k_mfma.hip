@@ -141,6 +141,9 @@ gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
     const int row0 = blockIdx.x * rows_per_block;
     const int rows_here = min(rows_per_block, n - row0);
     const int ncg = (S >> 3) / slabs_per_task;
+    const auto early = fetch_y(y, tid < rows_here * M,
+                               (size_t)(tid / rows_here) * n + row0 + tid % rows_here,
+                               row0 + tid % rows_here);
 
     // LDS: staged x (S columns of M vectors, column-major, and a spare
     // pair), the line rings, row sums (f64)
@@ -245,7 +248,8 @@ gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             v += __shfl_xor(v, 32, 64);
             if (g == 0 && r < rows_here) {
                 if (ncg == 1 && !parked(y)) {
-                    put_y(y, (size_t)b * n + row0 + r, row0 + r, v);
+                    const size_t at = (size_t)b * n + row0 + r;
+                    put_y(y, at, fetch_y(y, true, at, row0 + r), v);
                 } else {
                     ypart[(b * ncg + task % ncg) * rows_per_block + r] = v;
                 }
@@ -265,7 +269,8 @@ gemv_i8_lines_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             for (int cg = 0; cg < ncg; ++cg) {
                 a += ypart[(b * ncg + cg) * rows_per_block + r];
             }
-            put_y(y, (size_t)b * n + row0 + r, row0 + r, a);
+            const size_t at = (size_t)b * n + row0 + r;
+            put_y(y, at, i == tid ? early : fetch_y(y, true, at, row0 + r), a);
         }
     }
 }
@@ -567,6 +572,9 @@ gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
     const int row0 = blockIdx.x * rows_per_block;
     const int rows_here = min(rows_per_block, n - row0);
     const int ncg = ((S + 7) >> 3) / slabs_per_task;
+    const auto early = fetch_y(y, tid < rows_here * m,
+                               (size_t)(tid / rows_here) * n + row0 + tid % rows_here,
+                               row0 + tid % rows_here);
     const int k = S * 256;
     constexpr int kWaveRing = ANY ? kRing4Wave : kRingWave;
     constexpr uint32_t kWindow = ANY ? 511u : 255u;        // ring window of a row, minus one
@@ -910,7 +918,8 @@ gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             const int b = b4 + g;
             if (b < m && r < rows_here) {
                 if (ncg == 1 && !parked(y)) {
-                    put_y(y, (size_t)b * n + row0 + r, row0 + r, acc.at<q>());
+                    const size_t at = (size_t)b * n + row0 + r;
+                    put_y(y, at, fetch_y(y, true, at, row0 + r), acc.at<q>());
                 } else {
                     ypart[(b * ncg + task % ncg) * rows_per_block + r] = acc.at<q>();
                 }
@@ -957,7 +966,8 @@ gemv_i8_sub_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             for (int cg = 0; cg < ncg; ++cg) {
                 a += ypart[(b * ncg + cg) * rows_per_block + r];
             }
-            put_y(y, (size_t)b * n + row0 + r, row0 + r, a);
+            const size_t at = (size_t)b * n + row0 + r;
+            put_y(y, at, i == tid ? early : fetch_y(y, true, at, row0 + r), a);
         }
     }
 }
