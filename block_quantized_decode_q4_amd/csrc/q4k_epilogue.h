@@ -8,6 +8,12 @@
 //   gelu        z/2 erfc(-z / sqrt 2)
 //   gelu, tanh  z/2 (1 + tanh u) = z / (1 + e^-2u), u = sqrt(2/pi) (z + 0.044715 z^3)
 //   sigmoid     1 / (1 + e^-z)
+// e^x and 1 / x are the hardware's (a rounding or two each; the bound that the header
+// gives for act(z) allows for e^x's product, |z| 2^-24), erfc is the library's.
+//
+// Bound by nothing of its own: the operands are read once and y is written once, on the
+// way out of the product.  2048 x 14336 x 4096 with silu and a gate takes 240 us a call,
+// 1930 in separate operations in f32.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -1,6 +1,21 @@
 // q4k_f16_act.hip -- the prompts' products on fp16 mirrors with an epilogue:
 //   y = act(x W^T + bias) gate + residual,
-// dense or for rows grouped by matrix.
+// dense or for rows grouped by matrix.  The tile is q4k_f16_dma.h's; here are its
+// shapes, the order of the tiles and the choice between them.
+//
+// Measured (us a call among others; floor: a large matrix product's rate, 1.29
+// PFLOP/s, or the bytes):
+//   2048 x rows, 14336 x 4096, silu and a binary16 gate, out in binary16  237-243 (187):
+//     1.0 PFLOP/s, the matrix pipe busy 51 % of the launch
+//   2048 tokens, 2 of 8 experts of 14336 x 4096, the same epilogue  554-589 (373): 0.84
+//     PFLOP/s, busy 54 %; the groups' last tiles are part empty
+//   509 x rows, 4096 x 14336, bias and residual  97 (46): 256 workgroups of 128 x 64, one
+//     per CU, which take in 250 MB; busy 26 %, two thirds of the waves' time waiting to
+//     issue what waits for operands
+// What bounds the large ones: the operands' way into LDS.  A CU takes in about 31 B a
+// clock whatever the stages' size or number, so a tile's time per step is its operands'
+// bytes, and a tile as large as the accumulators allow is best; 256 x 256 (256 of them
+// per lane) made the compiler spill.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -134,7 +149,15 @@ f16_act_far_kernel(const _Float16* __restrict__ w16, const _Float16* __restrict_
 
 // --------------------------------------------------------------------- shapes
 // us of a round of the chip: per 64 of k, and beside them (one tile per CU, all CUs;
-// the operands mostly in the caches), as measured.
+// the operands mostly in the caches), as measured.  The choice takes the least sum over
+// the rounds that a call needs; it took the best of all six in each of these (us, silu and a
+// binary16 gate, in the order of the table):
+//   2048 x 14336 x 4096  252 / 234 / 279 / 400 / 379 / 534 (128 x 224: four full rounds)
+//   2048 x 4096 x 14336  212 / 354 / 269 / 379 / 334 / 483 (128 x 256: one full round)
+//   1000 x 4096 x 4096    56 /  89 /  38 /  53 /  51 /  61
+//   509 x 4096 x 14336   190 / 178 / 133 / 102 /  93 / 128 (256 tiles, the waves along k)
+//   200 x 7168 x 4096     47 /  43 /  30 /  23 /  23 /  30
+//   64 x 4096 x 4096      46 /  74 /  29 /  20 /  21 /  15
 struct ShapeCost {
     int bm, bn;
     bool deep;                         // steps of 128 of k, an even number of them

@@ -1,5 +1,17 @@
 // q4k_f16_dma.h -- a tile of y = act(x W^T + bias) gate + residual on fp16 mirrors,
 // its operands loaded straight into LDS.  Internal.
+//
+// Four waves, a ring of S stages of GK halves of k for both operands.  The loads go from
+// memory to LDS without registers on their way (which leaves them to the sums: 112 or
+// 128 of a lane's), S - 1 stages ahead, and are waited for by count; a barrier per stage.
+// Between the products of one 32 of k stand the LDS reads of the next, and in a stage's
+// last phase the loads that refill its place.  Pieces of 16 bytes are turned by their
+// row, so that reads have no conflicts (0.02 of the LDS's active cycles).
+// Against the same products with operands through registers (512 threads, two stages):
+// 2048 x 14336 x 4096 gated 373 -> 237 us, eight experts of 2048 tokens 849 -> 554,
+// 509 x 4096 x 14336 141 -> 97.
+// Tried without gain: stages of 32 of k, two workgroups a CU on 128 x 128 tiles, all loads
+// of a stage at its start, waves that load one operand each (97.5 us for 94 on the last).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,7 +31,8 @@ typedef _Float16 half8u_t __attribute__((ext_vector_type(8), aligned(2)));
 
 // 16 bytes from each lane's base + `from` (bytes) into LDS at `to` (bytes, the same
 // for the wave) plus 16 times the lane.  The wave waits for it with dma_wait alone:
-// the compiler does not know of it.  (M0 is the compiler's to set before each use.)
+// the compiler does not know of it.  (M0 is reserved: the compiler sets it before each
+// use of its own and keeps nothing there, and in these kernels has no use.)
 __device__ __forceinline__ void dma16(uint32_t to, uint32_t from, const void* base)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
@@ -203,7 +216,7 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
                     const float v = *reinterpret_cast<const float*>(
                         rows + at / (16 * T::FB) * T::kPitch + 4 * c);
                     const int64_t to = (int64_t)row * n + col0 + c;
-                    const EpOperands o = ep_fetch(ep, to, 0);
+                    const EpOperands o = ep_fetch(ep, to, 0);     // its bias is not used
                     const float z = v + (bias != nullptr ? bias[col0 + c] : 0.f);
                     ep_store(ep, to, ep_value(ep, o, z));
                 }

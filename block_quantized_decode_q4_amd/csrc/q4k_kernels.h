@@ -1,6 +1,5 @@
 // q4k_kernels.h -- internal interface between the C-ABI layer (q4k_api.hip)
-// and the kernels (q4k_kernels.hip, q4k_dpp.hip, q4k_mfma.hip, q4k_q8.hip,
-// q4k_q6k.hip, q4k_f16.hip).  Not installed, not part of the ABI.
+// and the kernels (the other .hip files).  Not installed, not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>

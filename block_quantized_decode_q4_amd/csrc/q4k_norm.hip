@@ -21,6 +21,8 @@
 // What bounds it: the bytes.  8192 rows of 4096, binary16 in, residual in and out,
 // binary16 out (402 MB): 73 us, 5.5 TB/s (a large copy on this card: 4.9).  One
 // row of 4096: 3.3 us, the latency of a load, the row's sum and a store.
+//
+// The norms on both sides of a block, and layer norms, are further down.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -343,7 +345,7 @@ hipError_t launch_t(const NormArgs& a, hipStream_t stream)
 // (v s is exact, its difference from the mean is rounded at its own size).
 //
 // What bounds it: the bytes.  4096 rows of 8192, binary16 in, residual in and out, binary16
-// out (402 MB): 87 us, 4.6 TB/s; a copy on this card runs at 5.1.  One row of 4096: 4.3 us,
+// out (402 MB): 80 us, 5.0 TB/s; a copy on this card runs at 5.1.  One row of 4096: 4.4 us,
 // two loads, two sums across waves and a store, one after the other.
 struct RowNorm {
     float s, high, low, r;
