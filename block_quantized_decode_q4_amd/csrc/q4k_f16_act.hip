@@ -10,12 +10,13 @@
 //   2048 tokens, 2 of 8 experts of 14336 x 4096, the same epilogue  554-589 (373): 0.84
 //     PFLOP/s, busy 54 %; the groups' last tiles are part empty
 //   509 x rows, 4096 x 14336, bias and residual  97 (46): 256 workgroups of 128 x 64, one
-//     per CU, which take in 250 MB; busy 26 %, two thirds of the waves' time waiting to
-//     issue what waits for operands
-// What bounds the large ones: the operands' way into LDS.  A CU takes in about 31 B a
-// clock whatever the stages' size or number, so a tile's time per step is its operands'
-// bytes, and a tile as large as the accumulators allow is best; 256 x 256 (256 of them
-// per lane) made the compiler spill.
+//     per CU, 5.5 MB of operands into each one's LDS; busy 26 %, two thirds of the waves'
+//     time waiting to issue
+// What bounds them: the operands' way into LDS.  A CU takes in about 31 B a clock at most,
+// whatever the stages' size or number, so a tile's time per step is its operands' bytes,
+// and a tile as large as the accumulators allow is best; 256 x 256 (256 of them per lane)
+// made the compiler spill.  Beside the steps a tile of 128 x 224 takes 13 us for its first
+// loads and its epilogue (52 of the 237 us), during which its CU multiplies nothing.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
