@@ -342,7 +342,8 @@ hipError_t launch_t(const NormArgs& a, hipStream_t stream)
 // from the loads to the outputs.  The sums are f64; the elements are f32, a power of
 // two s = about 1 / sqrt(..) taken out first, so that nothing overflows or vanishes:
 //   N = ((v s - mean s) r) weight + bias,   r sqrt(..) s = 1, mean s in two f32,
-// (v s is exact, its difference from the mean is rounded at its own size).
+// (v s is exact, its difference from the mean is rounded at its own size).  For a
+// constant row, whose root is eps's alone, s is smaller, so that mean s stays in f32.
 //
 // What bounds it: the bytes.  4096 rows of 8192, binary16 in, residual in and out, binary16
 // out (402 MB): 80 us, 5.0 TB/s; a copy on this card runs at 5.1.  One row of 4096: 4.4 us,
@@ -356,7 +357,12 @@ __device__ __forceinline__ RowNorm row_factors(double mean, double squares, cons
     const double r = 1.0 / __builtin_sqrt(squares / (double)a.k + (double)a.eps);
     int power = 0;                             // of a zero, an infinity or NaN: any
     (void)frexp(r, &power);
-    power = min(max(power, -126), 127);
+    // A mean more than 2^100 times sqrt(..) is that of a row whose elements are all the
+    // same (others deviate by 2^-24 / sqrt(k) of it at least): their difference is 0 at
+    // any scale.
+    int far = 0;                               // of an infinity or NaN: any
+    (void)frexp(mean, &far);
+    power = min(max(power, -126), mean == 0.0 ? 127 : min(100 - far, 127));
     RowNorm n;
     n.s = __builtin_bit_cast(float, (uint32_t)max(power + 127, 1) << 23);
     n.r = (float)ldexp(r, -power);
