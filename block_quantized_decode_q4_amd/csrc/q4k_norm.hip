@@ -344,6 +344,7 @@ hipError_t launch_t(const NormArgs& a, hipStream_t stream)
 //   N = ((v s - mean s) r) weight + bias,   r sqrt(..) s = 1, mean s in two f32,
 // (v s is exact, its difference from the mean is rounded at its own size).  For a
 // constant row, whose root is eps's alone, s is smaller, so that mean s stays in f32.
+// An h that is not finite is formed again with its products in f64 (block_h_far).
 //
 // What bounds it: the bytes.  4096 rows of 8192, binary16 in, residual in and out, binary16
 // out (402 MB): 80 us, 5.0 TB/s; a copy on this card runs at 5.1.  One row of 4096: 4.4 us,
@@ -407,8 +408,44 @@ __device__ __forceinline__ void block_residual(const BlockNormArgs& a, int64_t r
     }
 }
 
+// h of the elements that are not finite, again, its products in f64: a product of x, the
+// weight or the gate may have passed f32 although h does not.  One element at a time
+// and from memory: few rows come here, and the others keep their registers.
+template <int TYPE>
+__device__ __forceinline__ void block_h_far(const BlockNormArgs& a, int64_t row, int c,
+                                            const RowNorm& n, float* h)
+{
+    if (!(n.r < __builtin_inff())) {
+        return;                                // x's norm is NaN throughout
+    }
+    uint32_t lost = 0;                         // never an element behind the row's end
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lost |= fabsf(h[i]) < __builtin_inff() ? 0u : 1u << i;
+    }
+    for (; lost != 0; lost &= lost - 1) {
+        const int i = __builtin_ctz(lost);
+        const int at = c + i;
+        const float x = element<TYPE>(a.x, row * a.x_stride + at);
+        double p = x;
+        if (a.post_weight != nullptr) {
+            p = (double)normed(x, n) * (double)a.post_weight[at];
+            p = a.post_bias != nullptr ? p + (double)a.post_bias[at] : p;
+        }
+        if (a.gate != nullptr) {
+            p *= (double)a.gate[row * a.gate_stride + at];
+        }
+        const double r = a.residual != nullptr ? (double)a.residual[row * a.k + at] : 0.0;
+        const float value = (float)__builtin_fma(p, (double)a.scale, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = e == i ? value : h[e];
+        }
+    }
+}
+
 // h of the group at column c from its x and residual
-template <bool TAIL>
+template <int TYPE, bool TAIL>
 __device__ __forceinline__ void block_h(const BlockNormArgs& a, int64_t row, int c, const float* x,
                                         const float* r, const RowNorm& n, float* h)
 {
@@ -444,6 +481,15 @@ __device__ __forceinline__ void block_h(const BlockNormArgs& a, int64_t row, int
         if (TAIL && c + i >= a.k) {
             h[i] = 0.f;
         }
+    }
+    // an infinity or NaN among them: their sum of products with 0 is NaN
+    float none = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        none = __builtin_fmaf(h[i], 0.f, none);
+    }
+    if (__builtin_expect(__any(none != 0.f), 0)) {
+        block_h_far<TYPE>(a, row, c, n, h);
     }
 }
 
@@ -541,7 +587,7 @@ block_norm_kernel(BlockNormArgs a)
     for (int p = 0; p < P; ++p) {
         const int gi = p * threads + tid;
         if (gi < groups) {
-            block_h<TAIL>(a, row, gi * 8, v[p], res[p], post, v[p]);
+            block_h<TYPE, TAIL>(a, row, gi * 8, v[p], res[p], post, v[p]);
             if (a.sum != nullptr) {
                 put_f32<TAIL>(a, a.sum, row, gi * 8, v[p]);
             }
@@ -556,7 +602,7 @@ block_norm_kernel(BlockNormArgs a)
             float x[8], r[8];
             load_x(c, x);
             block_residual<TAIL>(a, row, c, r);
-            block_h<TAIL>(a, row, c, x, r, post, h);
+            block_h<TYPE, TAIL>(a, row, c, x, r, post, h);
         }
     };
     if (a.sum != nullptr) {
@@ -564,7 +610,7 @@ block_norm_kernel(BlockNormArgs a)
             float x[8], r[8];
             load_x(gi * 8, x);
             block_residual<TAIL>(a, row, gi * 8, r);
-            block_h<TAIL>(a, row, gi * 8, x, r, post, x);
+            block_h<TYPE, TAIL>(a, row, gi * 8, x, r, post, x);
             put_f32<TAIL>(a, a.sum, row, gi * 8, x);
         }
     }

@@ -651,7 +651,7 @@ enum q4k_norm {
 
 /* The norms on both sides of a residual's addition, in one call:
  *   p = N(x; post_weight, post_bias)          (x where post_weight is NULL)
- *   h = residual + scale * gate * p           (f32, rounded once)
+ *   h = residual + scale * gate * p           (f32)
  *   y = N(h; weight, bias)                    per row of k elements
  *  x         : device, m rows of k elements of x_type, x_stride elements from
  *              row to row (0 = k; at least k otherwise): the block's output
@@ -668,7 +668,8 @@ enum q4k_norm {
  *  y, y16, q, d : as for q4k_rmsnorm, of the f32 y
  * At least one output.  m, k >= 1, eps >= 0 and finite.  Sums in f64, elements in
  * f32: h is within 2^-21 |scale gate| (|p - post_bias| + |post_bias|) + 2^-24
- * |residual| of the exact value, y within 6 2^-24 (|y - bias| + |bias|) of the exact
+ * |residual| of the exact value (p and its products may pass f32 where h does not;
+ * what lies below f32 adds 2^-146 (|scale| + |scale gate|)), y within 6 2^-24 (|y - bias| + |bias|) of the exact
  * norm of the h that came out (a layer norm whose mean is m times its deviation
  * 2^-48 m |weight| more).  A row of h with a NaN, or with an infinity in a layer
  * norm, gives NaN; with an infinity in an rms norm NaN there and its bias (or 0)
