@@ -669,11 +669,13 @@ enum q4k_norm {
  * At least one output.  m, k >= 1, eps >= 0 and finite.  Sums in f64, elements in
  * f32: h is within 2^-21 |scale gate| (|p - post_bias| + |post_bias|) + 2^-24
  * |residual| of the exact value (p and its products may pass f32 where h does not;
- * what lies below f32 adds 2^-146 (|scale| + |scale gate|)), y within 6 2^-24 (|y - bias| + |bias|) of the exact
- * norm of the h that came out (a layer norm whose mean is m times its deviation
- * 2^-48 m |weight| more).  A row of h with a NaN, or with an infinity in a layer
- * norm, gives NaN; with an infinity in an rms norm NaN there and its bias (or 0)
- * elsewhere; x likewise gives p; an all-zero row with eps = 0 gives NaN.
+ * what lies below f32 adds 2^-146 (|scale| + |scale gate|)), y within
+ * 6 2^-24 (|y - bias| + |bias|) of the exact norm of the h that came out.  A layer
+ * norm of a row whose mean is m times its deviation adds 2^-48 m |weight| to y,
+ * 2^-48 m |scale gate post_weight| to h.  A row of h with a NaN, or with an infinity
+ * in a layer norm, gives NaN; with an infinity in an rms norm NaN there and its bias
+ * (or 0) elsewhere; x likewise gives p; with eps = 0 an all-zero row, and a constant
+ * one in a layer norm, gives NaN.
  * Asynchronous on `stream`; allocates nothing. */
 int q4k_block_norm(const void* x, int x_type, int64_t x_stride, int kind,
                    const float* post_weight, const float* post_bias, const float* gate,
