@@ -370,7 +370,9 @@ struct Choice {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (p == v * LANES + i0) {
-                    value[v] = second == kNone ? first : first + second;
+                    // a sum below f32's lowest is still a value
+                    value[v] = second == kNone ? first
+                                               : fmaxf(first + second, -0x1.fffffep127f);
                 }
             }
         };
