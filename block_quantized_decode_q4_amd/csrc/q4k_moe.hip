@@ -315,15 +315,24 @@ __device__ __forceinline__ void lanes_two(float& first, float& second)
     }
 }
 
-// A token's choice (its 16 or 64 lanes).  c: the values in f32, off by less than tol /
-// 2, experts i LANES + lane; exact(e): expert e's in f64.
+// A token's choice (its 16 or 64 lanes).  c: the values in f32, experts i LANES + lane, a
+// value c off by less than half + 2^-24 |c|; exact(e): expert e's in f64.  Margins go by
+// the sizes of the values that are compared, so that an expert with a far bias (one that
+// is kept out by -1e9, say) does not widen them for the others.
 template <int LANES, int NL, typename Exact>
 struct Choice {
     const BiasedRouteArgs& a;
     float (&c)[NL];
-    float tol;
+    float half;
     Exact exact;
     int i0;
+
+    // What is below this lies below v in f64 too, whatever its size: for two values d
+    // apart, the smaller at most |v| + d in size, the errors are 2 half + 2^-23 |v| + 2^-24 d
+    __device__ __forceinline__ float edge(float v) const
+    {
+        return v == -kNone ? v : v - (2.5f * half + 0x1p-21f * fabsf(v));
+    }
 
     // This lane's experts among `some` (bits): the best in f64, ties to the lowest, or
     // with second its two best
@@ -359,20 +368,19 @@ struct Choice {
     __device__ __forceinline__ void keep_groups()
     {
         const int each = a.groups / a.parts;
-        // group p's value in lane p % LANES, at p / LANES
+        // group p's two largest values in lane p % LANES, at p / LANES
         constexpr int V = kMaxExpertGroups / LANES;
-        float value[V];
+        float one[V], two[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            value[v] = kNone;
+            one[v] = two[v] = kNone;
         }
         auto put = [&](int p, float first, float second) __attribute__((always_inline)) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (p == v * LANES + i0) {
-                    // a sum below f32's lowest is still a value
-                    value[v] = second == kNone ? first
-                                               : fmaxf(first + second, -0x1.fffffep127f);
+                    one[v] = first;
+                    two[v] = second;
                 }
             }
         };
@@ -397,11 +405,18 @@ struct Choice {
                 put(p, first, second);
             }
         }
-        // the keep-th largest value: as many steps of the largest that is left
-        float left[V], least = kNone, most = kNone;
+        // a group's value (a sum that passes f32 is still one), and more than it can be off
+        // by: the two summands' errors and the sum's rounding; an infinite one is exact.  (An
+        // error grows with a value's size, so the two largest in f32 bound the two in f64.)
+        float value[V], off[V], left[V], low = -kNone, high = kNone;
         uint64_t kept = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            const float other = two[v] == kNone ? 0.f : two[v];
+            const bool finite = fabsf(one[v]) < -kNone;
+            const float most = 0x1.fffffep127f;
+            value[v] = finite ? fminf(fmaxf(one[v] + other, -most), most) : one[v];
+            off[v] = finite ? 2.5f * half + 0x1p-22f * fabsf(one[v]) + 0x1p-22f * fabsf(other) : 0.f;
             left[v] = value[v];
         }
         for (int j = 0; j < a.keep; ++j) {
@@ -418,45 +433,59 @@ struct Choice {
             }
             const int chosen = lanes_min<LANES>(mine);
             kept |= chosen < kMaxExpertGroups ? 1ull << chosen : 0ull;
-            least = chosen < kMaxExpertGroups ? best : least;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 left[v] = chosen == v * LANES + i0 ? kNone : left[v];
             }
         }
+        // the least that one of them can be, and the most that another can be
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            most = fmaxf(most, left[v]);
+            if (left[v] != kNone) {
+                high = fmaxf(high, value[v] + off[v]);
+            } else if (value[v] != kNone) {
+                low = fminf(low, value[v] - off[v]);
+            }
         }
-        most = lanes_max<LANES>(most);         // of those that do not stay
-        const bool close = most != kNone && !(least - most > 2.f * tol);
+        low = -lanes_max<LANES>(-low);
+        high = lanes_max<LANES>(high);
+        const bool close = high != kNone && !(low > high);
         if (__any(close)) {
-            // groups whose sums f32 does not tell from the last one that stays: in f64
+            // which groups stay (above all that did not) and which are to be told apart in
+            // f64 (not below all that did): bits
+            uint64_t above = 0, among = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const bool has = close && value[v] != kNone;
+                const bool stays = has && value[v] - off[v] > high;
+                const uint64_t s = __ballot(stays);
+                const uint64_t n = __ballot(has && !stays && !(value[v] + off[v] < low));
+                if constexpr (LANES == 64) {
+                    above = s;
+                    among = n;
+                } else {
+                    const int shift = threadIdx.x & 48;          // the token's lanes
+                    above |= (s >> shift & 0xFFFF) << (v * LANES);
+                    among |= (n >> shift & 0xFFFF) << (v * LANES);
+                }
+            }
             double near[V];
-            int sure = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 near[v] = kNoValue;
             }
             for (int p = 0; p < a.parts; ++p) {
-                float mine = kNone;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    mine = p == v * LANES + i0 ? value[v] : mine;
-                }
-                mine = lanes_max<LANES>(mine);
-                const bool above = mine != kNone && mine > least + 2.f * tol;
-                const bool in = close && mine != kNone && !above && !(mine < least - 2.f * tol);
-                sure += above ? 1 : 0;
+                const bool in = among >> p & 1;
                 if (__any(in)) {
                     float first, second;
                     group_two(p, each, first, second);
+                    const float least = edge(second);
                     uint32_t some = 0;
 #pragma unroll
                     for (int i = 0; i < NL; ++i) {
                         const int e = i * LANES + i0;
                         const bool has = in && e >= p * each && e < (p + 1) * each &&
-                                         c[i] != kNone && !(c[i] < second - tol);
+                                         c[i] != kNone && !(c[i] < least);
                         some |= has ? 1u << i : 0u;
                     }
                     double f, s;
@@ -473,19 +502,9 @@ struct Choice {
                     }
                 }
             }
-            // those above stay, and the largest of the close ones, ties to the lowest
-            if (close) {
-                kept = 0;
-            }
-            for (int p = 0; p < a.parts; ++p) {
-                float mine = kNone;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    mine = p == v * LANES + i0 ? value[v] : mine;
-                }
-                mine = lanes_max<LANES>(mine);
-                kept |= close && mine != kNone && mine > least + 2.f * tol ? 1ull << p : 0ull;
-            }
+            // those above stay, and the largest of the others, ties to the lowest
+            const int sure = __popcll(above);
+            kept = close ? above : kept;
             for (int j = 0; j < a.keep; ++j) {
                 double best = kNoValue;
 #pragma unroll
@@ -545,13 +564,13 @@ struct Choice {
                 break;                         // nothing left in any token
             }
             // the lowest expert with it, and whether others come near
-            const float edge = best - tol;
+            const float least = edge(best);
             int mine = 0x7fffffff;
             int many = 0;
 #pragma unroll
             for (int i = NL - 1; i >= 0; --i) {
                 mine = c[i] == best ? i * LANES + i0 : mine;
-                many += c[i] < edge ? 0 : 1;   // an edge that is NaN: all
+                many += c[i] < least ? 0 : 1;
             }
             int chosen = lanes_min<LANES>(mine);
             // a lane with one, if it is the chosen, stands alone
@@ -563,7 +582,7 @@ struct Choice {
                 uint32_t some = 0;
 #pragma unroll
                 for (int i = 0; i < NL; ++i) {
-                    some |= unsure && c[i] != kNone && !(c[i] < edge) ? 1u << i : 0u;
+                    some |= unsure && c[i] != kNone && !(c[i] < least) ? 1u << i : 0u;
                 }
                 double f, s;
                 int at;
@@ -601,8 +620,7 @@ __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t t
     }
     // Scores in f32.  The exp is off by (1.5 |x| + 2) steps of 2^-24, so a sigmoid by
     // less than 4 of them; a softmax's score by less than (NL + 8) steps of the largest
-    // score (its sum's roundings; x e^-x < 1).  half: no less than that; tol: twice that
-    // and more than the roundings of the bias's addition.
+    // score (its sum's roundings; x e^-x < 1).  half: no less than that.
     float c[NL], half = 0x1p-22f;
     double all = 1.0;
     if (a.sigmoid) {
@@ -630,15 +648,11 @@ __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t t
         }
         all = lanes_sum<LANES>(sum64);
     }
-    float largest = 0.f;
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
         const bool in = l[i] != kNone && b[i] == b[i] && b[i] != kNone;
         c[i] = in ? c[i] + b[i] : kNone;
-        largest = in ? fmaxf(largest, fabsf(c[i])) : largest;
     }
-    largest = lanes_max<LANES>(largest);
-    const float tol = 2.f * half + largest * 0x1p-21f;
     const float* const row = a.logits + token * a.stride;
     auto score = [&](float v) {
         return a.sigmoid ? 1.0 / (1.0 + exp(-(double)v)) : softmax_part(v, top) / all;
@@ -646,7 +660,7 @@ __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t t
     auto exact = [&](int e) {
         return score(row[e]) + (a.bias != nullptr ? (double)a.bias[e] : 0.0);
     };
-    Choice<LANES, NL, decltype(exact)> choice = {a, c, tol, exact, i0};
+    Choice<LANES, NL, decltype(exact)> choice = {a, c, half, exact, i0};
     if (a.keep < a.parts) {
         choice.keep_groups();
     }

@@ -53,3 +53,49 @@ def test_groups_whose_values_pass_f32(m, E, topk, parts, keep, sigmoid):
         bias[E // 2] = np.nan                  # a group with an expert kept out
         print("values", name, m, E, topk, parts, keep, sigmoid, flush=True)
         _check(logits, bias, sigmoid, parts, keep, topk, True, 1.0)
+
+
+CHOICES = [(16, 64, 6, 1, 1), (9, 200, 8, 1, 1), (600, 64, 8, 8, 4), (900, 256, 8, 8, 4),
+           (40, 512, 6, 16, 5), (6, 1024, 32, 1, 1), (50, 48, 5, 24, 7)]
+
+
+@pytest.mark.parametrize("m,E,topk,parts,keep", CHOICES)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_far_biases_among_others(m, E, topk, parts, keep, sigmoid, renorm):
+    """Experts far out of the others' range, either way: they are chosen first or last
+    and the others' order is that of their own values."""
+    rng = np.random.default_rng(E + topk)
+    logits = _logits(rng, m, E)
+    scale = 0.2 if sigmoid else 0.5 / E
+    near = (rng.standard_normal(E) * scale).astype(np.float32)
+    near[::2] = near[0]                        # equal values among them
+    at = rng.permutation(E)
+    for far in (-1e9, -1e30, LOWEST, 1e6, 1e30, -LOWEST, np.inf, -np.inf):
+        for count in (1, 3, E // 2):
+            bias = near.copy()
+            bias[at[:count]] = far
+            print("far", far, count, m, E, topk, parts, keep, sigmoid, renorm, flush=True)
+            _check(logits, bias, sigmoid, parts, keep, topk, renorm, 1.5)
+    bias = near.copy()                         # several sizes at once
+    bias[at[:6]] = [-1e9, 1e6, -300.0, 2e3, -LOWEST, LOWEST]
+    _check(logits, bias, sigmoid, parts, keep, topk, renorm, 1.5)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_groups_that_meet_in_their_sums(sigmoid):
+    """Groups whose largest values are far apart and whose sums are near: a value off by
+    its own size's rounding, not by the others'."""
+    rng = np.random.default_rng(11)
+    E, parts = 64, 8
+    logits = _logits(rng, 30, E)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32) - 50
+    for p in range(parts):                     # sums of 1 and a little, from summands of all sizes
+        size = np.float32(4.0 ** p)
+        bias[8 * p + 1] = size
+        bias[8 * p + 5] = np.float32(1 + rng.random() * 2.0 ** -20) - size
+    for keep in range(1, parts + 1):
+        _check(logits, bias, sigmoid, parts, keep, min(6, 8 * keep), True, 1.0)
+    logits[:, :] = 0.25                        # and the scores the same
+    for keep in range(1, parts + 1):
+        _check(logits, bias, sigmoid, parts, keep, min(6, 8 * keep), True, 1.0)
