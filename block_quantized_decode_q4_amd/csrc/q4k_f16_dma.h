@@ -19,6 +19,7 @@
 
 #include <type_traits>
 
+#include "q4k_device.h"
 #include "q4k_epilogue.h"
 #include "q4k_f16_tile.h"
 
@@ -191,6 +192,7 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
 #pragma unroll 1
     for (int blk = 0; blk < NA; ++blk) {
         if (blk % kBlocks == 0) {
+            wave_lds_order();                            // behind the reads of the blocks before
             unrolled<0, (NA + kBlocks - 1) / kBlocks>([&](auto cc) __attribute__((always_inline)) {
                 constexpr int c = decltype(cc)::value;
                 if (blk == c * kBlocks) {
@@ -205,6 +207,7 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
                     }
                 }
             });
+            wave_lds_order();                            // other lanes read what a lane wrote
         }
         const unsigned char* const rows = part + blk % kBlocks * 16 * T::kPitch;
         if (!inside) {
