@@ -92,17 +92,15 @@ struct DmaShape {
     static constexpr int kPitch = BN / WN * 4 + 16;      // LDS bytes of an epilogue row
     static constexpr int kLds = S * kStage;
     static constexpr int kPart = kLds / 4 / 16 * 16;     // a wave's part of it
-    // x rows of a wave that its part holds, in whole blocks
-    static constexpr int kFit = kPart / (16 * kPitch);
-    static constexpr int kBlocks = kFit < FA ? kFit : FA;
     static_assert(WM * WN * KW == 4, "four waves");
-    static_assert(kFit >= 1 && kLds <= 160 * 1024, "LDS");
+    static_assert(kLds <= 160 * 1024, "LDS");
+    static_assert(FA / KW * 16 * kPitch <= kPart, "the rows that a wave writes out");
 };
 
 // ---------------------------------------------------------------- the epilogue
 // A wave's sums, NA x FB blocks (lane 16 g + j of a block: x row j, columns 4 g ..
-// 4 g + 3), go out by rows: through its part of the LDS, kBlocks blocks of rows at a
-// time, so that neighbouring lanes hold neighbouring columns, eight each.  The gate
+// 4 g + 3), go out by rows: through its part of the LDS, so that neighbouring lanes hold
+// neighbouring columns, eight each.  The gate
 // and residual of the next 16 rows are on their way while 16 rows are computed: a row
 // that is not written reads another's.  Columns that pass n go out one by one.
 struct Eight {
@@ -144,7 +142,6 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
     constexpr int kLanes = 2 * T::FB;                    // lanes per row
     constexpr int kAt = kLanes <= 8 ? 8 : 4;             // rows at a time
     constexpr int IT = 16 / kAt;
-    constexpr int kBlocks = T::kBlocks;
     static_assert(kAt * kLanes <= 64, "a wave's lanes");
     const int lane = threadIdx.x & 63;
     const int g = lane >> 4;
@@ -189,27 +186,18 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
             fetch(min(q, NA - 1), way[q]);
         }
     }
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+#pragma unroll
+        for (int b = 0; b < T::FB; ++b) {
+            *reinterpret_cast<f32x4_t*>(part + (a * 16 + j) * T::kPitch + (16 * b + 4 * g) * 4) =
+                acc[a][b];
+        }
+    }
+    wave_lds_order();                                    // other lanes read what a lane wrote
 #pragma unroll 1
     for (int blk = 0; blk < NA; ++blk) {
-        if (blk % kBlocks == 0) {
-            wave_lds_order();                            // behind the reads of the blocks before
-            unrolled<0, (NA + kBlocks - 1) / kBlocks>([&](auto cc) __attribute__((always_inline)) {
-                constexpr int c = decltype(cc)::value;
-                if (blk == c * kBlocks) {
-#pragma unroll
-                    for (int a = c * kBlocks; a < (c + 1) * kBlocks && a < NA; ++a) {
-#pragma unroll
-                        for (int b = 0; b < T::FB; ++b) {
-                            *reinterpret_cast<f32x4_t*>(part +
-                                                        ((a - c * kBlocks) * 16 + j) * T::kPitch +
-                                                        (16 * b + 4 * g) * 4) = acc[a][b];
-                        }
-                    }
-                }
-            });
-            wave_lds_order();                            // other lanes read what a lane wrote
-        }
-        const unsigned char* const rows = part + blk % kBlocks * 16 * T::kPitch;
+        const unsigned char* const rows = part + blk * 16 * T::kPitch;
         if (!inside) {
             // element by element: lane l takes every 64th
             for (int at = lane; at < 16 * 16 * T::FB; at += 64) {
@@ -287,7 +275,8 @@ __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], in
 template <int GK>
 __device__ __forceinline__ int dma_turn(int row)
 {
-    return GK == 32 ? row >> 1 & 3 : GK == 64 ? row & 7 : row & 15;
+    static_assert(GK == 64 || GK == 128, "the stages' depth");
+    return GK == 64 ? row & 7 : row & 15;
 }
 
 // xoff(i): where the tile's x row i (i < BM) begins, in bytes behind x; yrow(i): its y row, -1 where
