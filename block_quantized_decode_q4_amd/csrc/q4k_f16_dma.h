@@ -34,6 +34,10 @@ typedef _Float16 half8u_t __attribute__((ext_vector_type(8), aligned(2)));
 // for the wave) plus 16 times the lane.  The wave waits for it with dma_wait alone:
 // the compiler does not know of it.  (M0 is reserved: the compiler sets it before each
 // use of its own and keeps nothing there, and in these kernels has no use.)
+// The compiler also does not count the wait states that such instructions need behind a
+// vector write: five for the base's scalar registers here (they come from scalar
+// additions), two for a product's operands below (they come from LDS reads).
+// tests/inline_waits.py looks for each of these in the code as it was built.
 __device__ __forceinline__ void dma16(uint32_t to, uint32_t from, const void* base)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
