@@ -1487,12 +1487,13 @@ int q4k_gemv_act(const void* w, const float* x, const q4k_epilogue* epilogue, in
     }
     // the sums meet in LDS (in f64) before the epilogue; kernels that put them
     // there to add up their parts have the room, others need it unless it does
-    // not fit
+    // not fit (kernel 2, 512 rows a workgroup at most, always: it has no other way)
     const bool whole = plan.kernel == 2   ? plan.nspans == 1
                        : plan.kernel >= 3 ? (plan.S + 7) / 8 * 8 == plan.cols_per_task
                                           : false;
     const size_t sums = (size_t)plan.rows_per_block * plan.m * 8;
-    ep.parked = plan.kernel >= 2 && (!whole || plan.lds_bytes + sums <= lds_max);
+    ep.parked = plan.kernel == 2 ||
+                (plan.kernel >= 3 && (!whole || plan.lds_bytes + sums <= lds_max));
     if (whole && ep.parked) {
         plan.lds_bytes += sums;
     }

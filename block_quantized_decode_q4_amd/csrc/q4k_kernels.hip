@@ -430,10 +430,11 @@ gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             }
             // y (global) or the per-span row sums (LDS): two typed pointers, so
             // that neither store becomes a flat access, which would make the
-            // compiler drain the prefetched loads at every row
+            // compiler drain the prefetched loads at every row (with an epilogue
+            // there is the second one alone: no y to point at)
             float* yout = direct_y(y) + row0 + rb;
             double* pout = ypart + span * rows_per_block + rb;
-            const bool direct = nspans == 1 && !parked(y);
+            const bool direct = !kEpilogue && nspans == 1;
             int t = 0;
             for (; t + P <= T; t += P) {
 #pragma unroll
@@ -465,7 +466,7 @@ gemv_stream_kernel(const uint8_t* __restrict__ w, const float* __restrict__ x,
             }
         }
     }
-    if (nspans > 1 || parked(y)) {
+    if (kEpilogue || nspans > 1) {
         __syncthreads();
         for (int r = tid; r < rows_here; r += NW * 64) {
             double acc = 0.0;
