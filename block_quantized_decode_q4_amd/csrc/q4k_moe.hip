@@ -618,9 +618,11 @@ __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t t
         l[i] = l[i] == l[i] ? l[i] : kNone;
         top = fmaxf(top, l[i]);
     }
-    // Scores in f32.  The exp is off by (1.5 |x| + 2) steps of 2^-24, so a sigmoid by
-    // less than 4 of them; a softmax's score by less than (NL + 8) steps of the largest
-    // score (its sum's roundings; x e^-x < 1).  half: no less than that.
+    // Scores in f32, in steps of 2^-24.  e^x is off by 1.25 |x| + 2 of itself, so a sigmoid
+    // by less than 4.  A softmax's e^(l - top) is off by 2.25 |x| + 2, the subtraction's
+    // rounding among them: at most 12 of a sum of 1024 (most where 1023 are at x = -5.5),
+    // whose additions are NL + 5 more, the share and its product 2, the value's own 2: less
+    // than NL + 22 steps of the largest score.  half: no less than that.
     float c[NL], half = 0x1p-22f;
     double all = 1.0;
     if (a.sigmoid) {
@@ -638,7 +640,7 @@ __device__ __forceinline__ void route_tokens(const BiasedRouteArgs& a, int64_t t
             sum += c[i];
         }
         const float share = 1.f / lanes_sum<LANES>(sum);
-        half = share * 0x1p-19f;
+        half = share * 0x1.4p-19f;
         // where weights are shares of all experts' scores, and where f64 decides
         double sum64 = 0.0;
 #pragma unroll

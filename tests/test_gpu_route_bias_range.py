@@ -99,3 +99,21 @@ def test_groups_that_meet_in_their_sums(sigmoid):
     logits[:, :] = 0.25                        # and the scores the same
     for keep in range(1, parts + 1):
         _check(logits, bias, sigmoid, parts, keep, min(6, 8 * keep), True, 1.0)
+
+
+@pytest.mark.parametrize("E,parts,keep", [(64, 1, 1), (64, 8, 3), (256, 1, 1), (256, 8, 4),
+                                          (512, 16, 5), (1024, 1, 1), (1024, 64, 9)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_values_that_meet_through_their_biases(E, parts, keep, sigmoid):
+    """Biases that take every score to the same value but for the biases' own rounding,
+    1e-8 of it: an error that f32's scores have in common, of the sum of all, counts
+    in each by its score's size."""
+    rng = np.random.default_rng(E + parts)
+    for spread in (0.5, 2.0, 6.0):
+        logits = (rng.standard_normal((1, E)) * spread).astype(np.float32)
+        logits[0, 0] = 5.5 if spread == 0.5 else 3 * spread
+        l = logits[0].astype(np.float64)
+        s = 1 / (1 + np.exp(-l)) if sigmoid else np.exp(l - l.max()) / np.exp(l - l.max()).sum()
+        bias = (s.max() - s).astype(np.float32)
+        _check(logits, bias, sigmoid, parts, keep, 8, True, 1.0)
+        _check(np.repeat(logits, 400, 0), bias, sigmoid, parts, keep, 8, False, 1.0)
