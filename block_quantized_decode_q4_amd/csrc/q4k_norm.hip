@@ -513,9 +513,9 @@ __device__ __forceinline__ void block_y(const BlockNormArgs& a, int64_t row, int
     put_outputs<TAIL>(a, row, c, y);
 }
 
-// The residual is asked for with x.
+// The residual is asked for with x.  Registers for eight waves a SIMD where they suffice.
 template <int TYPE, int P, bool TAIL>
-__global__ void __launch_bounds__(1024, P == 1 ? 8 : 4)
+__global__ void __launch_bounds__(1024, P == 1 || (P == 2 && !TAIL) ? 8 : 4)
 block_norm_kernel(BlockNormArgs a)
 {
     __shared__ double part[4][16];
