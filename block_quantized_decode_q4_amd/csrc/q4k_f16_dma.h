@@ -137,7 +137,10 @@ __device__ __forceinline__ void activate(Eight (&v)[N])
 
 // GATED: a binary16 gate and no residual (a prompt's gated block), whose loads take
 // few registers: kDepth blocks of rows on their way; else whatever the epilogue has.
-// (One kernel for each: with both in one the sums did not stay in registers.)
+// (One kernel for each: with both in one the sums did not stay in registers.)  The
+// other's rows on their way pass through scratch memory (48 or 112 bytes a lane), used
+// or not: 2048 x 14336 x 4096 takes 225 us with a binary16 gate, 265 with a residual, 301
+// with an f32 gate, 316 with a binary16 gate and a residual.
 template <typename T, int NA, bool GATED, typename YRow>
 __device__ __forceinline__ void dma_epilogue(const f32x4_t (&acc)[NA][T::FB], int xrow0, int col0,
                                          YRow yrow, const EpArgs& ep, const float* bias, int n,

@@ -29,10 +29,12 @@
 // time.  Eight tokens, 64 experts, all in one launch: 5.3 us.
 //
 // Choice by biased scores: the same split, the scores in f32 with f64 for what is near
-// (see there).  8192 tokens of 256 experts in 8 groups, topk 8: 16.8 us, bound by
-// instructions: 3000 a wave of four tokens, the vector pipe busy 66 %, two waves a SIMD;
-// with every score in
-// f64 the call took 35 us in place of 26.7.  16 tokens of 64 experts, one launch: 7.5 us.
+// (see there; a softmax also takes one f64 exp an expert).  8192 tokens of 256 experts in
+// 8 groups, topk 8, sigmoid: 16.9 us, bound by instructions: 3000 a wave of four tokens,
+// the vector pipe busy 67 %, two waves a SIMD; the call takes 25 us, with softmax 31, and
+// took 35 with every score in f64.  16 tokens of 64 experts, one launch: 7.6 us.  With 129
+// to 256 and 513 to 1024 experts that launch's 128 registers a lane do not suffice (77 and
+// 71 spilled): 24 tokens of 256 22 us, where 25 tokens in two launches take 17.
 //
 // The weighted sum reads every row of y once, four columns a thread: 201 MB
 // (4096 tokens, topk 2) in 35 us, 5.7 TB/s, bound by the bytes.
